@@ -259,7 +259,7 @@ def _coded(x):
     blocks = _rows_of(x, BLOCK)
     m, e = torch.frexp(blocks.abs().amax(2, keepdim=True))  # m in [0.5, 1): 128 m must not round past 127
     e = torch.where(m * 128 >= 127.5, e + 1, e)
-    e = torch.clamp(e - 7, min=-126)  # scale 2^e
+    e = torch.where(m == 0, -126, torch.clamp(e - 7, min=-126))  # scale 2^e
     q = torch.clamp(torch.round(torch.ldexp(blocks, -e)), -127, 127)
     return torch.ldexp(q, e).reshape(x.shape[0], -1, x.shape[2])[:, :x.shape[1]], (e + 127).squeeze(2)
 
