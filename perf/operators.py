@@ -13,8 +13,8 @@ and its gradients, with dh_t = dy_t + a_{t+1} dh_{t+1} (the final state's gradie
     a'_t = a_t ("log") or a_t (1 - a_t) ("logit").
 
 An 8-bit checkpoint holds blocks of 16 consecutive tokens of one channel as int8 codes with one
-power-of-two scale: the smallest 2^k for which round(max|block| / 2^k) <= 127.  A recurrence that
-trains on checkpoints keeps its x and its gate (limited to where the decay has not reached its
+power-of-two scale: 2^(E - 6) for a block with 2^E <= max|block| < 2^(E + 1), and codes
+round(x / scale) within +-127.  A recurrence that trains on checkpoints keeps its x and its gate (limited to where the decay has not reached its
 limit: from -16, for logits to 16) that way, and the exact fp32 state before every span of 64
 tokens; its backward pass puts the decoded values in the place of x and gate, inside each span
 from that span's exact state.
@@ -257,8 +257,7 @@ def _rows_of(x, n):
 def _coded(x):
     """(the values that the codes stand for, the biased exponents of the scales) of x [b, l, d]."""
     blocks = _rows_of(x, BLOCK)
-    m, e = torch.frexp(blocks.abs().amax(2, keepdim=True))  # m in [0.5, 1): 128 m must not round past 127
-    e = torch.where(m * 128 >= 127.5, e + 1, e)
+    m, e = torch.frexp(blocks.abs().amax(2, keepdim=True))  # largest = m 2^e, m in [0.5, 1)
     e = torch.where(m == 0, -126, torch.clamp(e - 7, min=-126))  # scale 2^e
     q = torch.clamp(torch.round(torch.ldexp(blocks, -e)), -127, 127)
     return torch.ldexp(q, e).reshape(x.shape[0], -1, x.shape[2])[:, :x.shape[1]], (e + 127).squeeze(2)
@@ -367,12 +366,12 @@ def _block_codes(v):
     top = v.abs().amax(1)
     k = torch.full_like(top, -126.0)
     some = top > 0
-    guess = torch.floor(torch.log2(torch.where(some, top, torch.ones_like(top)))) - 8
-    for _ in range(4):  # the smallest exponent whose largest code fits
-        guess = torch.where(torch.round(top * torch.exp2(-guess)) > 127, guess + 1, guess)
+    guess = torch.floor(torch.log2(torch.where(some, top, torch.ones_like(top)))) - 7
+    for _ in range(2):  # the exponent whose largest quotient lies in [64, 128)
+        guess = torch.where(top * torch.exp2(-guess) >= 128, guess + 1, guess)
     k = torch.where(some, torch.maximum(guess, k), k)
     step = torch.exp2(k)[:, None]
-    return torch.round(v / step) * step, k + 127
+    return torch.round(v / step).clamp(-127, 127) * step, k + 127
 
 
 def _exact_coded(v):
