@@ -14,10 +14,10 @@ and its gradients, with dh_t = dy_t + a_{t+1} dh_{t+1} (the final state's gradie
 
 An 8-bit checkpoint holds blocks of 16 consecutive tokens of one channel as int8 codes with one
 power-of-two scale: 2^(E - 6) for a block with 2^E <= max|block| < 2^(E + 1), and codes
-round(x / scale) within +-127.  A recurrence that trains on checkpoints keeps its x and its gate (limited to where the decay has not reached its
-limit: from -16, for logits to 16) that way, and the exact fp32 state before every span of 64
-tokens; its backward pass puts the decoded values in the place of x and gate, inside each span
-from that span's exact state.
+round(x / scale) within +-127.  A recurrence that trains on checkpoints keeps its x and its gate
+(limited to where the decay has not reached its limit: from -16, for logits to 16) that way, and
+the exact fp32 state before every span of 64 tokens; its backward pass puts the decoded values in
+the place of x and gate, inside each span from that span's exact state.
 
 ``run`` computes an operator in its plain form, or (``own``) through the package's calls.
 """
