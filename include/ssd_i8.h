@@ -295,6 +295,143 @@ SSD_API ssd_status ssd_i8_state_update_q8(int8_t *state_q, float *state_scale, c
 SSD_API ssd_status ssd_i8_chunk_cb(const int8_t *C, const int8_t *B, int batch, int seqlen, int ngroups,
                            int dstate, int chunk_size, int32_t *cb, void *stream);
 
+/*
+ * Gated linear recurrence with a decay per channel, forward and backward, and the 8-bit activation
+ * checkpoints it can train on.  Per sequence and channel:
+ *
+ *   h_t = a_t h_{t-1} + w_t x_t,   y_t = h_t
+ *   a_t = exp(gate_t)                   SSD_GATE_LOG    (gate <= 0; above it the formula is
+ *                                                        computed, without a range guarantee)
+ *   a_t = 1 / (1 + exp(-gate_t))        SSD_GATE_LOGIT
+ *   w_t = 1, or 1 - a_t                 with SSD_INPUT_COMPLEMENT OR-ed into the form
+ *
+ * This is the SSD recurrence with one state per channel in place of a [headdim, dstate] matrix per
+ * head, and with a decay that each channel reads from the input.
+ *
+ * Conventions of these entry points, beside those at the top of this file:
+ *   - x, gate, y, dy, dx and dgate have one element type, an SSD_IO_* code.  States and their
+ *     gradients are float.  All arithmetic is fp32; a 16-bit output is rounded once.
+ *   - x, gate, y, dy, dx and dgate are rows of `channels` contiguous elements, one per (batch,
+ *     token), at ptr + batch * batch_stride + token * token_stride (strides in elements, >= 0).
+ *     Input rows may overlap (stride 0).  Output rows may not: either batch_stride >=
+ *     (seqlen - 1) * token_stride + channels with token_stride >= channels, or token_stride >=
+ *     (batch - 1) * batch_stride + channels with batch_stride >= channels.  Pointers are aligned
+ *     to their element; 16-bit rows are read two channels at a time where every pointer is 4-byte
+ *     aligned and channels and strides are even.
+ *   - cu_seqlens NULL: `batch` sequences of `seqlen` tokens.  Otherwise DEVICE int32 [nseq + 1]:
+ *     batch is 1 and sequence s is tokens [cu_seqlens[s], cu_seqlens[s + 1]) of the `seqlen`
+ *     packed ones, non-decreasing offsets inside [0, seqlen].  Its contents are read on the device
+ *     only (the calls can be captured into a CUDA graph) and are not checked: wrong offsets give
+ *     wrong values, never an access outside the tensors.  Empty sequences pass their states on.
+ *     Tokens outside every sequence are without effect, whatever their rows hold, and their rows
+ *     of y, dx, dgate and of the codes are left as they were.
+ *   - Per-sequence states are float [batch, channels], or [nseq, channels] with cu_seqlens;
+ *     optional ones are NULL (zero when read, not written).
+ *   - No output may overlap an input or another output (SSD_ERR_INVALID_ARG where it does); the
+ *     `state` of the step is both.
+ *   - No workspace, no device-side waits other than hardware barriers, no atomics: results do not
+ *     change from run to run.
+ *   - Supported: channels >= 1, seqlen <= 2^31 - 65536 and batch * ceil(channels / 32) * 8 < 2^31
+ *     (else SSD_ERR_UNSUPPORTED).
+ */
+typedef enum ssd_io_dtype { SSD_IO_F32 = 0, SSD_IO_F16 = 1, SSD_IO_BF16 = 3 } ssd_io_dtype;
+typedef enum ssd_gate_form { SSD_GATE_LOG = 0, SSD_GATE_LOGIT = 1 } ssd_gate_form;
+#define SSD_INPUT_COMPLEMENT 16
+
+/* Tokens between the saved states, and tokens of one channel that share a checkpoint scale. */
+#define SSD_GATED_SPAN 64
+#define SSD_CKPT_BLOCK 16
+
+/*
+ * Forward.
+ *   init_state, final_state: per-sequence states, optional.
+ *   span_states float [batch, ceil(seqlen / 64), channels] or NULL: the state before tokens 0, 64,
+ *              128, .. of a row, which the backward calls start from (zero where a packed row's
+ *              sequence begins at that token or none holds it).
+ *   ckpt_x, ckpt_gate int8 [batch, seqlen, channels] with exponents ckpt_x_exp, ckpt_gate_exp
+ *              uint8 [batch, ceil(seqlen / 16), channels], all four or none (NULL): 8-bit
+ *              checkpoints of x and gate in the format of ssd_i8_ckpt_pack, for
+ *              ssd_i8_gated_scan_bwd_ckpt.  The gate is limited to >= -16 (SSD_GATE_LOGIT: to
+ *              [-16, 16]) first.  Tokens outside every sequence count as zero in their blocks.
+ */
+SSD_API ssd_status ssd_i8_gated_scan(const void *x, long long x_batch_stride,
+                                     long long x_token_stride, const void *gate,
+                                     long long gate_batch_stride, long long gate_token_stride,
+                                     void *y, long long y_batch_stride, long long y_token_stride,
+                                     int batch, int seqlen, int channels,
+                                     const int32_t *cu_seqlens, int nseq, int form, int io_dtype,
+                                     const float *init_state, float *final_state,
+                                     float *span_states, int8_t *ckpt_x, uint8_t *ckpt_x_exp,
+                                     int8_t *ckpt_gate, uint8_t *ckpt_gate_exp, void *stream);
+
+/*
+ * Backward.  With dh_t = dy_t + a_{t+1} dh_{t+1} (dfinal_state at a sequence's end):
+ *   dx_t = w_t dh_t
+ *   dgate_t = a'_t dh_t (h_{t-1} - [SSD_INPUT_COMPLEMENT] x_t),   a' = a, or a (1 - a) for logits
+ *   dinit_state = a_1 dh_1
+ *   x, gate, cu_seqlens, form and init_state as in the forward call (init_state is read where a
+ *   packed sequence begins), span_states as that call wrote them.
+ *   dfinal_state, dinit_state: per-sequence, optional.
+ */
+SSD_API ssd_status ssd_i8_gated_scan_bwd(const void *dy, long long dy_batch_stride,
+                                         long long dy_token_stride, const void *x,
+                                         long long x_batch_stride, long long x_token_stride,
+                                         const void *gate, long long gate_batch_stride,
+                                         long long gate_token_stride, void *dx,
+                                         long long dx_batch_stride, long long dx_token_stride,
+                                         void *dgate, long long dgate_batch_stride,
+                                         long long dgate_token_stride, int batch, int seqlen,
+                                         int channels, const int32_t *cu_seqlens, int nseq,
+                                         int form, int io_dtype, const float *init_state,
+                                         const float *span_states, const float *dfinal_state,
+                                         float *dinit_state, void *stream);
+
+/*
+ * Backward from the 8-bit checkpoints of the forward call: the formulas above with the decoded
+ * values in the place of x and gate; h_{t-1} is rebuilt inside each span of 64 tokens from that
+ * span's saved fp32 state.
+ */
+SSD_API ssd_status ssd_i8_gated_scan_bwd_ckpt(const void *dy, long long dy_batch_stride,
+                                              long long dy_token_stride, const int8_t *ckpt_x,
+                                              const uint8_t *ckpt_x_exp, const int8_t *ckpt_gate,
+                                              const uint8_t *ckpt_gate_exp, void *dx,
+                                              long long dx_batch_stride, long long dx_token_stride,
+                                              void *dgate, long long dgate_batch_stride,
+                                              long long dgate_token_stride, int batch, int seqlen,
+                                              int channels, const int32_t *cu_seqlens, int nseq,
+                                              int form, int io_dtype, const float *init_state,
+                                              const float *span_states, const float *dfinal_state,
+                                              float *dinit_state, void *stream);
+
+/*
+ * One token of the recurrence for every sequence of a decode batch, in place.
+ *   state      float [batch, channels]   read and overwritten with h_t
+ *   x, gate, y [batch, channels] of io_dtype, contiguous
+ */
+SSD_API ssd_status ssd_i8_gated_step(float *state, const void *x, const void *gate, void *y,
+                                     int batch, int channels, int form, int io_dtype,
+                                     void *stream);
+
+/*
+ * 8-bit activation checkpoint: blocks of 16 consecutive tokens of one channel as int8 codes with
+ * one power-of-two scale 2^(e - 127), value = code * 2^(e - 127).  The scale is 2^(E - 6) for a
+ * block with 2^E <= max|block| < 2^(E + 1), at least 2^-126, and code =
+ * clamp(round_half_even(x / scale), -127, 127), where x / scale is exact before that one rounding:
+ * |value - x| <= scale / 2, or below one scale where |x| > 127.5 scales.  A value of a tensor is
+ * representable in the tensor's type.  A block with an infinity or a NaN gets e = 255 and codes 0;
+ * its values are NaN.  An all-zero block gets e = 1.
+ *   x          [batch, seqlen, channels] of io_dtype, rows as above
+ *   q          int8 [batch, seqlen, channels];  e uint8 [batch, ceil(seqlen / 16), channels]
+ */
+SSD_API ssd_status ssd_i8_ckpt_pack(const void *x, long long x_batch_stride,
+                                    long long x_token_stride, int batch, int seqlen, int channels,
+                                    int io_dtype, int8_t *q, uint8_t *e, void *stream);
+
+/* The values of a checkpoint, x [batch, seqlen, channels] of io_dtype, contiguous (rounded to it;
+ * exact when the packed tensor had that type). */
+SSD_API ssd_status ssd_i8_ckpt_unpack(const int8_t *q, const uint8_t *e, int batch, int seqlen,
+                                      int channels, int io_dtype, void *x, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

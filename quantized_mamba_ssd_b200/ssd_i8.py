@@ -11,7 +11,7 @@ import contextlib
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -30,7 +30,16 @@ EXPORTED = ("ssd_i8_abi_version", "ssd_status_string", "ssd_i8_chunk_scan_worksp
             "ssd_i8_chunk_scan", "ssd_i8_state_update", "ssd_i8_chunk_cb",
             "ssd_i8_chunk_scan_noalloc", "ssd_i8_chunk_scan_status", "ssd_i8_debug_inject",
             "ssd_i8_chunk_scan_varlen_workspace_size", "ssd_i8_chunk_scan_varlen",
-            "ssd_i8_state_quantize", "ssd_i8_state_update_q8", "ssd_i8_chunk_scan_noalloc_status")
+            "ssd_i8_state_quantize", "ssd_i8_state_update_q8", "ssd_i8_chunk_scan_noalloc_status",
+            "ssd_i8_gated_scan", "ssd_i8_gated_scan_bwd", "ssd_i8_gated_scan_bwd_ckpt",
+            "ssd_i8_gated_step", "ssd_i8_ckpt_pack", "ssd_i8_ckpt_unpack")
+
+# the gated recurrence: element types, forms of the gate and of the input (include/ssd_i8.h)
+IO_DTYPES = {"f32": (0, torch.float32), "f16": (1, torch.float16), "bf16": (3, torch.bfloat16)}
+GATE_FORMS = {"log": 0, "logit": 1}
+INPUT_FORMS = {"plain": 0, "complement": 16}
+GATED_SPAN = 64  # tokens between the states that the forward saves for the backward
+CKPT_BLOCK = 16  # tokens of one channel that share a checkpoint scale
 
 # built-in scratch of ssd_i8_chunk_scan_noalloc (bytes); larger problems are refused
 NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -95,6 +104,20 @@ def library() -> ctypes.CDLL:
         lib.ssd_i8_chunk_scan_noalloc.argtypes = [vp] * 9 + [ci] * 7 + [vp, vp, vp, ci, cf, vp]
         lib.ssd_i8_chunk_scan_noalloc_status.restype = ci
         lib.ssd_i8_chunk_scan_noalloc_status.argtypes = [vp]
+        rows = [vp, ll, ll]
+        lib.ssd_i8_gated_scan.restype = ci
+        lib.ssd_i8_gated_scan.argtypes = rows * 3 + [ci] * 3 + [vp, ci, ci, ci] + [vp] * 8
+        lib.ssd_i8_gated_scan_bwd.restype = ci
+        lib.ssd_i8_gated_scan_bwd.argtypes = rows * 5 + [ci] * 3 + [vp, ci, ci, ci] + [vp] * 5
+        lib.ssd_i8_gated_scan_bwd_ckpt.restype = ci
+        lib.ssd_i8_gated_scan_bwd_ckpt.argtypes = (rows + [vp] * 4 + rows * 2 + [ci] * 3 +
+                                                   [vp, ci, ci, ci] + [vp] * 5)
+        lib.ssd_i8_gated_step.restype = ci
+        lib.ssd_i8_gated_step.argtypes = [vp] * 4 + [ci] * 4 + [vp]
+        lib.ssd_i8_ckpt_pack.restype = ci
+        lib.ssd_i8_ckpt_pack.argtypes = rows + [ci] * 4 + [vp] * 3
+        lib.ssd_i8_ckpt_unpack.restype = ci
+        lib.ssd_i8_ckpt_unpack.argtypes = [vp, vp] + [ci] * 4 + [vp, vp]
         _lib = lib
         return lib
 
@@ -481,3 +504,286 @@ def ssd_i8_chunk_scan_noalloc_status(stream=None) -> None:
     ``ssd_i8_chunk_scan_noalloc_status`` in include/ssd_i8.h."""
     _check("ssd_i8_chunk_scan_noalloc_status",
            library().ssd_i8_chunk_scan_noalloc_status(_stream(stream)))
+
+
+# ---------------------------------------------------------------------------------------
+# gated linear recurrence and 8-bit activation checkpoints
+# ---------------------------------------------------------------------------------------
+_IO_CODES = {t: code for code, t in IO_DTYPES.values()}
+
+
+class GatedCkpt(NamedTuple):
+    """8-bit checkpoints of x and gate: int8 codes of the tensors' shape and uint8 exponents with
+    ceil(l / 16) in the place of the token dim (``ssd_i8_gated_ckpt_empty`` allocates one)."""
+
+    x_q: torch.Tensor
+    x_e: torch.Tensor
+    gate_q: torch.Tensor
+    gate_e: torch.Tensor
+
+
+def _call(name: str, first: torch.Tensor, run, stream):
+    """``run(raw stream)``, a library call, with ``first``'s GPU as the current device.  Outputs
+    that ``run`` allocates belong to the stream the kernels run on."""
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("the library's tensors must be CUDA tensors")
+    dev = first.get_device()
+    if stream is None:
+        if torch.cuda.current_device() == dev:
+            return run(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(dev):
+            return run(torch.cuda.current_stream().cuda_stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device.index != dev:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return run(stream.cuda_stream)
+
+
+def _flat(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
+          dev: int) -> Optional[int]:
+    """Pointer of a contiguous tensor on GPU ``dev`` (None passes)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> tuple:
+    """Pointer, batch stride and token stride of [b, l, d] or [T, d] rows on GPU ``dev`` whose
+    channels are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1 and t.numel():
+        raise ValueError(f"{name}: the channels (last dim) must be contiguous")
+    return t.data_ptr(), (st[0] if len(st) == 3 else 0), st[-2]
+
+
+def _gated_shape(t: torch.Tensor, name: str, cu_seqlens) -> tuple:
+    """(batch, tokens, channels, sequences, pointer of cu_seqlens, their count or 0, GPU) of a
+    call on [b, l, d] rows, or on packed [T, d] rows with ``cu_seqlens``."""
+    dev = t.get_device()
+    if cu_seqlens is None:
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [b,l,d], or [T,d] with cu_seqlens")
+        b, l, d = t.shape
+        return b, l, d, b, None, 0, dev
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [T,d] with cu_seqlens")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be an int32 CUDA tensor of nseq + 1 token offsets")
+    l, d = t.shape
+    nseq = cu_seqlens.numel() - 1
+    return 1, l, d, nseq, _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev), nseq, dev
+
+
+def _io_code(t: torch.Tensor, name: str) -> int:
+    code = _IO_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _form(gate_form: str, input_form: str) -> int:
+    if gate_form not in GATE_FORMS or input_form not in INPUT_FORMS:
+        raise ValueError(f"gate_form is one of {tuple(GATE_FORMS)}, input_form one of "
+                         f"{tuple(INPUT_FORMS)}; got {gate_form!r}, {input_form!r}")
+    return GATE_FORMS[gate_form] | INPUT_FORMS[input_form]
+
+
+def _per(n: int, shape: tuple) -> tuple:
+    """``shape`` [.., l, d] with ceil(l / n) in the place of l."""
+    return (*shape[:-2], -(-shape[-2] // n), shape[-1])
+
+
+def _ckpt_ptrs(ckpt, shape: tuple, dev: int) -> tuple:
+    if len(ckpt) != 4:
+        raise ValueError("ckpt must hold x_q, x_e, gate_q and gate_e")
+    e = _per(CKPT_BLOCK, shape)
+    return (_flat(ckpt[0], "ckpt.x_q", torch.int8, shape, dev),
+            _flat(ckpt[1], "ckpt.x_e", torch.uint8, e, dev),
+            _flat(ckpt[2], "ckpt.gate_q", torch.int8, shape, dev),
+            _flat(ckpt[3], "ckpt.gate_e", torch.uint8, e, dev))
+
+
+def ssd_i8_gated_ckpt_empty(x: torch.Tensor) -> GatedCkpt:
+    """Uninitialised 8-bit checkpoints for a gated scan of ``x`` ([b,l,d] or [T,d])."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [b,l,d] or [T,d]")
+    e = _per(CKPT_BLOCK, x.shape)
+    def codes(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    return GatedCkpt(codes(x.shape, torch.int8), codes(e, torch.uint8),
+                     codes(x.shape, torch.int8), codes(e, torch.uint8))
+
+
+def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
+                      cu_seqlens: Optional[torch.Tensor] = None, *, gate_form: str = "log",
+                      input_form: str = "plain", init_state: Optional[torch.Tensor] = None,
+                      final_state: Optional[torch.Tensor] = None,
+                      y: Optional[torch.Tensor] = None,
+                      span_states: Optional[torch.Tensor] = None,
+                      ckpt: Optional[GatedCkpt] = None, stream=None) -> torch.Tensor:
+    """Gated linear recurrence h_t = a_t h_{t-1} + w_t x_t per channel, y_t = h_t (see
+    ``ssd_i8_gated_scan`` in include/ssd_i8.h).
+
+    x, gate [b,l,d], or packed [T,d] with ``cu_seqlens`` (int32 CUDA tensor of nseq + 1 token
+    offsets), float32, float16 or bfloat16, channels contiguous and any batch and token stride.
+    ``gate_form``: "log" (a = exp(gate)) or "logit" (a = sigmoid(gate)); ``input_form``: "plain"
+    (w = 1) or "complement" (w = 1 - a).  init_state / final_state f32 [b,d] ([nseq,d] packed).
+    For a backward pass: ``span_states`` f32 [b,ceil(l/64),d] ([ceil(T/64),d]) is written, and
+    ``ckpt`` (``ssd_i8_gated_ckpt_empty``) receives x and gate in 8 bits.  Returns y, of x's shape
+    and dtype; rows outside every packed sequence are left as they were."""
+    def run(raw):
+        b, l, d, seqs, cu, nseq, dev = _gated_shape(x, "x", cu_seqlens)
+        dt, shape = x.dtype, x.shape
+        code = _io_code(x, "x")
+        out = torch.empty(shape, dtype=dt, device=x.device) if y is None else y
+        q = (None,) * 4 if ckpt is None else _ckpt_ptrs(ckpt, shape, dev)
+        _check("ssd_i8_gated_scan", library().ssd_i8_gated_scan(
+            *_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev),
+            *_rows(out, "y", dt, shape, dev), b, l, d, cu, nseq, _form(gate_form, input_form),
+            code, _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
+            _flat(final_state, "final_state", torch.float32, (seqs, d), dev),
+            _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
+            *q, raw))
+        return out
+    return _call("ssd_i8_gated_scan", x, run, stream)
+
+
+def _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form, init_state,
+               dfinal_state, dinit_state, dx, dgate, stream):
+    def run(raw):
+        b, l, d, seqs, cu, nseq, dev = _gated_shape(dy, "dy", cu_seqlens)
+        dt, shape = dy.dtype, dy.shape
+        code = _io_code(dy, "dy")
+        if span_states is None:
+            raise TypeError("span_states must be the tensor that the forward call wrote")
+        o = [torch.empty(shape, dtype=dt, device=dy.device) if t is None else t
+             for t in (dx, dgate)]
+        _check(name, getattr(library(), name)(
+            *_rows(dy, "dy", dt, shape, dev), *inputs(dt, shape, dev),
+            *_rows(o[0], "dx", dt, shape, dev), *_rows(o[1], "dgate", dt, shape, dev),
+            b, l, d, cu, nseq, _form(gate_form, input_form), code,
+            _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
+            _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
+            _flat(dfinal_state, "dfinal_state", torch.float32, (seqs, d), dev),
+            _flat(dinit_state, "dinit_state", torch.float32, (seqs, d), dev), raw))
+        return o[0], o[1]
+    return _call(name, dy, run, stream)
+
+
+def ssd_i8_gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor,
+                          span_states: torch.Tensor,
+                          cu_seqlens: Optional[torch.Tensor] = None, *, gate_form: str = "log",
+                          input_form: str = "plain", init_state: Optional[torch.Tensor] = None,
+                          dfinal_state: Optional[torch.Tensor] = None,
+                          dinit_state: Optional[torch.Tensor] = None,
+                          dx: Optional[torch.Tensor] = None,
+                          dgate: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """Gradients (dx, dgate) of ``ssd_i8_gated_scan`` for the gradient ``dy`` of its output.
+
+    x, gate, cu_seqlens, the forms and init_state as in the forward call, span_states as it wrote
+    them; dfinal_state f32 [b,d] ([nseq,d]) is the gradient of the final states, dinit_state
+    receives that of the initial ones.  dy, x, gate, dx and dgate share shape and dtype; dx and
+    dgate may be column slices of one wider buffer."""
+    def inputs(dt, shape, dev):
+        return (*_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev))
+    return _gated_bwd("ssd_i8_gated_scan_bwd", dy, inputs, span_states, cu_seqlens, gate_form,
+                      input_form, init_state, dfinal_state, dinit_state, dx, dgate, stream)
+
+
+def ssd_i8_gated_scan_bwd_ckpt(dy: torch.Tensor, ckpt: GatedCkpt, span_states: torch.Tensor,
+                               cu_seqlens: Optional[torch.Tensor] = None, *,
+                               gate_form: str = "log", input_form: str = "plain",
+                               init_state: Optional[torch.Tensor] = None,
+                               dfinal_state: Optional[torch.Tensor] = None,
+                               dinit_state: Optional[torch.Tensor] = None,
+                               dx: Optional[torch.Tensor] = None,
+                               dgate: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """``ssd_i8_gated_scan_bwd`` from the 8-bit checkpoints that the forward call wrote, in the
+    place of x and gate."""
+    def inputs(dt, shape, dev):
+        return _ckpt_ptrs(ckpt, shape, dev)
+    return _gated_bwd("ssd_i8_gated_scan_bwd_ckpt", dy, inputs, span_states, cu_seqlens,
+                      gate_form, input_form, init_state, dfinal_state, dinit_state, dx, dgate,
+                      stream)
+
+
+def ssd_i8_gated_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, *,
+                      gate_form: str = "log", input_form: str = "plain",
+                      y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of ``ssd_i8_gated_scan`` for a decode batch: state f32 [b,d] updated in place;
+    x, gate [b,d], contiguous.  Returns y [b,d] of x's dtype."""
+    def run(raw):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("x must be a torch.Tensor")
+        dev, dt, shape = state.get_device(), x.dtype, state.shape
+        if len(shape) != 2:
+            raise ValueError("state must be [b,d]")
+        code = _io_code(x, "x")
+        out = torch.empty(shape, dtype=dt, device=state.device) if y is None else y
+        _check("ssd_i8_gated_step", library().ssd_i8_gated_step(
+            _flat(state, "state", torch.float32, shape, dev), _flat(x, "x", dt, shape, dev),
+            _flat(gate, "gate", dt, shape, dev), _flat(out, "y", dt, shape, dev), shape[0],
+            shape[1], _form(gate_form, input_form), code, raw))
+        return out
+    return _call("ssd_i8_gated_step", state, run, stream)
+
+
+def ssd_i8_ckpt_pack(x: torch.Tensor, *, q: Optional[torch.Tensor] = None,
+                     e: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """8-bit checkpoint of x [b,l,d] or [T,d] (float32, float16 or bfloat16, channels contiguous):
+    (int8 codes of x's shape, uint8 exponents [b,ceil(l/16),d] or [ceil(T/16),d]); a value is
+    code * 2^(exponent - 127) (see ``ssd_i8_ckpt_pack`` in include/ssd_i8.h)."""
+    def run(raw):
+        if x.dim() not in (2, 3):
+            raise ValueError("x must be [b,l,d] or [T,d]")
+        dev, shape = x.get_device(), x.shape
+        se = _per(CKPT_BLOCK, shape)
+        code = _io_code(x, "x")
+        qo = torch.empty(shape, dtype=torch.int8, device=x.device) if q is None else q
+        eo = torch.empty(se, dtype=torch.uint8, device=x.device) if e is None else e
+        _check("ssd_i8_ckpt_pack", library().ssd_i8_ckpt_pack(
+            *_rows(x, "x", x.dtype, shape, dev), shape[0] if len(shape) == 3 else 1, shape[-2],
+            shape[-1], code, _flat(qo, "q", torch.int8, shape, dev),
+            _flat(eo, "e", torch.uint8, se, dev), raw))
+        return qo, eo
+    return _call("ssd_i8_ckpt_pack", x, run, stream)
+
+
+def ssd_i8_ckpt_unpack(q: torch.Tensor, e: torch.Tensor, *, dtype: str = "bf16",
+                       x: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of an 8-bit checkpoint as ``dtype`` ("f32", "f16" or "bf16"), of q's shape."""
+    def run(raw):
+        if q.dim() not in (2, 3):
+            raise ValueError("q must be [b,l,d] or [T,d]")
+        if dtype not in IO_DTYPES:
+            raise ValueError(f"dtype is one of {tuple(IO_DTYPES)}, got {dtype!r}")
+        code, dt = IO_DTYPES[dtype]
+        dev, shape = q.get_device(), q.shape
+        out = torch.empty(shape, dtype=dt, device=q.device) if x is None else x
+        _check("ssd_i8_ckpt_unpack", library().ssd_i8_ckpt_unpack(
+            _flat(q, "q", torch.int8, shape, dev),
+            _flat(e, "e", torch.uint8, _per(CKPT_BLOCK, shape), dev),
+            shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], code,
+            _flat(out, "x", dt, shape, dev), raw))
+        return out
+    return _call("ssd_i8_ckpt_unpack", q, run, stream)
