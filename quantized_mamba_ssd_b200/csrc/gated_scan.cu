@@ -1,7 +1,6 @@
 // Gated linear recurrence over sequences, forward and backward: one thread per channel walks the
 // tokens.
-#include "gated.cuh"
-#include "gated_kernels.h"
+#include "gated_launch.cuh"
 
 namespace ssd {
 
@@ -20,63 +19,6 @@ template <typename T>
 __device__ __forceinline__ void store(const GatedRows& r, int b, int t, int c, float v) {
     T* p = static_cast<T*>(const_cast<void*>(r.ptr));
     p[b * r.batch_stride + t * r.token_stride + c] = from_f32<T>(v);
-}
-
-template <typename T, bool LOGIT>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const GatedArgs a) {
-    const int c = blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y;
-    if (c >= a.channels) return;
-    const int d = a.channels, spans = (a.seqlen + kSpan - 1) / kSpan;
-    const int blocks = (a.seqlen + kBlock - 1) / kBlock;
-    float h = 0.f;
-    if (!a.cu && a.init_state) h = a.init_state[(size_t)b * d + c];
-    if (a.cu && a.final_state)
-        for (int s = 0; s < a.nseq; ++s)
-            if (a.cu[s + 1] <= a.cu[s])
-                a.final_state[(size_t)s * d + c] = a.init_state ? a.init_state[(size_t)s * d + c] : 0.f;
-    for (int t = 0; t < a.seqlen; ++t) {
-        if (a.x_q && t % kBlock == 0) {  // the block that starts here
-            uint32_t top[2] = {0, 0};
-            for (int i = t; i < t + kBlock && i < a.seqlen; ++i) {
-                if (a.cu && sequence_of(a.cu, a.nseq, i) < 0) continue;
-                const uint32_t xa = __float_as_uint(fabsf(load<T>(a.x, b, i, c)));
-                const uint32_t ga = __float_as_uint(fabsf(held_gate<LOGIT>(load<T>(a.gate, b, i, c))));
-                top[0] = top[0] < xa ? xa : top[0];
-                top[1] = top[1] < ga ? ga : top[1];
-            }
-            const uint32_t ex = scale_exp(top[0]), eg = scale_exp(top[1]);
-            const float ix = inv_scale_of(ex), ig = inv_scale_of(eg);
-            for (int i = t; i < t + kBlock && i < a.seqlen; ++i) {
-                if (a.cu && sequence_of(a.cu, a.nseq, i) < 0) continue;
-                const size_t at = ((size_t)b * a.seqlen + i) * d + c;
-                a.x_q[at] = static_cast<int8_t>(code_of(load<T>(a.x, b, i, c), ix));
-                a.gate_q[at] = static_cast<int8_t>(code_of(held_gate<LOGIT>(load<T>(a.gate, b, i, c)), ig));
-            }
-            const size_t at = ((size_t)b * blocks + t / kBlock) * d + c;
-            a.x_e[at] = static_cast<uint8_t>(ex);
-            a.gate_e[at] = static_cast<uint8_t>(eg);
-        }
-        int s = b;
-        if (a.cu) {
-            s = sequence_of(a.cu, a.nseq, t);
-            if (s < 0 || a.cu[s] == t) {
-                if (a.span_states && t % kSpan == 0)
-                    a.span_states[((size_t)b * spans + t / kSpan) * d + c] = 0.f;
-                h = s >= 0 && a.init_state ? a.init_state[(size_t)s * d + c] : 0.f;
-                if (s < 0) continue;
-            } else if (a.span_states && t % kSpan == 0) {
-                a.span_states[((size_t)b * spans + t / kSpan) * d + c] = h;
-            }
-        } else if (a.span_states && t % kSpan == 0) {
-            a.span_states[((size_t)b * spans + t / kSpan) * d + c] = h;
-        }
-        const Decay k = decay_of<T, LOGIT>(load<T>(a.gate, b, t, c));
-        const float x = load<T>(a.x, b, t, c);
-        h = step<kTwo<T>>(k, h, a.complement ? k.u * x : x);
-        store<T>(a.y, b, t, c, h);
-        if (a.final_state && t + 1 == (a.cu ? a.cu[s + 1] : a.seqlen))
-            a.final_state[(size_t)s * d + c] = h;
-    }
 }
 
 template <typename T, bool LOGIT>
@@ -160,12 +102,7 @@ cudaError_t by_type(int io_dtype, F f) {
 }  // namespace
 
 cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t st) {
-    return by_type(a.io_dtype, [&](auto zero) {
-        using T = decltype(zero);
-        const dim3 grid((a.channels + kThreads - 1) / kThreads, a.batch);
-        (a.logit ? scan_kernel<T, true> : scan_kernel<T, false>)<<<grid, kThreads, 0, st>>>(a);
-        return cudaGetLastError();
-    });
+    return by_type(a.io_dtype, [&](auto zero) { return launch_gated_scan_as<decltype(zero)>(a, st); });
 }
 
 cudaError_t launch_gated_scan_bwd(const GatedArgs& a, cudaStream_t st) {
