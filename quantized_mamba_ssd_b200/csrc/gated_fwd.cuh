@@ -11,257 +11,227 @@
 namespace ssd {
 namespace gated {
 
-template <typename T, int V, bool LOGIT, bool COMP, bool PACKED>
+// Shared memory of the staged inputs: [stage][x, gate][warp][16 tokens][128 bytes].
+constexpr int kFwdStage = 2 * kTile * kRowBytes;
+constexpr int kFwdSmem = kFwdStages * kFwdStage;
+
+template <typename T, bool LOGIT, bool COMP, bool PACKED>
 __global__ void __launch_bounds__(kTileThreads, kFwdBlocks)
-scan_kernel(const __grid_constant__ GatedArgs a, const int R) {
+scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
+    constexpr int V = kChannels<T>;
     constexpr bool TWO = kTwo<T>;
-    using P = Pack<T, V>;
-    using Raw = typename P::Raw;
+    using P = Pack<T>;
     using Slots = MapSlots<V, TWO>;
+    extern __shared__ __align__(128) uint8_t staged[];
     __shared__ float seg_maps[2][kWarps * Slots::kFloats];
     __shared__ float cta_maps[2][kMaxCluster * Slots::kFloats];
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = ta.cluster;
     const int rank = blockIdx.x % R, unit = blockIdx.x / R;
-    const int d = a.channels, strips = (d + 32 * V - 1) / (32 * V);
-    const int b = unit / strips, c = (unit % strips) * 32 * V + lane * V;
-    const bool active = c < d;
+    const int d = a.channels, b = unit / ta.strips, c0 = unit % ta.strips * 32 * V;
+    const int c = c0 + lane * V, count = max(0, min(V, d - c));
     const int tiles = (a.seqlen + kTile - 1) / kTile, steps = (tiles + R - 1) / R;
+    const size_t row0 = (size_t)b * a.seqlen;
+    const float gate_one = LOGIT ? INFINITY : 0.f;  // the gate of a decay of 1
 
-    const Raw* px = reinterpret_cast<const Raw*>(static_cast<const T*>(a.x.ptr) + b * a.x.batch_stride + c);
-    const Raw* pg = reinterpret_cast<const Raw*>(static_cast<const T*>(a.gate.ptr) + b * a.gate.batch_stride + c);
-    Raw* py = reinterpret_cast<Raw*>(static_cast<T*>(const_cast<void*>(a.y.ptr)) + b * a.y.batch_stride + c);
-    const long long sx = a.x.token_stride / V, sg = a.gate.token_stride / V, sy = a.y.token_stride / V;
-    const Raw gate_one = LOGIT ? P::kInf : Raw(0);  // the gate of a decay of 1
+    const char* px = static_cast<const char*>(a.x.ptr) + (b * a.x.batch_stride + c0) * sizeof(T);
+    const char* pg = static_cast<const char*>(a.gate.ptr) + (b * a.gate.batch_stride + c0) * sizeof(T);
+    const long long sx = a.x.token_stride * sizeof(T), sg = a.gate.token_stride * sizeof(T);
+    const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
+    T* py = static_cast<T*>(const_cast<void*>(a.y.ptr)) + b * a.y.batch_stride + c;
 
-    // x and gate of the segment that this warp takes in step k; tokens behind the end keep the
-    // state (x 0, decay 1)
-    Raw rx[kSeg], rg[kSeg];
-    auto load = [&](int k) {
-        const int t0 = (k * R + rank) * kTile + warp * kSeg;
-        const Raw* qx = px + t0 * sx;
-        const Raw* qg = pg + t0 * sg;
-#pragma unroll
-        for (int j = 0; j < kSeg; ++j) {
-            const bool in = active && t0 + j < a.seqlen;
-            rx[j] = in ? load_once(qx + j * sx) : Raw(0);
-            rg[j] = in ? load_once(qg + j * sg) : gate_one;
+    auto slot = [&](int k, int tensor) {
+        return staged + (k % kFwdStages) * kFwdStage + (tensor * kWarps + warp) * kSeg * kRowBytes;
+    };
+    auto stage = [&](int k) {  // this warp's segment of step k
+        if (k < steps) {
+            const int t0 = (k * R + rank) * kTile + warp * kSeg;
+            const int n = max(0, min(kSeg, a.seqlen - t0));
+            stage_rows<kRowBytes>(slot(k, 0), n ? px + t0 * sx : px, sx, n, width, ta.align_x);
+            stage_rows<kRowBytes>(slot(k, 1), n ? pg + t0 * sg : pg, sg, n, width, ta.align_gate);
         }
+        copy_commit();
     };
 
     float carry[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        carry[v] = !PACKED && active && a.init_state ? a.init_state[(size_t)b * d + c + v] : 0.f;
-    if (PACKED && a.final_state && rank == 0 && active) {  // sequences without a token
-        for (int s = warp; s < a.nseq; s += kWarps)
-            if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
-                for (int v = 0; v < V; ++v)
-                    a.final_state[(size_t)s * d + c + v] =
-                        a.init_state ? a.init_state[(size_t)s * d + c + v] : 0.f;
+    load_floats<V>(!PACKED && a.init_state ? a.init_state + (size_t)b * d + c : nullptr, carry, count);
+    if (PACKED && a.final_state && rank == 0) {  // sequences without a token
+        for (int s = warp; s < a.nseq; s += kWarps) {
+            if (__ldg(a.cu + s + 1) > __ldg(a.cu + s)) continue;
+            float h[V];
+            load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, h, count);
+            store_floats<V>(a.final_state + (size_t)s * d + c, h, count);
+        }
     }
     Held held;
-    load(0);
+#pragma unroll
+    for (int k = 0; k < kFwdStages - 1; ++k) stage(k);
     for (int k = 0; k < steps; ++k) {
         const int tile = k * R + rank, t0 = tile * kTile + warp * kSeg;
         const int n = max(0, min(kSeg, a.seqlen - t0));
         Marks m;
         m.valid = (1u << n) - 1;
         m.begin = m.end = 0;
-        if constexpr (PACKED) {
-            m = marks_of(a.cu, a.nseq, t0, n, held);
-            if (m.valid != (1u << kSeg) - 1) {
+        if constexpr (PACKED) m = marks_of(a.cu, a.nseq, t0, n, held);
+        copy_wait<kFwdStages - 2>();
+        __syncwarp();  // the segment is here, and every lane is done with the slot filled next
+        stage(k + kFwdStages - 1);
+        const uint32_t* rx = reinterpret_cast<const uint32_t*>(slot(k, 0)) + lane;
+        const uint32_t* rg = reinterpret_cast<const uint32_t*>(slot(k, 1)) + lane;
+        auto get_x = [&](int j, float (&x)[V]) {
+            P::get(rx[j * 32], x);
+            if (!(m.valid >> j & 1))
 #pragma unroll
-                for (int j = 0; j < kSeg; ++j)
-                    if (!(m.valid >> j & 1)) {
-                        rx[j] = 0;
-                        rg[j] = gate_one;
-                    }
-            }
-        }
+                for (int v = 0; v < V; ++v) x[v] = 0.f;
+        };
+        auto get_gate = [&](int j, float (&g)[V], float none) {
+            P::get(rg[j * 32], g);
+            if (!(m.valid >> j & 1))
+#pragma unroll
+                for (int v = 0; v < V; ++v) g[v] = none;
+        };
 
-        if (a.x_q && n > 0 && active) {  // the segment is one checkpoint block per channel
-            float top_x[V], top_g[V];
+        if (a.x_q && n > 0) {  // the segment is one checkpoint block per channel
+            uint32_t top_x[V], top_g[V];  // bits of the magnitudes: their order, NaN on top
 #pragma unroll
-            for (int v = 0; v < V; ++v) top_x[v] = top_g[v] = 0.f;
-            bool nan_x[V] = {}, nan_g[V] = {};
+            for (int v = 0; v < V; ++v) top_x[v] = top_g[v] = 0;
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
                 float x[V], g[V];
-                P::get(rx[j], x);
-                P::get(rg[j], g);
+                get_x(j, x);
+                get_gate(j, g, 0.f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    // fmaxf drops a NaN: kept aside
-                    top_x[v] = fmaxf(top_x[v], fabsf(x[v]));
-                    nan_x[v] |= x[v] != x[v];
-                    const float hg = m.valid >> j & 1 ? held_gate<LOGIT>(g[v]) : 0.f;
-                    top_g[v] = fmaxf(top_g[v], fabsf(hg));
-                    nan_g[v] |= hg != hg;
+                    top_x[v] = max(top_x[v], __float_as_uint(fabsf(x[v])));
+                    top_g[v] = max(top_g[v], __float_as_uint(fabsf(held_gate<LOGIT>(g[v]))));
                 }
             }
             float inv_x[V], inv_g[V];
             int ex[V], eg[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                ex[v] = scale_exp(nan_x[v] ? 0x7fc00000u : __float_as_uint(top_x[v]));
-                eg[v] = scale_exp(nan_g[v] ? 0x7fc00000u : __float_as_uint(top_g[v]));
+                ex[v] = scale_exp(top_x[v]);
+                eg[v] = scale_exp(top_g[v]);
                 inv_x[v] = inv_scale_of(ex[v]);
                 inv_g[v] = inv_scale_of(eg[v]);
             }
-            using Codes = typename CodeRaw<V>::Raw;
-            const size_t at = ((size_t)b * a.seqlen + t0) * d + c;
+            const size_t at = (row0 + t0) * d + c;
+            uint8_t* qx = reinterpret_cast<uint8_t*>(a.x_q) + at;
+            uint8_t* qg = reinterpret_cast<uint8_t*>(a.gate_q) + at;
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
                 if (!(m.valid >> j & 1)) continue;
                 float x[V], g[V];
-                int qx[V], qg[V];
-                P::get(rx[j], x);
-                P::get(rg[j], g);
+                int code[V];
+                get_x(j, x);
+                get_gate(j, g, 0.f);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    qx[v] = code_of(x[v], inv_x[v]);
-                    qg[v] = code_of(held_gate<LOGIT>(g[v]), inv_g[v]);
-                }
-                *reinterpret_cast<Codes*>(a.x_q + at + (size_t)j * d) = put_codes<V>(qx);
-                *reinterpret_cast<Codes*>(a.gate_q + at + (size_t)j * d) = put_codes<V>(qg);
+                for (int v = 0; v < V; ++v) code[v] = code_of(x[v], inv_x[v]);
+                store_bytes<V>(qx + (size_t)j * d, code, ta.pair_codes, count);
+#pragma unroll
+                for (int v = 0; v < V; ++v) code[v] = code_of(held_gate<LOGIT>(g[v]), inv_g[v]);
+                store_bytes<V>(qg + (size_t)j * d, code, ta.pair_codes, count);
             }
-            const int blocks = (a.seqlen + kBlock - 1) / kBlock;
-            const size_t be = ((size_t)b * blocks + t0 / kBlock) * d + c;
-            *reinterpret_cast<Codes*>(a.x_e + be) = put_codes<V>(ex);
-            *reinterpret_cast<Codes*>(a.gate_e + be) = put_codes<V>(eg);
+            const size_t be = ((size_t)b * ta.blocks + t0 / kBlock) * d + c;
+            store_bytes<V>(a.x_e + be, ex, ta.pair_codes, count);
+            store_bytes<V>(a.gate_e + be, eg, ta.pair_codes, count);
         }
 
-        // decays and inputs of the segment, and its map
-        float da[kSeg][V], lo[TWO ? kSeg : 1][V], in[kSeg][V], init[V];
+        // decays (and weighted inputs) of the segment, and its map
+        float da[kSeg][V], lo[TWO ? kSeg : 1][V], wx[COMP ? kSeg : 1][V];
         Map<TWO> seg[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) seg[v] = identity_map<TWO>();
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
             float x[V], g[V];
-            P::get(rx[j], x);
-            P::get(rg[j], g);
-            const bool begins = PACKED && (m.begin >> j & 1);
-            if (begins) {
+            get_x(j, x);
+            get_gate(j, g, gate_one);
+            if (PACKED && (m.begin >> j & 1)) {
                 const int s = __shfl_sync(0xffffffffu, m.seq, j);
+                float h[V];
+                load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, h, count);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    init[v] = active && a.init_state ? a.init_state[(size_t)s * d + c + v] : 0.f;
+                for (int v = 0; v < V; ++v) seg[v].B = h[v];
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const Decay k = decay_of<T, LOGIT>(g[v]);
-                da[j][v] = k.a;
-                if constexpr (TWO) lo[j][v] = k.lo;
-                in[j][v] = COMP ? k.u * x[v] : x[v];
-                seg[v].B = step<TWO>(k, begins ? init[v] : seg[v].B, in[j][v]);
-                extend<TWO>(seg[v], k);
+                const Decay r = decay_of<T, LOGIT>(g[v]);
+                da[j][v] = r.a;
+                if constexpr (TWO) lo[j][v] = r.lo;
+                if constexpr (COMP) wx[j][v] = r.u * x[v];
+                seg[v].B = step<TWO>(r, seg[v].B, COMP ? wx[COMP ? j : 0][v] : x[v]);
+                extend<TWO>(seg[v], r);
             }
         }
         if (PACKED && m.begin) {
 #pragma unroll
             for (int v = 0; v < V; ++v) seg[v].A = -1.f;
         }
-        if (k + 1 < steps) load(k + 1);
 
         // the carry into this segment, and into the next step
         float* segs = seg_maps[k & 1];
-        float* ctas = cta_maps[k & 1];
+        float h[V];
         Slots::write(segs, warp, lane, seg);
         __syncthreads();
-        float h[V];
-        Map<TWO> q[V];
         if (R > 1) {
+            float* ctas = cta_maps[k & 1];
             if (warp == kWarps - 1) {
                 Map<TWO> all[V];
-                Slots::read(segs, 0, lane, all);
-                for (int i = 1; i < kWarps; ++i) {
-                    Slots::read(segs, i, lane, q);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) all[v] = join<TWO, PACKED>(all[v], q[v]);
-                }
+                Slots::template join_runs<PACKED>(segs, lane, all);
                 for (int r = 0; r < R; ++r) Slots::send(ctas, rank, lane, r, all);
             }
             cluster_barrier();
-            for (int r = 0; r < R; ++r) {
-                Slots::read(ctas, r, lane, q);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (r == rank) h[v] = carry[v];
-                    carry[v] = through<TWO, PACKED>(q[v], carry[v]);
-                }
-            }
-            for (int i = 0; i < warp; ++i) {
-                Slots::read(segs, i, lane, q);
-#pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = through<TWO, PACKED>(q[v], h[v]);
-            }
+            Slots::template carry_through<PACKED>(ctas, R, rank, lane, carry, h);
+            Slots::template carry_into<PACKED>(segs, warp, lane, h);
         } else {
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                Slots::read(segs, i, lane, q);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (i == warp) h[v] = carry[v];
-                    carry[v] = through<TWO, PACKED>(q[v], carry[v]);
-                }
-            }
+            Slots::template carry_through<PACKED>(segs, kWarps, warp, lane, carry, h);
         }
 
-        if (a.span_states && warp == 0 && n > 0 && active) {
-            const size_t at = ((size_t)b * tiles + tile) * d + c;
+        if (a.span_states && warp == 0 && n > 0) {
+            float s[V];
             const bool none = PACKED && (!(m.valid & 1) || (m.begin & 1));
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.span_states[at + v] = none ? 0.f : h[v];
+            for (int v = 0; v < V; ++v) s[v] = none ? 0.f : h[v];
+            store_floats<V>(a.span_states + ((size_t)b * tiles + tile) * d + c, s, count);
         }
-        Raw* qy = py + t0 * sy;
+        T* qy = py + t0 * a.y.token_stride;
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
+            float x[V];
+            if constexpr (!COMP) get_x(j, x);
             if (PACKED && (m.begin >> j & 1)) {
                 const int s = __shfl_sync(0xffffffffu, m.seq, j);
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    h[v] = active && a.init_state ? a.init_state[(size_t)s * d + c + v] : 0.f;
+                load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, h, count);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float low = TWO ? fmaf(lo[TWO ? j : 0][v], h[v], in[j][v]) : in[j][v];
-                h[v] = fmaf(da[j][v], h[v], low);
+                const float in = COMP ? wx[COMP ? j : 0][v] : x[v];
+                h[v] = fmaf(da[j][v], h[v], TWO ? fmaf(lo[TWO ? j : 0][v], h[v], in) : in);
             }
-            if ((m.valid >> j & 1) && active) qy[j * sy] = P::put(h);
+            if (m.valid >> j & 1) store_row<T>(qy + j * a.y.token_stride, h, ta.pair_out, count);
             if (PACKED && (m.end >> j & 1)) {
                 const int s = __shfl_sync(0xffffffffu, m.seq, j);
-                if (a.final_state && active)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) a.final_state[(size_t)s * d + c + v] = h[v];
+                if (a.final_state) store_floats<V>(a.final_state + (size_t)s * d + c, h, count);
             }
         }
     }
     // the carry behind the last tile is the final state, in every thread of the cluster
-    if (!PACKED && a.final_state && rank == 0 && warp == 0 && active)
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.final_state[(size_t)b * d + c + v] = carry[v];
+    if (!PACKED && a.final_state && rank == 0 && warp == 0)
+        store_floats<V>(a.final_state + (size_t)b * d + c, carry, count);
 }
 
-template <typename T, int V>
-cudaError_t dispatch_fwd_as(const GatedArgs& a, cudaStream_t st) {
+template <typename T>
+cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
     auto go = [&](auto logit, auto comp) {
         constexpr bool L = decltype(logit)::value, C = decltype(comp)::value;
-        return a.cu ? launch_tiles(scan_kernel<T, V, L, C, true>, a, V, kFwdBlocks, st)
-                    : launch_tiles(scan_kernel<T, V, L, C, false>, a, V, kFwdBlocks, st);
+        return a.cu ? launch_tiles<T>(scan_kernel<T, L, C, true>, a, kFwdBlocks, kFwdSmem, st)
+                    : launch_tiles<T>(scan_kernel<T, L, C, false>, a, kFwdBlocks, kFwdSmem, st);
     };
     using Y = std::true_type;
     using N = std::false_type;
     if (a.logit) return a.complement ? go(Y{}, Y{}) : go(Y{}, N{});
     return a.complement ? go(N{}, Y{}) : go(N{}, N{});
-}
-
-template <typename T>
-cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
-    if constexpr (sizeof(T) == 2)
-        if (two_channels(a)) return dispatch_fwd_as<T, 2>(a, st);
-    return dispatch_fwd_as<T, 1>(a, st);
 }
 
 }  // namespace gated

@@ -19,81 +19,139 @@ constexpr int kWarps = 4;
 constexpr int kSeg = kBlock;               // tokens per warp: a checkpoint block stays in a thread
 constexpr int kTile = kWarps * kSeg;       // tokens per CTA and step
 constexpr int kTileThreads = 32 * kWarps;
+constexpr int kRowBytes = 128;             // a token's channels of one warp
 constexpr int kMaxCluster = 8;
 static_assert(kTile == kSpan, "the backward starts every tile from a saved state");
 
 // ---------------------------------------------------------------------------------------
-// V channels of one token
+// the channels of one token and lane: one 32-bit word, so that a warp's row is 128 bytes
 // ---------------------------------------------------------------------------------------
-template <typename T, int V> struct Pack;
-template <> struct Pack<float, 1> {
-    using Raw = uint32_t;
-    static constexpr Raw kInf = 0x7f800000u;
-    static __device__ __forceinline__ void get(Raw r, float (&f)[1]) { f[0] = __uint_as_float(r); }
-    static __device__ __forceinline__ Raw put(const float (&f)[1]) { return __float_as_uint(f[0]); }
+template <typename T> constexpr int kChannels = 4 / sizeof(T);
+
+template <typename T> struct Pack;
+template <> struct Pack<float> {
+    static __device__ __forceinline__ void get(uint32_t r, float (&f)[1]) { f[0] = __uint_as_float(r); }
+    static __device__ __forceinline__ uint32_t put(const float (&f)[1]) { return __float_as_uint(f[0]); }
 };
-template <> struct Pack<__half, 1> {
-    using Raw = uint16_t;
-    static constexpr Raw kInf = 0x7c00u;
-    static __device__ __forceinline__ void get(Raw r, float (&f)[1]) {
-        f[0] = __half2float(__ushort_as_half(r));
-    }
-    static __device__ __forceinline__ Raw put(const float (&f)[1]) {
-        return __half_as_ushort(__float2half_rn(f[0]));
-    }
-};
-template <> struct Pack<__nv_bfloat16, 1> {
-    using Raw = uint16_t;
-    static constexpr Raw kInf = 0x7f80u;
-    static __device__ __forceinline__ void get(Raw r, float (&f)[1]) {
-        f[0] = __uint_as_float((uint32_t)r << 16);
-    }
-    static __device__ __forceinline__ Raw put(const float (&f)[1]) {
-        return __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
-    }
-};
-template <> struct Pack<__half, 2> {
-    using Raw = uint32_t;
-    static constexpr Raw kInf = 0x7c007c00u;
-    static __device__ __forceinline__ void get(Raw r, float (&f)[2]) {
+template <> struct Pack<__half> {
+    static __device__ __forceinline__ void get(uint32_t r, float (&f)[2]) {
         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r));
         f[0] = v.x;
         f[1] = v.y;
     }
-    static __device__ __forceinline__ Raw put(const float (&f)[2]) {
+    static __device__ __forceinline__ uint32_t put(const float (&f)[2]) {
         const __half2 v = __floats2half2_rn(f[0], f[1]);
-        return *reinterpret_cast<const Raw*>(&v);
+        return *reinterpret_cast<const uint32_t*>(&v);
     }
 };
-template <> struct Pack<__nv_bfloat16, 2> {
-    using Raw = uint32_t;
-    static constexpr Raw kInf = 0x7f807f80u;
-    static __device__ __forceinline__ void get(Raw r, float (&f)[2]) {
+template <> struct Pack<__nv_bfloat16> {
+    static __device__ __forceinline__ void get(uint32_t r, float (&f)[2]) {
         f[0] = __uint_as_float(r << 16);
         f[1] = __uint_as_float(r & 0xffff0000u);
     }
-    static __device__ __forceinline__ Raw put(const float (&f)[2]) {
+    static __device__ __forceinline__ uint32_t put(const float (&f)[2]) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(f[0], f[1]);
-        return *reinterpret_cast<const Raw*>(&v);
+        return *reinterpret_cast<const uint32_t*>(&v);
     }
 };
 
-// int8 codes of V channels
-template <int V> struct CodeRaw;
-template <> struct CodeRaw<1> { using Raw = uint8_t; };
-template <> struct CodeRaw<2> { using Raw = uint16_t; };
-
-template <int V>
-__device__ __forceinline__ typename CodeRaw<V>::Raw put_codes(const int (&q)[V]) {
-    uint32_t r = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) r |= (static_cast<uint32_t>(q[v]) & 0xffu) << (8 * v);
-    return static_cast<typename CodeRaw<V>::Raw>(r);
+// Row pointers may be aligned to less than that word: `pair` says that every output row of the
+// call is, and `count` is how many of the lane's channels exist (0 behind the last one).
+template <typename T>
+__device__ __forceinline__ void store_row(T* p, const float (&f)[kChannels<T>], bool pair, int count) {
+    const uint32_t r = Pack<T>::put(f);
+    if (pair && count == kChannels<T>) {
+        *reinterpret_cast<uint32_t*>(p) = r;
+    } else {
+        uint16_t* h = reinterpret_cast<uint16_t*>(p);
+        if (sizeof(T) == 2 && count > 0) h[0] = static_cast<uint16_t>(r);
+        if (sizeof(T) == 2 && count > 1) h[1] = static_cast<uint16_t>(r >> 16);
+    }
 }
 
-template <typename R>
-__device__ __forceinline__ R load_once(const R* p) {
-    return __ldg(p);
+template <int V>
+__device__ __forceinline__ void store_bytes(uint8_t* p, const int (&q)[V], bool pair, int count) {
+    if (V == 2 && pair && count == 2) {
+        *reinterpret_cast<uint16_t*>(p) =
+            static_cast<uint16_t>((q[0] & 0xff) | (q[V - 1] & 0xff) << 8);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < count) p[v] = static_cast<uint8_t>(q[v]);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void load_floats(const float* p, float (&f)[V], int count) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = p && v < count ? p[v] : 0.f;
+}
+
+template <int V>
+__device__ __forceinline__ void store_floats(float* p, const float (&f)[V], int count) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (v < count) p[v] = f[v];
+}
+
+// ---------------------------------------------------------------------------------------
+// asynchronous copies of a warp's segment, kSeg rows of W bytes, into its own shared memory
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows at src + j * pitch (bytes); rows from `rows` on and bytes from `width` on become 0 and are
+// not read.  `align` is what base and pitch are multiples of: 16, 4, or less.
+template <int W>
+__device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int rows,
+                                           int width, int align) {
+    const int lane = threadIdx.x & 31;
+    char* to = static_cast<char*>(dst);
+    if (align == 16) {
+        constexpr int kPer = W / 16;  // pieces per row
+#pragma unroll
+        for (int i = 0; i < kSeg * kPer / 32; ++i) {
+            const int row = (lane + 32 * i) / kPer, at = (lane + 32 * i) % kPer * 16;
+            const int bytes = row < rows ? max(0, min(16, width - at)) : 0;
+            copy_async16(static_cast<uint32_t>(__cvta_generic_to_shared(to + row * W + at)),
+                         bytes ? src + row * pitch + at : src, bytes);
+        }
+    } else if (align == 4) {
+        constexpr int kPer = W / 4;
+#pragma unroll
+        for (int i = 0; i < kSeg * kPer / 32; ++i) {
+            const int row = (lane + 32 * i) / kPer, at = (lane + 32 * i) % kPer * 4;
+            const int bytes = row < rows ? max(0, min(4, width - at)) : 0;
+            copy_async4(static_cast<uint32_t>(__cvta_generic_to_shared(to + row * W + at)),
+                        bytes ? src + row * pitch + at : src, bytes);
+        }
+    } else if (align == 2) {
+        constexpr int kPer = W / 2;
+#pragma unroll 16
+        for (int i = 0; i < kSeg * kPer / 32; ++i) {
+            const int row = (lane + 32 * i) / kPer, at = (lane + 32 * i) % kPer * 2;
+            const bool in = row < rows && at < width;
+            *reinterpret_cast<uint16_t*>(to + row * W + at) =
+                in ? __ldg(reinterpret_cast<const uint16_t*>(src + row * pitch + at)) : uint16_t(0);
+        }
+    } else {
+#pragma unroll 16
+        for (int i = 0; i < kSeg * W / 32; ++i) {
+            const int row = (lane + 32 * i) / W, at = (lane + 32 * i) % W;
+            const bool in = row < rows && at < width;
+            to[row * W + at] = in ? __ldg(src + row * pitch + at) : char(0);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -200,6 +258,43 @@ struct MapSlots {
             store_remote(p + (v * kWords + 0) * 128, m[v].A);
             store_remote(p + (v * kWords + 1) * 128, m[v].B);
             if constexpr (TWO) store_remote(p + (v * kWords + 2) * 128, m[v].L);
+        }
+    }
+    // The map of a whole tile: its warps' runs, written in the order of the recurrence.
+    template <bool PACKED>
+    static __device__ __forceinline__ void join_runs(const float* s, int lane, Map<TWO> (&all)[V]) {
+        read(s, 0, lane, all);
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) {
+            Map<TWO> m[V];
+            read(s, i, lane, m);
+#pragma unroll
+            for (int v = 0; v < V; ++v) all[v] = join<TWO, PACKED>(all[v], m[v]);
+        }
+    }
+    // `carry` through runs 0 .. n - 1; `mine` is what run `which` receives.
+    template <bool PACKED>
+    static __device__ __forceinline__ void carry_through(const float* s, int n, int which, int lane,
+                                                         float (&carry)[V], float (&mine)[V]) {
+        for (int i = 0; i < n; ++i) {
+            Map<TWO> m[V];
+            read(s, i, lane, m);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (i == which) mine[v] = carry[v];
+                carry[v] = through<TWO, PACKED>(m[v], carry[v]);
+            }
+        }
+    }
+    // h through the runs before `to`
+    template <bool PACKED>
+    static __device__ __forceinline__ void carry_into(const float* s, int to, int lane,
+                                                      float (&h)[V]) {
+        for (int i = 0; i < to; ++i) {
+            Map<TWO> m[V];
+            read(s, i, lane, m);
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = through<TWO, PACKED>(m[v], h[v]);
         }
     }
 };
