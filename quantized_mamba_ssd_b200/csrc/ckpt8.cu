@@ -22,12 +22,12 @@ pack_kernel(GatedRows x, int seqlen, int d, int8_t* __restrict__ q, uint8_t* __r
     const T* src = static_cast<const T*>(x.ptr) + b * x.batch_stride + t0 * x.token_stride + c;
     uint32_t top = 0;
     for (int j = 0; j < n; ++j)
-        top = max(top, __float_as_uint(fabsf(to_f32(src[j * x.token_stride]))));
+        top = max(top, __float_as_uint(fabsf(static_cast<float>(src[j * x.token_stride]))));
     const uint32_t ex = scale_exp(top);
     const float inv = inv_scale_of(ex);
     int8_t* dst = q + ((size_t)b * seqlen + t0) * d + c;
     for (int j = 0; j < n; ++j)
-        dst[(size_t)j * d] = static_cast<int8_t>(code_of(to_f32(src[j * x.token_stride]), inv));
+        dst[(size_t)j * d] = static_cast<int8_t>(code_of(static_cast<float>(src[j * x.token_stride]), inv));
     e[(size_t)blockIdx.y * d + c] = static_cast<uint8_t>(ex);
 }
 
@@ -42,7 +42,7 @@ unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, int s
     const int n = min(kBlock, seqlen - t0);
     const float scale = scale_of(e[(size_t)blockIdx.y * d + c]);
     const size_t at = ((size_t)b * seqlen + t0) * d + c;
-    for (int j = 0; j < n; ++j) x[at + (size_t)j * d] = from_f32<T>(scale * q[at + (size_t)j * d]);
+    for (int j = 0; j < n; ++j) x[at + (size_t)j * d] = static_cast<T>(scale * q[at + (size_t)j * d]);
 }
 
 }  // namespace

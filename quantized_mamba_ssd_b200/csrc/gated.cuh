@@ -7,7 +7,7 @@
 // floats, a = hi + lo with lo from 1 - a computed without cancellation, so that the error is a
 // rounding of the state per step instead of one of the decay.  16-bit tensors carry one float
 // from the fast exponential: its 2^-22 only reaches half a bf16 step (2^-9 of the state) at a
-// memory of 1 / (1 - a) = 8192 tokens of one and the same gate.
+// memory of 1 / (1 - a) = 8192 tokens of one and the same gate.  (Its results below 2^-126 are 0.)
 #pragma once
 
 #include <cstdint>
@@ -38,53 +38,133 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 }
 
 // ---------------------------------------------------------------------------------------
-// decays
+// the channels of one lane: one fp32, or two 16-bit ones whose fp32 values share the two-wide
+// instructions of sm_100 (half the instructions per element)
 // ---------------------------------------------------------------------------------------
-// Two-float decays for fp32 tensors (see the top of this file).
-template <typename T> constexpr bool kTwo = sizeof(T) == 4;
+template <typename T> constexpr int kChannels = 4 / sizeof(T);
+template <typename T> constexpr bool kTwo = sizeof(T) == 4;  // two-float decays
 
-struct Decay {
-    float a;   // decay, rounded to one float
-    float lo;  // a + lo is the decay to about 2^-24 of 1 - a (fp32 tensors; else 0)
-    float u;   // 1 - a without cancellation
+template <int V> struct Vec;
+template <> struct Vec<1> {
+    float x;
+    __device__ __forceinline__ float operator[](int) const { return x; }
+    __device__ __forceinline__ void set(int, float v) { x = v; }
+};
+template <> struct Vec<2> {
+    float2 x;
+    __device__ __forceinline__ float operator[](int i) const { return i ? x.y : x.x; }
+    __device__ __forceinline__ void set(int i, float v) { (i ? x.y : x.x) = v; }
 };
 
-template <typename T, bool LOGIT>
-__device__ __forceinline__ Decay decay_of(float g) {
-    Decay d;
+template <int V> __device__ __forceinline__ Vec<V> splat(float v) {
+    Vec<V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.set(i, v);
+    return r;
+}
+
+__device__ __forceinline__ unsigned long long as_pair(Vec<2> v) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x.x), "f"(v.x.y));
+    return r;
+}
+__device__ __forceinline__ Vec<2> from_pair(unsigned long long r) {
+    Vec<2> v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x.x), "=f"(v.x.y) : "l"(r));
+    return v;
+}
+
+__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) { return {fmaf(a.x, b.x, c.x)}; }
+__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {a.x * b.x}; }
+__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {a.x + b.x}; }
+__device__ __forceinline__ Vec<1> sub(Vec<1> a, Vec<1> b) { return {a.x - b.x}; }
+__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_pair(a)), "l"(as_pair(b)), "l"(as_pair(c)));
+    return from_pair(r);
+}
+__device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_pair(a)), "l"(as_pair(b)));
+    return from_pair(r);
+}
+__device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_pair(a)), "l"(as_pair(b)));
+    return from_pair(r);
+}
+__device__ __forceinline__ Vec<2> sub(Vec<2> a, Vec<2> b) { return fma(b, splat<2>(-1.f), a); }
+
+// ---------------------------------------------------------------------------------------
+// decays
+// ---------------------------------------------------------------------------------------
+template <int V> struct Decay {
+    Vec<V> a;   // decay, rounded to one float
+    Vec<V> lo;  // V == 1 (fp32 tensors): a + lo is the decay to about 2^-24 of 1 - a
+    Vec<V> u;   // 1 - a without cancellation
+};
+
+__device__ __forceinline__ float fast_exp2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float fast_rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+template <bool LOGIT>
+__device__ __forceinline__ Decay<1> decay_of(Vec<1> gate) {
+    const float g = gate.x;
+    Decay<1> d;
     if constexpr (LOGIT) {
-        if constexpr (kTwo<T>) {
-            const float t = expf(-fabsf(g));
-            const float r = __frcp_rn(1.f + t), tr = __fdiv_rn(t, 1.f + t);
-            d.a = g >= 0.f ? r : tr;
-            d.u = g >= 0.f ? tr : r;
-            if (!(g == g)) d.a = d.u = g;
-        } else {
-            // exp(-gate) = inf gives a = 0, 1 - a = 1; the product t a would be inf * 0 there
-            const float t = __expf(-g);
-            d.a = __fdividef(1.f, 1.f + t);
-            d.u = d.a < 0.5f ? 1.f - d.a : t * d.a;
-        }
+        const float t = expf(-fabsf(g));
+        const float r = __frcp_rn(1.f + t), tr = __fdiv_rn(t, 1.f + t);
+        d.a.x = g >= 0.f ? r : tr;
+        d.u.x = g >= 0.f ? tr : r;
+        if (!(g == g)) d.a.x = d.u.x = g;
     } else {
-        d.a = kTwo<T> ? expf(g) : __expf(g);
-        if constexpr (kTwo<T>) {
-            d.u = -expm1f(g);
-        } else {
-            // 1 - exp(g) = -g (1 + g/2 + g^2/6 + ..): the three terms are 2^-16 accurate
-            // below 1/16, above it the difference is
-            const float s = -g * fmaf(g, fmaf(g, 1.f / 6.f, 0.5f), 1.f);
-            d.u = fabsf(g) < 0.0625f ? s : 1.f - d.a;
-        }
+        d.a.x = expf(g);
+        d.u.x = -expm1f(g);
     }
-    d.lo = kTwo<T> && d.a >= 0.5f ? (1.f - d.a) - d.u : 0.f;
+    d.lo.x = d.a.x >= 0.5f ? (1.f - d.a.x) - d.u.x : 0.f;
+    return d;
+}
+
+template <bool LOGIT>
+__device__ __forceinline__ Decay<2> decay_of(Vec<2> g) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    Decay<2> d;
+    d.lo = splat<2>(0.f);
+    const Vec<2> one = splat<2>(1.f);
+    const Vec<2> e = mul(g, splat<2>(LOGIT ? -kLog2e : kLog2e));
+    Vec<2> t;
+    t.x = make_float2(fast_exp2(e.x.x), fast_exp2(e.x.y));
+    if constexpr (LOGIT) {
+        // t = inf gives a = 0 and 1 - a = 1; the product t a would be inf * 0 there
+        const Vec<2> s = add(one, t);
+        d.a.x = make_float2(fast_rcp(s.x.x), fast_rcp(s.x.y));
+        const Vec<2> near = mul(t, d.a), far = sub(one, d.a);
+        d.u.x = make_float2(d.a.x.x < 0.5f ? far.x.x : near.x.x, d.a.x.y < 0.5f ? far.x.y : near.x.y);
+    } else {
+        d.a = t;
+        // 1 - exp(g) = -g (1 + g/2 + g^2/6 + ..): the three terms are 2^-16 accurate below 1/16,
+        // above it the difference is
+        const Vec<2> p = fma(g, fma(g, splat<2>(1.f / 6.f), splat<2>(0.5f)), one);
+        const Vec<2> near = mul(mul(g, splat<2>(-1.f)), p), far = sub(one, d.a);
+        d.u.x = make_float2(fabsf(g.x.x) < 0.0625f ? near.x.x : far.x.x,
+                            fabsf(g.x.y) < 0.0625f ? near.x.y : far.x.y);
+    }
     return d;
 }
 
 // a h + b
-template <bool TWO>
-__device__ __forceinline__ float step(const Decay& d, float h, float b) {
-    return fmaf(d.a, h, TWO ? fmaf(d.lo, h, b) : b);
+__device__ __forceinline__ Vec<1> step(Vec<1> a, Vec<1> lo, Vec<1> h, Vec<1> b) {
+    return fma(a, h, fma(lo, h, b));
 }
+__device__ __forceinline__ Vec<2> step(Vec<2> a, Vec<2>, Vec<2> h, Vec<2> b) { return fma(a, h, b); }
 
 // ---------------------------------------------------------------------------------------
 // packed sequences

@@ -26,22 +26,22 @@ template <typename T, bool LOGIT, bool COMP, bool PACKED, bool CKPT>
 __global__ void __launch_bounds__(kTileThreads, kBwdBlocks)
 scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
     constexpr int V = kChannels<T>;
-    constexpr bool TWO = kTwo<T>;
     constexpr int kRow = kInRow<T, CKPT>;
     using P = Pack<T>;
-    using Slots = MapSlots<V, TWO>;
+    using F = Vec<V>;
+    using Slots = MapSlots<V>;
     extern __shared__ __align__(128) uint8_t staged[];
     __shared__ float fwd_maps[2][kWarps * Slots::kFloats];
     __shared__ float seg_maps[2][kWarps * Slots::kFloats];
     __shared__ float cta_maps[2][kMaxCluster * Slots::kFloats];
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = ta.cluster;
-    const int rank = blockIdx.x % R, unit = blockIdx.x / R;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int R = ta.cluster, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int d = a.channels, b = unit / ta.strips, c0 = unit % ta.strips * 32 * V;
     const int c = c0 + lane * V, count = max(0, min(V, d - c));
+    const bool whole = d - c0 >= 32 * V && ta.pair_out;
     const int tiles = (a.seqlen + kTile - 1) / kTile, steps = (tiles + R - 1) / R;
     const size_t row0 = (size_t)b * a.seqlen;
-    const float gate_one = LOGIT ? INFINITY : 0.f;  // the gate of a decay of 1
 
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
     const char *px, *pg;
@@ -57,9 +57,10 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
         sg = a.gate.token_stride * sizeof(T);
     }
     const char* pdy = static_cast<const char*>(a.dy.ptr) + (b * a.dy.batch_stride + c0) * sizeof(T);
-    const long long sdy = a.dy.token_stride * sizeof(T);
-    T* pdx = static_cast<T*>(const_cast<void*>(a.dx.ptr)) + b * a.dx.batch_stride + c;
-    T* pdg = static_cast<T*>(const_cast<void*>(a.dgate.ptr)) + b * a.dgate.batch_stride + c;
+    char* pdx = static_cast<char*>(const_cast<void*>(a.dx.ptr)) + (b * a.dx.batch_stride + c0) * sizeof(T);
+    char* pdg = static_cast<char*>(const_cast<void*>(a.dgate.ptr)) + (b * a.dgate.batch_stride + c0) * sizeof(T);
+    const long long sdy = a.dy.token_stride * sizeof(T), sdx = a.dx.token_stride * sizeof(T);
+    const long long sdg = a.dgate.token_stride * sizeof(T);
 
     // rows of step k: x, gate (or their codes), dy
     auto slot = [&](int k, int tensor) {
@@ -80,17 +81,15 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
         }
         copy_commit();
     };
+    auto state_of = [&](const float* states, int s) {
+        return load_floats<V>(states ? states + (size_t)s * d + c : nullptr, count);
+    };
 
-    float carry[V];
-    load_floats<V>(!PACKED && a.dfinal_state ? a.dfinal_state + (size_t)b * d + c : nullptr, carry, count);
-    if (PACKED && a.dinit_state && rank == 0) {  // sequences without a token
-        for (int s = warp; s < a.nseq; s += kWarps) {
-            if (__ldg(a.cu + s + 1) > __ldg(a.cu + s)) continue;
-            float h[V];
-            load_floats<V>(a.dfinal_state ? a.dfinal_state + (size_t)s * d + c : nullptr, h, count);
-            store_floats<V>(a.dinit_state + (size_t)s * d + c, h, count);
-        }
-    }
+    F carry = PACKED ? splat<V>(0.f) : state_of(a.dfinal_state, b);
+    if (PACKED && a.dinit_state && rank == 0)  // sequences without a token
+        for (int s = warp; s < a.nseq; s += kWarps)
+            if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
+                store_floats<V>(a.dinit_state + (size_t)s * d + c, state_of(a.dfinal_state, s), count);
     Held held;
 #pragma unroll
     for (int k = 0; k < kBwdStages - 1; ++k) stage(k);
@@ -102,162 +101,137 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
         m.valid = (1u << n) - 1;
         m.begin = m.end = 0;
         if constexpr (PACKED) m = marks_of(a.cu, a.nseq, t0, n, held);
-        float before[V];  // the state before the tile, then before this warp's segment
-        load_floats<V>(tile >= 0 ? a.span_states + ((size_t)b * tiles + tile) * d + c : nullptr,
-                       before, count);
-        float scale_x[V], scale_g[V];
+        // the state before the tile, then before this warp's segment
+        F before = load_floats<V>(
+            tile >= 0 ? a.span_states + ((size_t)b * tiles + tile) * d + c : nullptr, count);
+        F scale_x, scale_g;
         if constexpr (CKPT) {
             const size_t be = ((size_t)b * ta.blocks + t0 / kBlock) * d + c;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                scale_x[v] = n > 0 && v < count ? scale_of(__ldg(a.x_e + be + v)) : 1.f;
-                scale_g[v] = n > 0 && v < count ? scale_of(__ldg(a.gate_e + be + v)) : 1.f;
+                scale_x.set(v, n > 0 && v < count ? scale_of(__ldg(a.x_e + be + v)) : 0.f);
+                scale_g.set(v, n > 0 && v < count ? scale_of(__ldg(a.gate_e + be + v)) : 0.f);
             }
         }
         copy_wait<kBwdStages - 2>();
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
         stage(k + kBwdStages - 1);
-        const uint8_t* rx = slot(k, 0) + lane * (kRow / 32);
-        const uint8_t* rg = slot(k, 1) + lane * (kRow / 32);
-        const uint32_t* rdy = reinterpret_cast<const uint32_t*>(slot(k, 2)) + lane;
-        auto get = [&](const uint8_t* r, const float (&scale)[V], int j, float (&f)[V], float none) {
+        uint8_t* rx = slot(k, 0) + lane * (kRow / 32);
+        uint8_t* rg = slot(k, 1) + lane * (kRow / 32);
+        uint32_t* rdy = reinterpret_cast<uint32_t*>(slot(k, 2)) + lane;
+        if (m.valid != (1u << kSeg) - 1) {
+            // tokens of no sequence pass state and gradient on: x and dy 0, decay 1 (each lane
+            // mends its own words)
+            for (int j = 0; j < kSeg; ++j)
+                if (!(m.valid >> j & 1)) {
+                    rdy[j * 32] = 0;
+                    if constexpr (CKPT) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) rx[j * kRow + v] = rg[j * kRow + v] = 0;
+                    } else {
+                        *reinterpret_cast<uint32_t*>(rx + j * kRow) = 0;
+                        *reinterpret_cast<uint32_t*>(rg + j * kRow) = LOGIT ? P::kInf : 0u;
+                    }
+                }
+        }
+        auto decoded = [&](const uint8_t* r, F scale, int j) {
             if constexpr (CKPT) {
+                F f;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    f[v] = scale[v] * static_cast<float>(reinterpret_cast<const int8_t*>(r)[j * kRow + v]);
+                    f.set(v, static_cast<float>(reinterpret_cast<const int8_t*>(r)[j * kRow + v]));
+                return mul(f, scale);
             } else {
-                P::get(*reinterpret_cast<const uint32_t*>(r + j * kRow), f);
+                return P::get(*reinterpret_cast<const uint32_t*>(r + j * kRow));
             }
-            if (!(m.valid >> j & 1))
-#pragma unroll
-                for (int v = 0; v < V; ++v) f[v] = none;
         };
-        auto get_dy = [&](int j, float (&f)[V]) {
-            P::get(rdy[j * 32], f);
-            if (!(m.valid >> j & 1))
-#pragma unroll
-                for (int v = 0; v < V; ++v) f[v] = 0.f;
-        };
-        auto init_of = [&](int j, float (&h)[V]) {
-            const int s = __shfl_sync(0xffffffffu, m.seq, j);
-            load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, h, count);
-        };
-        auto dfinal_of = [&](int j, float (&h)[V]) {
-            const int s = __shfl_sync(0xffffffffu, m.seq, j);
-            load_floats<V>(a.dfinal_state ? a.dfinal_state + (size_t)s * d + c : nullptr, h, count);
+        auto x_of = [&](int j) { return decoded(rx, scale_x, j); };
+        auto gate_of = [&](int j) {
+            F g = decoded(rg, scale_g, j);
+            // no code stands for the logit of a decay of 1
+            if (CKPT && LOGIT && !(m.valid >> j & 1)) g = splat<V>(INFINITY);
+            return g;
         };
 
         // The segment's maps, both in one pass: of the state (forward), and of the gradient, which
         // from behind the segment reaches its first token through the product of the decays and
         // from token j through the product up to j.
-        float da[kSeg][V], lo[TWO ? kSeg : 1][V];
-        Map<TWO> fwd[V], back[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            fwd[v] = identity_map<TWO>();
-            back[v].B = 0.f;
-        }
+        F da[kSeg], lo[V == 1 ? kSeg : 1];
+        Map<V> fwd = identity_map<V>(), back = identity_map<V>();
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
-            float x[V], g[V], dy[V];
-            get(rx, scale_x, j, x, 0.f);
-            get(rg, scale_g, j, g, gate_one);
-            get_dy(j, dy);
-            if (PACKED && (m.begin >> j & 1)) {
-                float h[V];
-                init_of(j, h);
-#pragma unroll
-                for (int v = 0; v < V; ++v) fwd[v].B = h[v];
-            }
-            if (PACKED && (m.end >> j & 1)) {
-                float e[V];
-                dfinal_of(j, e);
-#pragma unroll
-                for (int v = 0; v < V; ++v) dy[v] += e[v];
-            }
+            F in = x_of(j), dy = P::get(rdy[j * 32]);
+            const Decay<V> r = decay_of<LOGIT>(gate_of(j));
+            if (PACKED && (m.begin >> j & 1))
+                fwd.B = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
+            if (PACKED && (m.end >> j & 1))
+                dy = add(dy, state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j)));
+            da[j] = r.a;
+            if constexpr (V == 1) lo[j] = r.lo;
+            if constexpr (COMP) in = mul(r.u, in);
+            fwd.B = step(r.a, r.lo, fwd.B, in);
+            extend(fwd, r);
             // behind the first end nothing reaches the segment's first token
-            const bool open = !PACKED || !(m.end & ((1u << j) - 1));
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Decay r = decay_of<T, LOGIT>(g[v]);
-                da[j][v] = r.a;
-                if constexpr (TWO) lo[j][v] = r.lo;
-                fwd[v].B = step<TWO>(r, fwd[v].B, COMP ? r.u * x[v] : x[v]);
-                extend<TWO>(fwd[v], r);
-                if (open) {
-                    if constexpr (TWO) back[v].B = fmaf(fwd[v].L, dy[v], back[v].B);
-                    back[v].B = fmaf(fwd[v].A, dy[v], back[v].B);
-                }
-            }
+            if (!PACKED || !(m.end & ((1u << j) - 1))) back.B = step(fwd.A, fwd.L, dy, back.B);
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            back[v].A = PACKED && m.end ? -1.f : fwd[v].A;
-            if constexpr (TWO) back[v].L = fwd[v].L;
-            if (PACKED && m.begin) fwd[v].A = -1.f;
-        }
+        back.A = PACKED && m.end ? splat<V>(-1.f) : fwd.A;
+        back.L = fwd.L;
+        if (PACKED && m.begin) fwd.A = splat<V>(-1.f);
 
         float* segs = seg_maps[k & 1];
         float* fwds = fwd_maps[k & 1];
-        float e[V];  // the gradient from behind this segment
-        Slots::write(segs, kWarps - 1 - warp, lane, back);
+        const int order = kWarps - 1 - warp;  // place of this warp's run
+        F e;                                  // the gradient from behind this segment
+        Slots::write(segs, order, lane, back);
         Slots::write(fwds, warp, lane, fwd);
         __syncthreads();
-        const int order = kWarps - 1 - warp;  // place of this warp's run
         if (R > 1) {
             float* ctas = cta_maps[k & 1];
             if (warp == 0) {
-                Map<TWO> all[V];
-                Slots::template join_runs<PACKED>(segs, lane, all);
+                const Map<V> all = Slots::template join_runs<PACKED>(segs, lane);
                 for (int r = 0; r < R; ++r) Slots::send(ctas, rank, lane, r, all);
             }
-            cluster_barrier();
-            Slots::template carry_through<PACKED>(ctas, R, rank, lane, carry, e);
-            Slots::template carry_into<PACKED>(segs, order, lane, e);
+            cluster_barrier(warp == 0);
+            e = Slots::template carry_through<PACKED>(ctas, R, rank, lane, carry);
+            e = Slots::template carry_into<PACKED>(segs, order, lane, e);
         } else {
-            Slots::template carry_through<PACKED>(segs, kWarps, order, lane, carry, e);
+            e = Slots::template carry_through<PACKED>(segs, kWarps, order, lane, carry);
         }
-        Slots::template carry_into<PACKED>(fwds, warp, lane, before);
+        before = Slots::template carry_into<PACKED>(fwds, warp, lane, before);
 
         // the state before every token
-        float h[kSeg][V];
+        F h[kSeg];
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
-            float x[V], g[V];
-            get(rx, scale_x, j, x, 0.f);
-            if constexpr (COMP) get(rg, scale_g, j, g, gate_one);
-            if (PACKED && (m.begin >> j & 1)) init_of(j, before);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h[j][v] = before[v];
-                const float in = COMP ? decay_of<T, LOGIT>(g[v]).u * x[v] : x[v];
-                before[v] = fmaf(da[j][v], before[v],
-                                 TWO ? fmaf(lo[TWO ? j : 0][v], before[v], in) : in);
-            }
+            F in = x_of(j);
+            if constexpr (COMP) in = mul(decay_of<LOGIT>(gate_of(j)).u, in);
+            if (PACKED && (m.begin >> j & 1))
+                before = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
+            h[j] = before;
+            before = step(da[j], lo[V == 1 ? j : 0], before, in);
         }
-        T* qdx = pdx + t0 * a.dx.token_stride;
-        T* qdg = pdg + t0 * a.dgate.token_stride;
+        char* qdx = pdx + (t0 + kSeg - 1) * sdx;
+        char* qdg = pdg + (t0 + kSeg - 1) * sdg;
 #pragma unroll
         for (int j = kSeg - 1; j >= 0; --j) {
-            float x[V], g[V], dy[V], dx[V], dg[V];
-            if constexpr (COMP) get(rx, scale_x, j, x, 0.f);
-            if constexpr (COMP || LOGIT) get(rg, scale_g, j, g, gate_one);
-            get_dy(j, dy);
-            if (PACKED && (m.end >> j & 1)) dfinal_of(j, e);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float dh = dy[v] + e[v];
-                e[v] = da[j][v] * dh;
-                if constexpr (TWO) e[v] = fmaf(da[j][v], dh, lo[TWO ? j : 0][v] * dh);
-                const float u = COMP || LOGIT ? decay_of<T, LOGIT>(g[v]).u : 1.f;
-                dx[v] = COMP ? u * dh : dh;
-                dg[v] = e[v] * (COMP ? h[j][v] - x[v] : h[j][v]);
-                if constexpr (LOGIT) dg[v] *= u;
+            if (PACKED && (m.end >> j & 1))
+                e = state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j));
+            const F dh = add(P::get(rdy[j * 32]), e);
+            e = step(da[j], lo[V == 1 ? j : 0], dh, splat<V>(0.f));
+            F u, dx = dh, past = h[j];
+            if constexpr (COMP || LOGIT) u = decay_of<LOGIT>(gate_of(j)).u;
+            if constexpr (COMP) {
+                dx = mul(u, dh);
+                past = sub(past, x_of(j));
             }
+            F dg = mul(e, past);
+            if constexpr (LOGIT) dg = mul(dg, u);
             if (m.valid >> j & 1) {
-                store_row<T>(qdx + j * a.dx.token_stride, dx, ta.pair_out, count);
-                store_row<T>(qdg + j * a.dgate.token_stride, dg, ta.pair_out, count);
+                store_row<T>(qdx + lane * 4, dx, whole, count);
+                store_row<T>(qdg + lane * 4, dg, whole, count);
             }
+            qdx -= sdx;
+            qdg -= sdg;
             if (PACKED && (m.begin >> j & 1)) {
                 const int s = __shfl_sync(0xffffffffu, m.seq, j);
                 if (a.dinit_state) store_floats<V>(a.dinit_state + (size_t)s * d + c, e, count);

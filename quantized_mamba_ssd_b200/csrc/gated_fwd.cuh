@@ -19,26 +19,29 @@ template <typename T, bool LOGIT, bool COMP, bool PACKED>
 __global__ void __launch_bounds__(kTileThreads, kFwdBlocks)
 scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
     constexpr int V = kChannels<T>;
-    constexpr bool TWO = kTwo<T>;
     using P = Pack<T>;
-    using Slots = MapSlots<V, TWO>;
+    using F = Vec<V>;
+    using Slots = MapSlots<V>;
     extern __shared__ __align__(128) uint8_t staged[];
     __shared__ float seg_maps[2][kWarps * Slots::kFloats];
     __shared__ float cta_maps[2][kMaxCluster * Slots::kFloats];
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = ta.cluster;
-    const int rank = blockIdx.x % R, unit = blockIdx.x / R;
+    // the shuffle tells the compiler that the warp's index, and with it every row's address, is
+    // the same in all lanes
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int R = ta.cluster, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int d = a.channels, b = unit / ta.strips, c0 = unit % ta.strips * 32 * V;
     const int c = c0 + lane * V, count = max(0, min(V, d - c));
+    const bool full = d - c0 >= 32 * V, whole = full && ta.pair_out, whole_codes = full && ta.pair_codes;
     const int tiles = (a.seqlen + kTile - 1) / kTile, steps = (tiles + R - 1) / R;
     const size_t row0 = (size_t)b * a.seqlen;
-    const float gate_one = LOGIT ? INFINITY : 0.f;  // the gate of a decay of 1
 
     const char* px = static_cast<const char*>(a.x.ptr) + (b * a.x.batch_stride + c0) * sizeof(T);
     const char* pg = static_cast<const char*>(a.gate.ptr) + (b * a.gate.batch_stride + c0) * sizeof(T);
+    char* py = static_cast<char*>(const_cast<void*>(a.y.ptr)) + (b * a.y.batch_stride + c0) * sizeof(T);
     const long long sx = a.x.token_stride * sizeof(T), sg = a.gate.token_stride * sizeof(T);
+    const long long sy = a.y.token_stride * sizeof(T);
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
-    T* py = static_cast<T*>(const_cast<void*>(a.y.ptr)) + b * a.y.batch_stride + c;
 
     auto slot = [&](int k, int tensor) {
         return staged + (k % kFwdStages) * kFwdStage + (tensor * kWarps + warp) * kSeg * kRowBytes;
@@ -52,17 +55,15 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
         }
         copy_commit();
     };
+    auto init_of = [&](int s) {
+        return load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, count);
+    };
 
-    float carry[V];
-    load_floats<V>(!PACKED && a.init_state ? a.init_state + (size_t)b * d + c : nullptr, carry, count);
-    if (PACKED && a.final_state && rank == 0) {  // sequences without a token
-        for (int s = warp; s < a.nseq; s += kWarps) {
-            if (__ldg(a.cu + s + 1) > __ldg(a.cu + s)) continue;
-            float h[V];
-            load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, h, count);
-            store_floats<V>(a.final_state + (size_t)s * d + c, h, count);
-        }
-    }
+    F carry = PACKED ? splat<V>(0.f) : init_of(b);
+    if (PACKED && a.final_state && rank == 0)  // sequences without a token
+        for (int s = warp; s < a.nseq; s += kWarps)
+            if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
+                store_floats<V>(a.final_state + (size_t)s * d + c, init_of(s), count);
     Held held;
 #pragma unroll
     for (int k = 0; k < kFwdStages - 1; ++k) stage(k);
@@ -76,20 +77,16 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
         copy_wait<kFwdStages - 2>();
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
         stage(k + kFwdStages - 1);
-        const uint32_t* rx = reinterpret_cast<const uint32_t*>(slot(k, 0)) + lane;
-        const uint32_t* rg = reinterpret_cast<const uint32_t*>(slot(k, 1)) + lane;
-        auto get_x = [&](int j, float (&x)[V]) {
-            P::get(rx[j * 32], x);
-            if (!(m.valid >> j & 1))
-#pragma unroll
-                for (int v = 0; v < V; ++v) x[v] = 0.f;
-        };
-        auto get_gate = [&](int j, float (&g)[V], float none) {
-            P::get(rg[j * 32], g);
-            if (!(m.valid >> j & 1))
-#pragma unroll
-                for (int v = 0; v < V; ++v) g[v] = none;
-        };
+        uint32_t* rx = reinterpret_cast<uint32_t*>(slot(k, 0)) + lane;
+        uint32_t* rg = reinterpret_cast<uint32_t*>(slot(k, 1)) + lane;
+        if (m.valid != (1u << kSeg) - 1) {
+            // tokens of no sequence keep the state: x 0, decay 1 (each lane mends its own words)
+            for (int j = 0; j < kSeg; ++j)
+                if (!(m.valid >> j & 1)) {
+                    rx[j * 32] = 0;
+                    rg[j * 32] = LOGIT ? P::kInf : 0u;
+                }
+        }
 
         if (a.x_q && n > 0) {  // the segment is one checkpoint block per channel
             uint32_t top_x[V], top_g[V];  // bits of the magnitudes: their order, NaN on top
@@ -97,13 +94,12 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
             for (int v = 0; v < V; ++v) top_x[v] = top_g[v] = 0;
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
-                float x[V], g[V];
-                get_x(j, x);
-                get_gate(j, g, 0.f);
+                const F x = P::get(rx[j * 32]), g = P::get(rg[j * 32]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     top_x[v] = max(top_x[v], __float_as_uint(fabsf(x[v])));
-                    top_g[v] = max(top_g[v], __float_as_uint(fabsf(held_gate<LOGIT>(g[v]))));
+                    if (!LOGIT || (m.valid >> j & 1))
+                        top_g[v] = max(top_g[v], __float_as_uint(fabsf(held_gate<LOGIT>(g[v]))));
                 }
             }
             float inv_x[V], inv_g[V];
@@ -121,95 +117,69 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
                 if (!(m.valid >> j & 1)) continue;
-                float x[V], g[V];
+                const F x = P::get(rx[j * 32]), g = P::get(rg[j * 32]);
                 int code[V];
-                get_x(j, x);
-                get_gate(j, g, 0.f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) code[v] = code_of(x[v], inv_x[v]);
-                store_bytes<V>(qx + (size_t)j * d, code, ta.pair_codes, count);
+                store_bytes<V>(qx + (size_t)j * d, code, whole_codes, count);
 #pragma unroll
                 for (int v = 0; v < V; ++v) code[v] = code_of(held_gate<LOGIT>(g[v]), inv_g[v]);
-                store_bytes<V>(qg + (size_t)j * d, code, ta.pair_codes, count);
+                store_bytes<V>(qg + (size_t)j * d, code, whole_codes, count);
             }
             const size_t be = ((size_t)b * ta.blocks + t0 / kBlock) * d + c;
-            store_bytes<V>(a.x_e + be, ex, ta.pair_codes, count);
-            store_bytes<V>(a.gate_e + be, eg, ta.pair_codes, count);
+            store_bytes<V>(a.x_e + be, ex, whole_codes, count);
+            store_bytes<V>(a.gate_e + be, eg, whole_codes, count);
         }
 
         // decays (and weighted inputs) of the segment, and its map
-        float da[kSeg][V], lo[TWO ? kSeg : 1][V], wx[COMP ? kSeg : 1][V];
-        Map<TWO> seg[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) seg[v] = identity_map<TWO>();
+        F da[kSeg], lo[V == 1 ? kSeg : 1], wx[COMP ? kSeg : 1];
+        Map<V> seg = identity_map<V>();
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
-            float x[V], g[V];
-            get_x(j, x);
-            get_gate(j, g, gate_one);
-            if (PACKED && (m.begin >> j & 1)) {
-                const int s = __shfl_sync(0xffffffffu, m.seq, j);
-                float h[V];
-                load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, h, count);
-#pragma unroll
-                for (int v = 0; v < V; ++v) seg[v].B = h[v];
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Decay r = decay_of<T, LOGIT>(g[v]);
-                da[j][v] = r.a;
-                if constexpr (TWO) lo[j][v] = r.lo;
-                if constexpr (COMP) wx[j][v] = r.u * x[v];
-                seg[v].B = step<TWO>(r, seg[v].B, COMP ? wx[COMP ? j : 0][v] : x[v]);
-                extend<TWO>(seg[v], r);
-            }
+            F in = P::get(rx[j * 32]);
+            const Decay<V> r = decay_of<LOGIT>(P::get(rg[j * 32]));
+            if (PACKED && (m.begin >> j & 1)) seg.B = init_of(__shfl_sync(0xffffffffu, m.seq, j));
+            da[j] = r.a;
+            if constexpr (V == 1) lo[j] = r.lo;
+            if constexpr (COMP) wx[j] = in = mul(r.u, in);
+            seg.B = step(r.a, r.lo, seg.B, in);
+            extend(seg, r);
         }
-        if (PACKED && m.begin) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) seg[v].A = -1.f;
-        }
+        if (PACKED && m.begin) seg.A = splat<V>(-1.f);
 
         // the carry into this segment, and into the next step
         float* segs = seg_maps[k & 1];
-        float h[V];
+        F h;
         Slots::write(segs, warp, lane, seg);
         __syncthreads();
         if (R > 1) {
             float* ctas = cta_maps[k & 1];
             if (warp == kWarps - 1) {
-                Map<TWO> all[V];
-                Slots::template join_runs<PACKED>(segs, lane, all);
+                const Map<V> all = Slots::template join_runs<PACKED>(segs, lane);
                 for (int r = 0; r < R; ++r) Slots::send(ctas, rank, lane, r, all);
             }
-            cluster_barrier();
-            Slots::template carry_through<PACKED>(ctas, R, rank, lane, carry, h);
-            Slots::template carry_into<PACKED>(segs, warp, lane, h);
+            cluster_barrier(warp == kWarps - 1);
+            h = Slots::template carry_through<PACKED>(ctas, R, rank, lane, carry);
+            h = Slots::template carry_into<PACKED>(segs, warp, lane, h);
         } else {
-            Slots::template carry_through<PACKED>(segs, kWarps, warp, lane, carry, h);
+            h = Slots::template carry_through<PACKED>(segs, kWarps, warp, lane, carry);
         }
 
         if (a.span_states && warp == 0 && n > 0) {
-            float s[V];
             const bool none = PACKED && (!(m.valid & 1) || (m.begin & 1));
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = none ? 0.f : h[v];
-            store_floats<V>(a.span_states + ((size_t)b * tiles + tile) * d + c, s, count);
+            store_floats<V>(a.span_states + ((size_t)b * tiles + tile) * d + c,
+                            none ? splat<V>(0.f) : h, count);
         }
-        T* qy = py + t0 * a.y.token_stride;
+        char* qy = py + t0 * sy;
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
-            float x[V];
-            if constexpr (!COMP) get_x(j, x);
-            if (PACKED && (m.begin >> j & 1)) {
-                const int s = __shfl_sync(0xffffffffu, m.seq, j);
-                load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, h, count);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float in = COMP ? wx[COMP ? j : 0][v] : x[v];
-                h[v] = fmaf(da[j][v], h[v], TWO ? fmaf(lo[TWO ? j : 0][v], h[v], in) : in);
-            }
-            if (m.valid >> j & 1) store_row<T>(qy + j * a.y.token_stride, h, ta.pair_out, count);
+            F in;
+            if constexpr (COMP) in = wx[j];
+            else in = P::get(rx[j * 32]);
+            if (PACKED && (m.begin >> j & 1)) h = init_of(__shfl_sync(0xffffffffu, m.seq, j));
+            h = step(da[j], lo[V == 1 ? j : 0], h, in);
+            if (m.valid >> j & 1) store_row<T>(qy + lane * 4, h, whole, count);
+            qy += sy;
             if (PACKED && (m.end >> j & 1)) {
                 const int s = __shfl_sync(0xffffffffu, m.seq, j);
                 if (a.final_state) store_floats<V>(a.final_state + (size_t)s * d + c, h, count);

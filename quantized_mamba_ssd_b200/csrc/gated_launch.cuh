@@ -44,7 +44,7 @@ inline int cluster_size(long long units, int tiles, int blocks_per_sm) {
     const double room = (double)sms * blocks_per_sm;
     int best = 1;
     double most = 0;
-    for (int r = 1; r <= kMaxCluster && (r == 1 || r <= tiles); r *= 2) {
+    for (int r = 1; r <= kMaxCluster && (r == 1 || r <= tiles); ++r) {
         const double waves = units * r / room;
         const double full = waves <= 1 ? waves : waves / std::ceil(waves);
         if (full > most * 1.02) {

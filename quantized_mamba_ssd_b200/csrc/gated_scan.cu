@@ -11,13 +11,23 @@ constexpr int kThreads = 128;
 
 template <typename T, bool LOGIT>
 __global__ void __launch_bounds__(kThreads) step_kernel(const GatedStepArgs a) {
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+    constexpr int V = kChannels<T>;
+    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * V;
     if (i >= a.count) return;
-    const Decay k = decay_of<T, LOGIT>(to_f32(static_cast<const T*>(a.gate)[i]));
-    const float x = to_f32(static_cast<const T*>(a.x)[i]);
-    const float h = step<kTwo<T>>(k, a.state[i], a.complement ? k.u * x : x);
-    a.state[i] = h;
-    static_cast<T*>(a.y)[i] = from_f32<T>(h);
+    const int n = static_cast<int>(a.count - i < V ? a.count - i : V);
+    Vec<V> g = splat<V>(0.f), x = g, h = g;
+    for (int v = 0; v < n; ++v) {
+        g.set(v, static_cast<float>(static_cast<const T*>(a.gate)[i + v]));
+        x.set(v, static_cast<float>(static_cast<const T*>(a.x)[i + v]));
+        h.set(v, a.state[i + v]);
+    }
+    const Decay<V> r = decay_of<LOGIT>(g);
+    if (a.complement) x = mul(r.u, x);
+    h = step(r.a, r.lo, h, x);
+    for (int v = 0; v < n; ++v) {
+        a.state[i + v] = h[v];
+        static_cast<T*>(a.y)[i + v] = static_cast<T>(h[v]);
+    }
 }
 
 template <typename F>
@@ -47,7 +57,8 @@ cudaError_t launch_gated_scan_bwd(const GatedArgs& a, cudaStream_t st) {
 cudaError_t launch_gated_step(const GatedStepArgs& a, cudaStream_t st) {
     return by_type(a.io_dtype, [&](auto zero) {
         using T = decltype(zero);
-        const long long grid = (a.count + kThreads - 1) / kThreads;
+        constexpr int per = kThreads * kChannels<T>;
+        const long long grid = (a.count + per - 1) / per;
         (a.logit ? step_kernel<T, true> : step_kernel<T, false>)<<<(unsigned)grid, kThreads, 0, st>>>(a);
         return cudaGetLastError();
     });

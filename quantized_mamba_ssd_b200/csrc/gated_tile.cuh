@@ -26,52 +26,52 @@ static_assert(kTile == kSpan, "the backward starts every tile from a saved state
 // ---------------------------------------------------------------------------------------
 // the channels of one token and lane: one 32-bit word, so that a warp's row is 128 bytes
 // ---------------------------------------------------------------------------------------
-template <typename T> constexpr int kChannels = 4 / sizeof(T);
-
 template <typename T> struct Pack;
 template <> struct Pack<float> {
-    static __device__ __forceinline__ void get(uint32_t r, float (&f)[1]) { f[0] = __uint_as_float(r); }
-    static __device__ __forceinline__ uint32_t put(const float (&f)[1]) { return __float_as_uint(f[0]); }
+    static constexpr uint32_t kInf = 0x7f800000u;
+    static __device__ __forceinline__ Vec<1> get(uint32_t r) { return {__uint_as_float(r)}; }
+    static __device__ __forceinline__ uint32_t put(Vec<1> f) { return __float_as_uint(f.x); }
 };
 template <> struct Pack<__half> {
-    static __device__ __forceinline__ void get(uint32_t r, float (&f)[2]) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r));
-        f[0] = v.x;
-        f[1] = v.y;
+    static constexpr uint32_t kInf = 0x7c007c00u;
+    static __device__ __forceinline__ Vec<2> get(uint32_t r) {
+        return {__half22float2(*reinterpret_cast<const __half2*>(&r))};
     }
-    static __device__ __forceinline__ uint32_t put(const float (&f)[2]) {
-        const __half2 v = __floats2half2_rn(f[0], f[1]);
+    static __device__ __forceinline__ uint32_t put(Vec<2> f) {
+        const __half2 v = __floats2half2_rn(f.x.x, f.x.y);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
 };
 template <> struct Pack<__nv_bfloat16> {
-    static __device__ __forceinline__ void get(uint32_t r, float (&f)[2]) {
-        f[0] = __uint_as_float(r << 16);
-        f[1] = __uint_as_float(r & 0xffff0000u);
+    static constexpr uint32_t kInf = 0x7f807f80u;
+    static __device__ __forceinline__ Vec<2> get(uint32_t r) {
+        return {make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u))};
     }
-    static __device__ __forceinline__ uint32_t put(const float (&f)[2]) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(f[0], f[1]);
+    static __device__ __forceinline__ uint32_t put(Vec<2> f) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f.x.x, f.x.y);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
 };
 
-// Row pointers may be aligned to less than that word: `pair` says that every output row of the
-// call is, and `count` is how many of the lane's channels exist (0 behind the last one).
+// Row pointers may be aligned to less than that word, and the last strip may be narrower: `whole`
+// (the same in all lanes) says that neither is so; `count` is how many of the lane's channels exist.
 template <typename T>
-__device__ __forceinline__ void store_row(T* p, const float (&f)[kChannels<T>], bool pair, int count) {
+__device__ __forceinline__ void store_row(char* p, Vec<kChannels<T>> f, bool whole, int count) {
     const uint32_t r = Pack<T>::put(f);
-    if (pair && count == kChannels<T>) {
+    if (whole) {
         *reinterpret_cast<uint32_t*>(p) = r;
-    } else {
+    } else if (sizeof(T) == 2) {
         uint16_t* h = reinterpret_cast<uint16_t*>(p);
-        if (sizeof(T) == 2 && count > 0) h[0] = static_cast<uint16_t>(r);
-        if (sizeof(T) == 2 && count > 1) h[1] = static_cast<uint16_t>(r >> 16);
+        if (count > 0) h[0] = static_cast<uint16_t>(r);
+        if (count > 1) h[1] = static_cast<uint16_t>(r >> 16);
+    } else if (count > 0) {
+        *reinterpret_cast<uint32_t*>(p) = r;
     }
 }
 
 template <int V>
-__device__ __forceinline__ void store_bytes(uint8_t* p, const int (&q)[V], bool pair, int count) {
-    if (V == 2 && pair && count == 2) {
+__device__ __forceinline__ void store_bytes(uint8_t* p, const int (&q)[V], bool whole, int count) {
+    if (V == 2 && whole) {
         *reinterpret_cast<uint16_t*>(p) =
             static_cast<uint16_t>((q[0] & 0xff) | (q[V - 1] & 0xff) << 8);
     } else {
@@ -81,14 +81,17 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, const int (&q)[V], bool 
     }
 }
 
+// Floats of the lane's channels; 0 from a null pointer and for channels that do not exist.
 template <int V>
-__device__ __forceinline__ void load_floats(const float* p, float (&f)[V], int count) {
+__device__ __forceinline__ Vec<V> load_floats(const float* p, int count) {
+    Vec<V> f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = p && v < count ? p[v] : 0.f;
+    for (int v = 0; v < V; ++v) f.set(v, p && v < count ? p[v] : 0.f);
+    return f;
 }
 
 template <int V>
-__device__ __forceinline__ void store_floats(float* p, const float (&f)[V], int count) {
+__device__ __forceinline__ void store_floats(float* p, Vec<V> f, int count) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
         if (v < count) p[v] = f[v];
@@ -100,6 +103,9 @@ __device__ __forceinline__ void store_floats(float* p, const float (&f)[V], int 
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
+}
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -118,13 +124,24 @@ __device__ __forceinline__ void stage_rows(void* dst, const char* src, long long
     const int lane = threadIdx.x & 31;
     char* to = static_cast<char*>(dst);
     if (align == 16) {
-        constexpr int kPer = W / 16;  // pieces per row
+        constexpr int kPer = W / 16;   // pieces per row
+        constexpr int kStep = 32 / kPer;  // rows per instruction
+        const int row = lane / kPer, at = lane % kPer * 16;
+        const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(to)) + row * W + at;
+        const char* p = src + row * pitch + at;
+        if (rows == kSeg && width >= W) {
 #pragma unroll
-        for (int i = 0; i < kSeg * kPer / 32; ++i) {
-            const int row = (lane + 32 * i) / kPer, at = (lane + 32 * i) % kPer * 16;
-            const int bytes = row < rows ? max(0, min(16, width - at)) : 0;
-            copy_async16(static_cast<uint32_t>(__cvta_generic_to_shared(to + row * W + at)),
-                         bytes ? src + row * pitch + at : src, bytes);
+            for (int i = 0; i < kSeg / kStep; ++i) {
+                copy_async16(d + i * kStep * W, p);
+                p += kStep * pitch;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSeg / kStep; ++i) {
+                const int bytes = row + i * kStep < rows ? max(0, min(16, width - at)) : 0;
+                copy_async16(d + i * kStep * W, bytes ? p : src, bytes);
+                p += kStep * pitch;
+            }
         }
     } else if (align == 4) {
         constexpr int kPer = W / 4;
@@ -160,58 +177,57 @@ __device__ __forceinline__ void stage_rows(void* dst, const char* src, long long
 // In packed rows A < 0 marks a run in which a sequence begins (or, backward, ends): the carry is
 // dropped by a selection, not by a factor 0, so that what another sequence left in it (infinities
 // and NaN included) cannot come through.
-template <bool TWO> struct Map;
-template <> struct Map<false> {
-    float A, B;
-};
-template <> struct Map<true> {
-    float A, B, L;
+template <int V> struct Map {
+    Vec<V> A, B;
+    Vec<V> L;  // V == 1 only: fp32 tensors carry decays as two floats
 };
 
-template <bool TWO>
-__device__ __forceinline__ Map<TWO> identity_map() {
-    Map<TWO> m;
-    m.A = 1.f;
-    m.B = 0.f;
-    if constexpr (TWO) m.L = 0.f;
-    return m;
+template <int V> __device__ __forceinline__ Map<V> identity_map() {
+    return {splat<V>(1.f), splat<V>(0.f), splat<V>(0.f)};
 }
 
-template <bool TWO, bool PACKED>
-__device__ __forceinline__ float through(const Map<TWO>& m, float carry) {
-    float b = m.B;
-    if constexpr (TWO) b = fmaf(m.L, carry, b);
-    const float r = fmaf(m.A, carry, b);
-    return PACKED && m.A < 0.f ? m.B : r;
+template <bool PACKED, int V>
+__device__ __forceinline__ Vec<V> through(const Map<V>& m, Vec<V> carry) {
+    Vec<V> r = step(m.A, m.L, carry, m.B);
+    if constexpr (PACKED) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (m.A[v] < 0.f) r.set(v, m.B[v]);
+    }
+    return r;
 }
 
 // The decay product of a run followed by one more decay (B is the caller's).
-template <bool TWO>
-__device__ __forceinline__ void extend(Map<TWO>& m, const Decay& d) {
-    const float p = m.A * d.a;
-    if constexpr (TWO) m.L = fmaf(m.A, d.lo, fmaf(m.L, d.a, fmaf(m.A, d.a, -p)));
+__device__ __forceinline__ void extend(Map<1>& m, const Decay<1>& d) {
+    const Vec<1> p = mul(m.A, d.a);
+    m.L = fma(m.A, d.lo, fma(m.L, d.a, fma(m.A, d.a, sub(splat<1>(0.f), p))));
     m.A = p;
 }
+__device__ __forceinline__ void extend(Map<2>& m, const Decay<2>& d) { m.A = mul(m.A, d.a); }
 
 // first, then second
-template <bool TWO, bool PACKED>
-__device__ __forceinline__ Map<TWO> join(const Map<TWO>& first, const Map<TWO>& second) {
-    Map<TWO> r;
-    r.B = through<TWO, PACKED>(second, first.B);
-    const float p = first.A * second.A;
-    r.A = p;
-    if constexpr (TWO)
-        r.L = fmaf(first.A, second.L, fmaf(first.L, second.A, fmaf(first.A, second.A, -p)));
-    if (PACKED && (first.A < 0.f || second.A < 0.f)) r.A = -1.f;
+template <bool PACKED, int V>
+__device__ __forceinline__ Map<V> join(const Map<V>& first, const Map<V>& second) {
+    Map<V> r = first;
+    r.B = through<PACKED>(second, first.B);
+    extend(r, Decay<V>{second.A, second.L, second.A});
+    if constexpr (PACKED) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (first.A[v] < 0.f || second.A[v] < 0.f) r.A.set(v, -1.f);
+    }
     return r;
 }
 
 // ---------------------------------------------------------------------------------------
 // clusters
 // ---------------------------------------------------------------------------------------
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-                 ::: "memory");
+// All threads of all CTAs of the cluster meet.  Only the threads that sent maps release: a release
+// waits for every write the thread has in flight, its rows of the last step included.
+__device__ __forceinline__ void cluster_barrier(bool sent) {
+    if (sent) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Address of this CTA's shared-memory word `p` in CTA `rank` of the cluster.
@@ -226,76 +242,77 @@ __device__ __forceinline__ void store_remote(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// Maps of `n` runs, [n][floats of a map][32 * V]: lanes read and write consecutive words.
-template <int V, bool TWO>
+// Maps of runs, [run][word][lane] with A, B (and L) of every channel as words of their own.
+template <int V>
 struct MapSlots {
-    static constexpr int kWords = TWO ? 3 : 2;
-    static constexpr int kFloats = kWords * 32 * V;  // per run
+    static constexpr int kWords = V == 1 ? 3 : 4;
+    static constexpr int kFloats = kWords * 32;  // per run
 
-    static __device__ __forceinline__ void write(float* s, int run, int lane, const Map<TWO> (&m)[V]) {
+    static __device__ __forceinline__ void write(float* s, int run, int lane, const Map<V>& m) {
         float* p = s + run * kFloats + lane;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            p[(v * kWords + 0) * 32] = m[v].A;
-            p[(v * kWords + 1) * 32] = m[v].B;
-            if constexpr (TWO) p[(v * kWords + 2) * 32] = m[v].L;
+        if constexpr (V == 1) {
+            p[0] = m.A.x;
+            p[32] = m.B.x;
+            p[64] = m.L.x;
+        } else {
+            p[0] = m.A.x.x;
+            p[32] = m.A.x.y;
+            p[64] = m.B.x.x;
+            p[96] = m.B.x.y;
         }
     }
-    static __device__ __forceinline__ void read(const float* s, int run, int lane, Map<TWO> (&m)[V]) {
+    static __device__ __forceinline__ Map<V> read(const float* s, int run, int lane) {
         const float* p = s + run * kFloats + lane;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            m[v].A = p[(v * kWords + 0) * 32];
-            m[v].B = p[(v * kWords + 1) * 32];
-            if constexpr (TWO) m[v].L = p[(v * kWords + 2) * 32];
+        Map<V> m;
+        if constexpr (V == 1) {
+            m.A.x = p[0];
+            m.B.x = p[32];
+            m.L.x = p[64];
+        } else {
+            m.A.x = make_float2(p[0], p[32]);
+            m.B.x = make_float2(p[64], p[96]);
+            m.L = splat<V>(0.f);
         }
+        return m;
     }
     static __device__ __forceinline__ void send(const float* s, int run, int lane, int rank,
-                                                const Map<TWO> (&m)[V]) {
+                                                const Map<V>& m) {
         const uint32_t p = remote_smem(s + run * kFloats + lane, rank);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            store_remote(p + (v * kWords + 0) * 128, m[v].A);
-            store_remote(p + (v * kWords + 1) * 128, m[v].B);
-            if constexpr (TWO) store_remote(p + (v * kWords + 2) * 128, m[v].L);
+        if constexpr (V == 1) {
+            store_remote(p, m.A.x);
+            store_remote(p + 128, m.B.x);
+            store_remote(p + 256, m.L.x);
+        } else {
+            store_remote(p, m.A.x.x);
+            store_remote(p + 128, m.A.x.y);
+            store_remote(p + 256, m.B.x.x);
+            store_remote(p + 384, m.B.x.y);
         }
     }
     // The map of a whole tile: its warps' runs, written in the order of the recurrence.
     template <bool PACKED>
-    static __device__ __forceinline__ void join_runs(const float* s, int lane, Map<TWO> (&all)[V]) {
-        read(s, 0, lane, all);
+    static __device__ __forceinline__ Map<V> join_runs(const float* s, int lane) {
+        Map<V> all = read(s, 0, lane);
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) {
-            Map<TWO> m[V];
-            read(s, i, lane, m);
-#pragma unroll
-            for (int v = 0; v < V; ++v) all[v] = join<TWO, PACKED>(all[v], m[v]);
-        }
+        for (int i = 1; i < kWarps; ++i) all = join<PACKED>(all, read(s, i, lane));
+        return all;
     }
-    // `carry` through runs 0 .. n - 1; `mine` is what run `which` receives.
+    // `carry` through runs 0 .. n - 1; returns what run `which` receives.
     template <bool PACKED>
-    static __device__ __forceinline__ void carry_through(const float* s, int n, int which, int lane,
-                                                         float (&carry)[V], float (&mine)[V]) {
+    static __device__ __forceinline__ Vec<V> carry_through(const float* s, int n, int which,
+                                                           int lane, Vec<V>& carry) {
+        Vec<V> mine = carry;
         for (int i = 0; i < n; ++i) {
-            Map<TWO> m[V];
-            read(s, i, lane, m);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (i == which) mine[v] = carry[v];
-                carry[v] = through<TWO, PACKED>(m[v], carry[v]);
-            }
+            if (i == which) mine = carry;
+            carry = through<PACKED>(read(s, i, lane), carry);
         }
+        return mine;
     }
     // h through the runs before `to`
     template <bool PACKED>
-    static __device__ __forceinline__ void carry_into(const float* s, int to, int lane,
-                                                      float (&h)[V]) {
-        for (int i = 0; i < to; ++i) {
-            Map<TWO> m[V];
-            read(s, i, lane, m);
-#pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = through<TWO, PACKED>(m[v], h[v]);
-        }
+    static __device__ __forceinline__ Vec<V> carry_into(const float* s, int to, int lane, Vec<V> h) {
+        for (int i = 0; i < to; ++i) h = through<PACKED>(read(s, i, lane), h);
+        return h;
     }
 };
 
