@@ -27,13 +27,15 @@ __global__ void __launch_bounds__(kTileThreads, kBwdBlocks)
 scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
     constexpr int V = kChannels<T>;
     constexpr int kRow = kInRow<T, CKPT>;
-    using P = Pack<T>;
+    using Pk = Pack<T>;
+    constexpr bool kUsesU = COMP || LOGIT;      // the gradients need 1 - a
+    constexpr bool kHold = V == 1 || !kUsesU;  // decays stay in registers; else they are computed again
     using F = Vec<V>;
     using Slots = MapSlots<V>;
     extern __shared__ __align__(128) uint8_t staged[];
-    __shared__ float fwd_maps[2][kWarps * Slots::kFloats];
-    __shared__ float seg_maps[2][kWarps * Slots::kFloats];
-    __shared__ float cta_maps[2][kMaxCluster * Slots::kFloats];
+    __shared__ __align__(16) float fwd_maps[2][kWarps * Slots::kFloats];
+    __shared__ __align__(16) float seg_maps[2][kWarps * Slots::kFloats];
+    __shared__ __align__(16) float cta_maps[2][kMaxCluster * Slots::kFloats];
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int R = ta.cluster, rank = blockIdx.x % R, unit = blockIdx.x / R;
@@ -119,7 +121,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
         uint8_t* rx = slot(k, 0) + lane * (kRow / 32);
         uint8_t* rg = slot(k, 1) + lane * (kRow / 32);
         uint32_t* rdy = reinterpret_cast<uint32_t*>(slot(k, 2)) + lane;
-        if (m.valid != (1u << kSeg) - 1) {
+        if (m.valid != kAll) {
             // tokens of no sequence pass state and gradient on: x and dy 0, decay 1 (each lane
             // mends its own words)
             for (int j = 0; j < kSeg; ++j)
@@ -130,7 +132,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
                         for (int v = 0; v < V; ++v) rx[j * kRow + v] = rg[j * kRow + v] = 0;
                     } else {
                         *reinterpret_cast<uint32_t*>(rx + j * kRow) = 0;
-                        *reinterpret_cast<uint32_t*>(rg + j * kRow) = LOGIT ? P::kInf : 0u;
+                        *reinterpret_cast<uint32_t*>(rg + j * kRow) = LOGIT ? Pk::kInf : 0u;
                     }
                 }
         }
@@ -142,7 +144,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
                     f.set(v, static_cast<float>(reinterpret_cast<const int8_t*>(r)[j * kRow + v]));
                 return mul(f, scale);
             } else {
-                return P::get(*reinterpret_cast<const uint32_t*>(r + j * kRow));
+                return Pk::get(*reinterpret_cast<const uint32_t*>(r + j * kRow));
             }
         };
         auto x_of = [&](int j) { return decoded(rx, scale_x, j); };
@@ -153,24 +155,29 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
             return g;
         };
 
-        // The segment's maps, both in one pass: of the state (forward), and of the gradient, which
-        // from behind the segment reaches its first token through the product of the decays and
-        // from token j through the product up to j.
-        F da[kSeg], lo[V == 1 ? kSeg : 1];
+        // The segment's maps, both in one pass: of the state, which behind token j is P[j] carry +
+        // B[j] (P with its low part Q in fp32), and of the gradient, which from behind the segment
+        // reaches its first token through the product of the decays and from token j through P[j].
+        F P[kSeg], Q[V == 1 ? kSeg : 1], B[kSeg];
+        F da[kHold ? kSeg : 1], lo[V == 1 ? kSeg : 1], u[V == 1 && kUsesU ? kSeg : 1];
         Map<V> fwd = identity_map<V>(), back = identity_map<V>();
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
-            F in = x_of(j), dy = P::get(rdy[j * 32]);
+            F in = x_of(j), dy = Pk::get(rdy[j * 32]);
             const Decay<V> r = decay_of<LOGIT>(gate_of(j));
             if (PACKED && (m.begin >> j & 1))
                 fwd.B = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
             if (PACKED && (m.end >> j & 1))
                 dy = add(dy, state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j)));
-            da[j] = r.a;
+            if constexpr (kHold) da[j] = r.a;
             if constexpr (V == 1) lo[j] = r.lo;
+            if constexpr (V == 1 && kUsesU) u[j] = r.u;
             if constexpr (COMP) in = mul(r.u, in);
             fwd.B = step(r.a, r.lo, fwd.B, in);
             extend(fwd, r);
+            P[j] = fwd.A;
+            B[j] = fwd.B;
+            if constexpr (V == 1) Q[j] = fwd.L;
             // behind the first end nothing reaches the segment's first token
             if (!PACKED || !(m.end & ((1u << j) - 1))) back.B = step(fwd.A, fwd.L, dy, back.B);
         }
@@ -199,43 +206,58 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
         }
         before = Slots::template carry_into<PACKED>(fwds, warp, lane, before);
 
-        // the state before every token
-        F h[kSeg];
+        F past0 = before;  // the state before the segment
+        if (PACKED && m.begin) {  // it only reaches the tokens before the first beginning
 #pragma unroll
-        for (int j = 0; j < kSeg; ++j) {
-            F in = x_of(j);
-            if constexpr (COMP) in = mul(decay_of<LOGIT>(gate_of(j)).u, in);
-            if (PACKED && (m.begin >> j & 1))
-                before = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
-            h[j] = before;
-            before = step(da[j], lo[V == 1 ? j : 0], before, in);
+            for (int j = 0; j < kSeg; ++j) {
+                if (!(m.begin & ((2u << j) - 1))) B[j] = step(P[j], Q[V == 1 ? j : 0], before, B[j]);
+                P[j] = splat<V>(0.f);
+                if constexpr (V == 1) Q[j] = P[j];
+            }
+            before = splat<V>(0.f);
         }
-        char* qdx = pdx + (t0 + kSeg - 1) * sdx;
-        char* qdg = pdg + (t0 + kSeg - 1) * sdg;
-#pragma unroll
-        for (int j = kSeg - 1; j >= 0; --j) {
+        // token j's gradients, from the last token to the first
+        auto gradients = [&](int j, F& dx, F& dg) {
             if (PACKED && (m.end >> j & 1))
                 e = state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j));
-            const F dh = add(P::get(rdy[j * 32]), e);
-            e = step(da[j], lo[V == 1 ? j : 0], dh, splat<V>(0.f));
-            F u, dx = dh, past = h[j];
-            if constexpr (COMP || LOGIT) u = decay_of<LOGIT>(gate_of(j)).u;
-            if constexpr (COMP) {
-                dx = mul(u, dh);
-                past = sub(past, x_of(j));
+            F past = j ? step(P[j ? j - 1 : 0], Q[V == 1 && j ? j - 1 : 0], before, B[j ? j - 1 : 0]) : past0;
+            if (PACKED && (m.begin >> j & 1))
+                past = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
+            Decay<V> r;
+            if constexpr (kHold) {
+                r.a = da[j];
+                r.lo = lo[V == 1 ? j : 0];
+                r.u = u[V == 1 && kUsesU ? j : 0];
+            } else {
+                r = decay_of<LOGIT>(gate_of(j));
             }
-            F dg = mul(e, past);
-            if constexpr (LOGIT) dg = mul(dg, u);
-            if (m.valid >> j & 1) {
-                store_row<T>(qdx + lane * 4, dx, whole, count);
-                store_row<T>(qdg + lane * 4, dg, whole, count);
-            }
-            qdx -= sdx;
-            qdg -= sdg;
+            const F dh = add(Pk::get(rdy[j * 32]), e);
+            e = step(r.a, r.lo, dh, splat<V>(0.f));
+            dx = COMP ? mul(r.u, dh) : dh;
+            if constexpr (COMP) past = sub(past, x_of(j));
+            dg = mul(e, past);
+            if constexpr (LOGIT) dg = mul(dg, r.u);
             if (PACKED && (m.begin >> j & 1)) {
                 const int s = __shfl_sync(0xffffffffu, m.seq, j);
                 if (a.dinit_state) store_floats<V>(a.dinit_state + (size_t)s * d + c, e, count);
             }
+        };
+        char* qdx = pdx + (t0 + kSeg - 1) * sdx + lane * 4;
+        char* qdg = pdg + (t0 + kSeg - 1) * sdg + lane * 4;
+        const bool plain = whole && m.valid == kAll;
+#pragma unroll
+        for (int j = kSeg - 1; j >= 0; --j) {
+            F dx, dg;
+            gradients(j, dx, dg);
+            if (plain) {
+                *reinterpret_cast<uint32_t*>(qdx) = Pk::put(dx);
+                *reinterpret_cast<uint32_t*>(qdg) = Pk::put(dg);
+            } else if (m.valid >> j & 1) {
+                store_row<T>(qdx, dx, whole, count);
+                store_row<T>(qdg, dg, whole, count);
+            }
+            qdx -= sdx;
+            qdg -= sdg;
         }
     }
     // the carry behind the first tile is the initial state's gradient, in every thread

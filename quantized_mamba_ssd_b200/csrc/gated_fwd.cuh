@@ -19,12 +19,12 @@ template <typename T, bool LOGIT, bool COMP, bool PACKED>
 __global__ void __launch_bounds__(kTileThreads, kFwdBlocks)
 scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
     constexpr int V = kChannels<T>;
-    using P = Pack<T>;
+    using Pk = Pack<T>;
     using F = Vec<V>;
     using Slots = MapSlots<V>;
     extern __shared__ __align__(128) uint8_t staged[];
-    __shared__ float seg_maps[2][kWarps * Slots::kFloats];
-    __shared__ float cta_maps[2][kMaxCluster * Slots::kFloats];
+    __shared__ __align__(16) float seg_maps[2][kWarps * Slots::kFloats];
+    __shared__ __align__(16) float cta_maps[2][kMaxCluster * Slots::kFloats];
 
     // the shuffle tells the compiler that the warp's index, and with it every row's address, is
     // the same in all lanes
@@ -79,12 +79,12 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
         stage(k + kFwdStages - 1);
         uint32_t* rx = reinterpret_cast<uint32_t*>(slot(k, 0)) + lane;
         uint32_t* rg = reinterpret_cast<uint32_t*>(slot(k, 1)) + lane;
-        if (m.valid != (1u << kSeg) - 1) {
+        if (m.valid != kAll) {
             // tokens of no sequence keep the state: x 0, decay 1 (each lane mends its own words)
             for (int j = 0; j < kSeg; ++j)
                 if (!(m.valid >> j & 1)) {
                     rx[j * 32] = 0;
-                    rg[j * 32] = LOGIT ? P::kInf : 0u;
+                    rg[j * 32] = LOGIT ? Pk::kInf : 0u;
                 }
         }
 
@@ -94,7 +94,7 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
             for (int v = 0; v < V; ++v) top_x[v] = top_g[v] = 0;
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
-                const F x = P::get(rx[j * 32]), g = P::get(rg[j * 32]);
+                const F x = Pk::get(rx[j * 32]), g = Pk::get(rg[j * 32]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     top_x[v] = max(top_x[v], __float_as_uint(fabsf(x[v])));
@@ -117,7 +117,7 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
                 if (!(m.valid >> j & 1)) continue;
-                const F x = P::get(rx[j * 32]), g = P::get(rg[j * 32]);
+                const F x = Pk::get(rx[j * 32]), g = Pk::get(rg[j * 32]);
                 int code[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) code[v] = code_of(x[v], inv_x[v]);
@@ -131,19 +131,21 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
             store_bytes<V>(a.gate_e + be, eg, whole_codes, count);
         }
 
-        // decays (and weighted inputs) of the segment, and its map
-        F da[kSeg], lo[V == 1 ? kSeg : 1], wx[COMP ? kSeg : 1];
+        // The state behind token j is P[j] carry + B[j] (P with its low part Q in fp32): from the
+        // carry on, the tokens do not depend on one another.
+        F P[kSeg], Q[V == 1 ? kSeg : 1], B[kSeg];
         Map<V> seg = identity_map<V>();
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
-            F in = P::get(rx[j * 32]);
-            const Decay<V> r = decay_of<LOGIT>(P::get(rg[j * 32]));
+            F in = Pk::get(rx[j * 32]);
+            const Decay<V> r = decay_of<LOGIT>(Pk::get(rg[j * 32]));
             if (PACKED && (m.begin >> j & 1)) seg.B = init_of(__shfl_sync(0xffffffffu, m.seq, j));
-            da[j] = r.a;
-            if constexpr (V == 1) lo[j] = r.lo;
-            if constexpr (COMP) wx[j] = in = mul(r.u, in);
+            if constexpr (COMP) in = mul(r.u, in);
             seg.B = step(r.a, r.lo, seg.B, in);
             extend(seg, r);
+            P[j] = seg.A;
+            B[j] = seg.B;
+            if constexpr (V == 1) Q[j] = seg.L;
         }
         if (PACKED && m.begin) seg.A = splat<V>(-1.f);
 
@@ -170,19 +172,35 @@ scan_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
             store_floats<V>(a.span_states + ((size_t)b * tiles + tile) * d + c,
                             none ? splat<V>(0.f) : h, count);
         }
-        char* qy = py + t0 * sy;
+        if (PACKED && m.begin) {  // the carry only reaches the tokens before the first beginning
 #pragma unroll
-        for (int j = 0; j < kSeg; ++j) {
-            F in;
-            if constexpr (COMP) in = wx[j];
-            else in = P::get(rx[j * 32]);
-            if (PACKED && (m.begin >> j & 1)) h = init_of(__shfl_sync(0xffffffffu, m.seq, j));
-            h = step(da[j], lo[V == 1 ? j : 0], h, in);
-            if (m.valid >> j & 1) store_row<T>(qy + lane * 4, h, whole, count);
-            qy += sy;
-            if (PACKED && (m.end >> j & 1)) {
-                const int s = __shfl_sync(0xffffffffu, m.seq, j);
-                if (a.final_state) store_floats<V>(a.final_state + (size_t)s * d + c, h, count);
+            for (int j = 0; j < kSeg; ++j) {
+                if (!(m.begin & ((2u << j) - 1))) B[j] = step(P[j], Q[V == 1 ? j : 0], h, B[j]);
+                P[j] = splat<V>(0.f);
+                if constexpr (V == 1) Q[j] = P[j];
+            }
+            h = splat<V>(0.f);
+        }
+        if (PACKED && m.end && a.final_state) {
+#pragma unroll
+            for (int j = 0; j < kSeg; ++j)
+                if (m.end >> j & 1)
+                    store_floats<V>(a.final_state + (size_t)__shfl_sync(0xffffffffu, m.seq, j) * d + c,
+                                    step(P[j], Q[V == 1 ? j : 0], h, B[j]), count);
+        }
+        char* qy = py + t0 * sy + lane * 4;
+        if (whole && m.valid == kAll) {
+#pragma unroll
+            for (int j = 0; j < kSeg; ++j) {
+                *reinterpret_cast<uint32_t*>(qy) = Pk::put(step(P[j], Q[V == 1 ? j : 0], h, B[j]));
+                qy += sy;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSeg; ++j) {
+                if (m.valid >> j & 1)
+                    store_row<T>(qy, step(P[j], Q[V == 1 ? j : 0], h, B[j]), whole, count);
+                qy += sy;
             }
         }
     }

@@ -17,6 +17,7 @@ namespace gated {
 
 constexpr int kWarps = 4;
 constexpr int kSeg = kBlock;               // tokens per warp: a checkpoint block stays in a thread
+constexpr uint32_t kAll = (1u << kSeg) - 1;  // every token of a segment
 constexpr int kTile = kWarps * kSeg;       // tokens per CTA and step
 constexpr int kTileThreads = 32 * kWarps;
 constexpr int kRowBytes = 128;             // a token's channels of one warp
@@ -238,56 +239,41 @@ __device__ __forceinline__ uint32_t remote_smem(const void* p, int rank) {
     return r;
 }
 
-__device__ __forceinline__ void store_remote(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void store_remote(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
 }
 
-// Maps of runs, [run][word][lane] with A, B (and L) of every channel as words of their own.
+// Maps of runs, [run][lane] as four floats each: A and B of two channels, or A, B and L of one.
 template <int V>
 struct MapSlots {
-    static constexpr int kWords = V == 1 ? 3 : 4;
-    static constexpr int kFloats = kWords * 32;  // per run
+    static constexpr int kFloats = 4 * 32;  // per run
 
+    static __device__ __forceinline__ float4 words(const Map<V>& m) {
+        if constexpr (V == 1) return make_float4(m.A.x, m.B.x, m.L.x, 0.f);
+        else return make_float4(m.A.x.x, m.A.x.y, m.B.x.x, m.B.x.y);
+    }
     static __device__ __forceinline__ void write(float* s, int run, int lane, const Map<V>& m) {
-        float* p = s + run * kFloats + lane;
-        if constexpr (V == 1) {
-            p[0] = m.A.x;
-            p[32] = m.B.x;
-            p[64] = m.L.x;
-        } else {
-            p[0] = m.A.x.x;
-            p[32] = m.A.x.y;
-            p[64] = m.B.x.x;
-            p[96] = m.B.x.y;
-        }
+        *reinterpret_cast<float4*>(s + run * kFloats + lane * 4) = words(m);
     }
     static __device__ __forceinline__ Map<V> read(const float* s, int run, int lane) {
-        const float* p = s + run * kFloats + lane;
+        const float4 w = *reinterpret_cast<const float4*>(s + run * kFloats + lane * 4);
         Map<V> m;
         if constexpr (V == 1) {
-            m.A.x = p[0];
-            m.B.x = p[32];
-            m.L.x = p[64];
+            m.A.x = w.x;
+            m.B.x = w.y;
+            m.L.x = w.z;
         } else {
-            m.A.x = make_float2(p[0], p[32]);
-            m.B.x = make_float2(p[64], p[96]);
+            m.A.x = make_float2(w.x, w.y);
+            m.B.x = make_float2(w.z, w.w);
             m.L = splat<V>(0.f);
         }
         return m;
     }
     static __device__ __forceinline__ void send(const float* s, int run, int lane, int rank,
                                                 const Map<V>& m) {
-        const uint32_t p = remote_smem(s + run * kFloats + lane, rank);
-        if constexpr (V == 1) {
-            store_remote(p, m.A.x);
-            store_remote(p + 128, m.B.x);
-            store_remote(p + 256, m.L.x);
-        } else {
-            store_remote(p, m.A.x.x);
-            store_remote(p + 128, m.A.x.y);
-            store_remote(p + 256, m.B.x.x);
-            store_remote(p + 384, m.B.x.y);
-        }
+        store_remote(remote_smem(s + run * kFloats + lane * 4, rank), words(m));
     }
     // The map of a whole tile: its warps' runs, written in the order of the recurrence.
     template <bool PACKED>
@@ -335,7 +321,7 @@ __device__ __forceinline__ Marks marks_of(const int32_t* __restrict__ cu, int ns
     Marks m;
     const int lane = threadIdx.x & 31;
     if (n == kSeg && t0 > held.from && t0 + kSeg < held.to) {
-        m.valid = (1u << kSeg) - 1;
+        m.valid = kAll;
         m.begin = m.end = 0;
         m.seq = held.seq;
         return m;
