@@ -14,38 +14,38 @@
 namespace ssd {
 namespace gated {
 
-// Staged inputs: x, gate and dy as rows of 128 bytes, or codes as rows of one byte per channel.
+// A warp's staged segment: x and gate (rows of 128 bytes, or codes, one byte per channel) and dy.
+template <typename T, bool CKPT> constexpr int kInRow = CKPT ? 32 * kChannels<T> : kRowBytes;
 template <typename T, bool CKPT>
-constexpr int kInRow = CKPT ? 32 * kChannels<T> : kRowBytes;
-template <typename T, bool CKPT>
-constexpr int kBwdStage = kTile * (2 * kInRow<T, CKPT> + kRowBytes);
-template <typename T, bool CKPT>
-constexpr int kBwdSmem = kBwdStages * kBwdStage<T, CKPT>;
+constexpr int kBwdSegBytes = 2 * kSubBytes<kInRow<T, CKPT>> + kSubBytes<kRowBytes>;
+constexpr int kSpanSegs = kSpan / kSub;
+constexpr int kBwdSlots = 2;
+// Segments from codes are smaller: 8 warps of them fit twice into an SM's shared memory, where of
+// full ones only 4 warps fit three times.
+template <bool CKPT> constexpr int kBwdWarps = CKPT ? 8 : 4;
+template <bool CKPT> constexpr int kBwdBlocks = CKPT ? 2 : 3;
+template <int V, int W> constexpr int kFwdMapBytes = 2 * W * MapSlots<V>::kFloats * 4;
 
 template <typename T, bool LOGIT, bool COMP, bool PACKED, bool CKPT>
-__global__ void __launch_bounds__(kTileThreads, kBwdBlocks)
-scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
-    constexpr int V = kChannels<T>;
-    constexpr int kRow = kInRow<T, CKPT>;
+__global__ void __launch_bounds__(32 * kBwdWarps<CKPT>, kBwdBlocks<CKPT>)
+scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
+    constexpr int V = kChannels<T>, kRow = kInRow<T, CKPT>;
+    constexpr bool kHold = COMP || LOGIT;  // the gradients need 1 - a
     using Pk = Pack<T>;
-    constexpr bool kUsesU = COMP || LOGIT;      // the gradients need 1 - a
-    constexpr bool kHold = V == 1 || !kUsesU;  // decays stay in registers; else they are computed again
     using F = Vec<V>;
-    using Slots = MapSlots<V>;
     extern __shared__ __align__(128) uint8_t staged[];
-    __shared__ __align__(16) float fwd_maps[2][kWarps * Slots::kFloats];
-    __shared__ __align__(16) float seg_maps[2][kWarps * Slots::kFloats];
-    __shared__ __align__(16) float cta_maps[2][kMaxCluster * Slots::kFloats];
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    constexpr int W = kBwdWarps<CKPT>;
     const int R = ta.cluster, rank = blockIdx.x % R, unit = blockIdx.x / R;
     const int d = a.channels, b = unit / ta.strips, c0 = unit % ta.strips * 32 * V;
     const int c = c0 + lane * V, count = max(0, min(V, d - c));
-    const bool whole = d - c0 >= 32 * V && ta.pair_out;
-    const int tiles = (a.seqlen + kTile - 1) / kTile, steps = (tiles + R - 1) / R;
+    const bool whole = d - c0 >= 32 * V && ta.whole_out;
+    const int tiles = (ta.blocks + W - 1) / W, steps = (tiles + R - 1) / R;
     const size_t row0 = (size_t)b * a.seqlen;
 
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
+    const int in_width = CKPT ? min(kRow, d - c0) : width;
     const char *px, *pg;
     long long sx, sg;
     if constexpr (CKPT) {
@@ -64,22 +64,19 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
     const long long sdy = a.dy.token_stride * sizeof(T), sdx = a.dx.token_stride * sizeof(T);
     const long long sdg = a.dgate.token_stride * sizeof(T);
 
-    // rows of step k: x, gate (or their codes), dy
-    auto slot = [&](int k, int tensor) {
-        return staged + (k % kBwdStages) * kBwdStage<T, CKPT> +
-               (tensor < 2 ? (tensor * kWarps + warp) * kSeg * kRow
-                           : 2 * kTile * kRow + warp * kSeg * kRowBytes);
-    };
+    // the gradient's maps meet; the state's only serve the warps of the same tile
+    Meeting<V, W>& meeting = *reinterpret_cast<Meeting<V, W>*>(staged);
+    float* fwds = reinterpret_cast<float*>(staged + kMeetingBytes<V, W>);
+    uint8_t* own = staged + kMeetingBytes<V, W> + kFwdMapBytes<V, W> + warp * kBwdSlots * kBwdSegBytes<T, CKPT>;
+    // tiles of W segments from the last one down, below 0: nothing left for this CTA
+    auto start = [&](int k) { return ((tiles - 1 - (k * R + rank)) * W + warp) * kSub; };
     auto stage = [&](int k) {
-        const int t0 = (tiles - 1 - (k * R + rank)) * kTile + warp * kSeg;
-        if (k < steps && t0 >= 0) {
-            const int n = max(0, min(kSeg, a.seqlen - t0));
-            const int in_width = CKPT ? min(kRow, d - c0) : width;
-            stage_rows<kRow>(slot(k, 0), n ? px + t0 * sx : px, sx, n, in_width,
-                             CKPT ? ta.align_codes : ta.align_x);
-            stage_rows<kRow>(slot(k, 1), n ? pg + t0 * sg : pg, sg, n, in_width,
-                             CKPT ? ta.align_codes : ta.align_gate);
-            stage_rows<kRowBytes>(slot(k, 2), n ? pdy + t0 * sdy : pdy, sdy, n, width, ta.align_dy);
+        const int t = start(k), n = t < 0 ? 0 : max(0, min(kSub, a.seqlen - t));
+        if (k < steps && n > 0) {
+            uint8_t* to = own + k % kBwdSlots * kBwdSegBytes<T, CKPT>;
+            stage_rows<kRow>(to, px + t * sx, sx, n, in_width, ta.align_x);
+            stage_rows<kRow>(to + kSubBytes<kRow>, pg + t * sg, sg, n, in_width, ta.align_gate);
+            stage_rows<kRowBytes>(to + 2 * kSubBytes<kRow>, pdy + t * sdy, sdy, n, width, ta.align_dy);
         }
         copy_commit();
     };
@@ -89,23 +86,20 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
 
     F carry = PACKED ? splat<V>(0.f) : state_of(a.dfinal_state, b);
     if (PACKED && a.dinit_state && rank == 0)  // sequences without a token
-        for (int s = warp; s < a.nseq; s += kWarps)
+        for (int s = warp; s < a.nseq; s += W)
             if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
                 store_floats<V>(a.dinit_state + (size_t)s * d + c, state_of(a.dfinal_state, s), count);
     Held held;
-#pragma unroll
-    for (int k = 0; k < kBwdStages - 1; ++k) stage(k);
+    stage(0);
     for (int k = 0; k < steps; ++k) {
-        const int tile = tiles - 1 - (k * R + rank);  // below 0: nothing left for this CTA
-        const int t0 = tile * kTile + warp * kSeg;
-        const int n = tile < 0 ? 0 : max(0, min(kSeg, a.seqlen - t0));
+        const int t0 = start(k), n = t0 < 0 ? 0 : max(0, min(kSub, a.seqlen - t0));
         Marks m;
         m.valid = (1u << n) - 1;
         m.begin = m.end = 0;
         if constexpr (PACKED) m = marks_of(a.cu, a.nseq, t0, n, held);
-        // the state before the tile, then before this warp's segment
+        // the state before the segment's span, then before the segment
         F before = load_floats<V>(
-            tile >= 0 ? a.span_states + ((size_t)b * tiles + tile) * d + c : nullptr, count);
+            n > 0 ? a.span_states + ((size_t)b * ta.spans + t0 / kSpan) * d + c : nullptr, count);
         F scale_x, scale_g;
         if constexpr (CKPT) {
             const size_t be = ((size_t)b * ta.blocks + t0 / kBlock) * d + c;
@@ -115,16 +109,20 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
                 scale_g.set(v, n > 0 && v < count ? scale_of(__ldg(a.gate_e + be + v)) : 0.f);
             }
         }
-        copy_wait<kBwdStages - 2>();
+        copy_wait<kBwdSlots - 2>();
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
-        stage(k + kBwdStages - 1);
-        uint8_t* rx = slot(k, 0) + lane * (kRow / 32);
-        uint8_t* rg = slot(k, 1) + lane * (kRow / 32);
-        uint32_t* rdy = reinterpret_cast<uint32_t*>(slot(k, 2)) + lane;
-        if (m.valid != kAll) {
+        stage(k + kBwdSlots - 1);
+        uint8_t* here = own + k % kBwdSlots * kBwdSegBytes<T, CKPT>;
+        if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRow>(here, px + t0 * sx, sx);
+        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRow>(here + kSubBytes<kRow>, pg + t0 * sg, sg);
+        if (ta.align_dy < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + 2 * kSubBytes<kRow>, pdy + t0 * sdy, sdy);
+        uint8_t* rx = here + lane * (kRow / 32);
+        uint8_t* rg = rx + kSubBytes<kRow>;
+        uint32_t* rdy = reinterpret_cast<uint32_t*>(here + 2 * kSubBytes<kRow>) + lane;
+        if (m.valid != kAll) [[unlikely]] {
             // tokens of no sequence pass state and gradient on: x and dy 0, decay 1 (each lane
             // mends its own words)
-            for (int j = 0; j < kSeg; ++j)
+            for (int j = 0; j < kSub; ++j)
                 if (!(m.valid >> j & 1)) {
                     rdy[j * 32] = 0;
                     if constexpr (CKPT) {
@@ -137,12 +135,16 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
                 }
         }
         auto decoded = [&](const uint8_t* r, F scale, int j) {
-            if constexpr (CKPT) {
+            if constexpr (CKPT && V == 2) {
+                // code + 128 in the low byte of 2^23 is that number as a float; times a power of
+                // two, and less (2^23 + 128) of it, the value, all exact
+                const uint32_t q = *reinterpret_cast<const uint16_t*>(r + j * kRow) ^ 0x8080u;
                 F f;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    f.set(v, static_cast<float>(reinterpret_cast<const int8_t*>(r)[j * kRow + v]));
-                return mul(f, scale);
+                f.x = make_float2(__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7440)),
+                                  __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7441)));
+                return fma(f, scale, mul(scale, splat<V>(-8388736.f)));
+            } else if constexpr (CKPT) {
+                return mul(F{static_cast<float>(*reinterpret_cast<const int8_t*>(r + j * kRow))}, scale);
             } else {
                 return Pk::get(*reinterpret_cast<const uint32_t*>(r + j * kRow));
             }
@@ -155,110 +157,108 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
             return g;
         };
 
-        // The segment's maps, both in one pass: of the state, which behind token j is P[j] carry +
-        // B[j] (P with its low part Q in fp32), and of the gradient, which from behind the segment
-        // reaches its first token through the product of the decays and from token j through P[j].
-        F P[kSeg], Q[V == 1 ? kSeg : 1], B[kSeg];
-        F da[kHold ? kSeg : 1], lo[V == 1 ? kSeg : 1], u[V == 1 && kUsesU ? kSeg : 1];
+        // The segment's maps, both in one pass: of the state, and of the gradient, which from behind
+        // the segment reaches its first token through the product of the decays and from token j
+        // through the product up to j.  Where the gradients only need the decays, the state behind
+        // token j is kept as the product P[j] and the rest B[j], which together with the carry give
+        // it at once; where they need 1 - a as well, decays and 1 - a are kept instead and the
+        // states computed again (both together do not fit the registers of three CTAs).
+        F P[kHold ? 1 : kSub], Q[kHold || V == 2 ? 1 : kSub], B[kHold ? 1 : kSub];
+        F da[kSub], lo[V == 1 ? kSub : 1], u[kHold ? kSub : 1];
         Map<V> fwd = identity_map<V>(), back = identity_map<V>();
+        // segments inside one sequence, by far the most, go without the checks of every token
+        const bool inside = !PACKED || !(m.begin | m.end);
+        auto maps = [&](auto checks) {
+            constexpr bool CHECK = decltype(checks)::value;
 #pragma unroll
-        for (int j = 0; j < kSeg; ++j) {
-            F in = x_of(j), dy = Pk::get(rdy[j * 32]);
-            const Decay<V> r = decay_of<LOGIT>(gate_of(j));
-            if (PACKED && (m.begin >> j & 1))
-                fwd.B = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
-            if (PACKED && (m.end >> j & 1))
-                dy = add(dy, state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j)));
-            if constexpr (kHold) da[j] = r.a;
-            if constexpr (V == 1) lo[j] = r.lo;
-            if constexpr (V == 1 && kUsesU) u[j] = r.u;
-            if constexpr (COMP) in = mul(r.u, in);
-            fwd.B = step(r.a, r.lo, fwd.B, in);
-            extend(fwd, r);
-            P[j] = fwd.A;
-            B[j] = fwd.B;
-            if constexpr (V == 1) Q[j] = fwd.L;
-            // behind the first end nothing reaches the segment's first token
-            if (!PACKED || !(m.end & ((1u << j) - 1))) back.B = step(fwd.A, fwd.L, dy, back.B);
-        }
+            for (int j = 0; j < kSub; ++j) {
+                F in = x_of(j), dy = Pk::get(rdy[j * 32]);
+                const Decay<V> r = decay_of<LOGIT>(gate_of(j));
+                if (CHECK && (m.begin >> j & 1))
+                    fwd.B = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
+                if (CHECK && (m.end >> j & 1))
+                    dy = add(dy, state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j)));
+                da[j] = r.a;
+                if constexpr (V == 1) lo[j] = r.lo;
+                if constexpr (kHold) u[j] = r.u;
+                if constexpr (COMP) in = mul(r.u, in);
+                fwd.B = step(r.a, r.lo, fwd.B, in);
+                extend(fwd, r);
+                if constexpr (!kHold) {
+                    P[j] = fwd.A;
+                    B[j] = fwd.B;
+                    if constexpr (V == 1) Q[j] = fwd.L;
+                }
+                // behind the first end nothing reaches the segment's first token
+                if (!CHECK || !(m.end & ((1u << j) - 1))) back.B = step(fwd.A, fwd.L, dy, back.B);
+            }
+        };
+        if (inside) [[likely]] maps(std::false_type{});
+        else maps(std::true_type{});
         back.A = PACKED && m.end ? splat<V>(-1.f) : fwd.A;
         back.L = fwd.L;
         if (PACKED && m.begin) fwd.A = splat<V>(-1.f);
 
-        float* segs = seg_maps[k & 1];
-        float* fwds = fwd_maps[k & 1];
-        const int order = kWarps - 1 - warp;  // place of this warp's run
-        F e;                                  // the gradient from behind this segment
-        Slots::write(segs, order, lane, back);
-        Slots::write(fwds, warp, lane, fwd);
-        __syncthreads();
-        if (R > 1) {
-            float* ctas = cta_maps[k & 1];
-            if (warp == 0) {
-                const Map<V> all = Slots::template join_runs<PACKED>(segs, lane);
-                for (int r = 0; r < R; ++r) Slots::send(ctas, rank, lane, r, all);
-            }
-            cluster_barrier(warp == 0);
-            e = Slots::template carry_through<PACKED>(ctas, R, rank, lane, carry);
-            e = Slots::template carry_into<PACKED>(segs, order, lane, e);
-        } else {
-            e = Slots::template carry_through<PACKED>(segs, kWarps, order, lane, carry);
-        }
-        before = Slots::template carry_into<PACKED>(fwds, warp, lane, before);
+        float* states = fwds + (k & 1) * W * MapSlots<V>::kFloats;
+        MapSlots<V>::write(states, warp, lane, fwd);
+        // the gradient from behind the segment
+        F e = meeting.template meet<PACKED>(k, W - 1 - warp, R, rank, back, carry);
+        // (the spans of a tile begin at multiples of kSpanSegs warps)
+        const Map<V> into = MapSlots<V>::template join_runs<PACKED, W>(
+            states, warp - warp % kSpanSegs, warp, lane);
+        before = through<PACKED>(into, before);
 
-        F past0 = before;  // the state before the segment
-        if (PACKED && m.begin) {  // it only reaches the tokens before the first beginning
+        char* qdx = pdx + (t0 + kSub - 1) * sdx + lane * 4;
+        char* qdg = pdg + (t0 + kSub - 1) * sdg + lane * 4;
+        auto gradients = [&](auto checks) {
+            constexpr bool CHECK = decltype(checks)::value;
+            // what the gradient of token j's decay multiplies: h_{j-1}, or h_{j-1} - x_j
+            F past[kSub];
 #pragma unroll
-            for (int j = 0; j < kSeg; ++j) {
-                if (!(m.begin & ((2u << j) - 1))) B[j] = step(P[j], Q[V == 1 ? j : 0], before, B[j]);
-                P[j] = splat<V>(0.f);
-                if constexpr (V == 1) Q[j] = P[j];
+            for (int j = 0; j < kSub; ++j) {
+                const bool begins = CHECK && (m.begin >> j & 1);
+                if constexpr (kHold) {
+                    F in = x_of(j);
+                    if (begins) before = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
+                    past[j] = COMP ? sub(before, in) : before;
+                    if constexpr (COMP) in = mul(u[j], in);
+                    before = step(da[j], lo[V == 1 ? j : 0], before, in);
+                } else {
+                    constexpr int none = 0;
+                    const int i = j ? j - 1 : none;
+                    if (begins) past[j] = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
+                    else if (!j) past[j] = before;
+                    else if (CHECK && (m.begin & ((1u << j) - 1))) past[j] = B[i];  // the carry ends there
+                    else past[j] = step(P[i], Q[V == 1 ? i : 0], before, B[i]);
+                }
             }
-            before = splat<V>(0.f);
-        }
-        // token j's gradients, from the last token to the first
-        auto gradients = [&](int j, F& dx, F& dg) {
-            if (PACKED && (m.end >> j & 1))
-                e = state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j));
-            F past = j ? step(P[j ? j - 1 : 0], Q[V == 1 && j ? j - 1 : 0], before, B[j ? j - 1 : 0]) : past0;
-            if (PACKED && (m.begin >> j & 1))
-                past = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
-            Decay<V> r;
-            if constexpr (kHold) {
-                r.a = da[j];
-                r.lo = lo[V == 1 ? j : 0];
-                r.u = u[V == 1 && kUsesU ? j : 0];
-            } else {
-                r = decay_of<LOGIT>(gate_of(j));
-            }
-            const F dh = add(Pk::get(rdy[j * 32]), e);
-            e = step(r.a, r.lo, dh, splat<V>(0.f));
-            dx = COMP ? mul(r.u, dh) : dh;
-            if constexpr (COMP) past = sub(past, x_of(j));
-            dg = mul(e, past);
-            if constexpr (LOGIT) dg = mul(dg, r.u);
-            if (PACKED && (m.begin >> j & 1)) {
-                const int s = __shfl_sync(0xffffffffu, m.seq, j);
-                if (a.dinit_state) store_floats<V>(a.dinit_state + (size_t)s * d + c, e, count);
+            const bool plain = whole && m.valid == kAll;
+#pragma unroll
+            for (int j = kSub - 1; j >= 0; --j) {
+                if (CHECK && (m.end >> j & 1))
+                    e = state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j));
+                const F dh = add(Pk::get(rdy[j * 32]), e);
+                e = step(da[j], lo[V == 1 ? j : 0], dh, splat<V>(0.f));
+                const F dx = COMP ? mul(u[kHold ? j : 0], dh) : dh;
+                F dg = mul(e, past[j]);
+                if constexpr (LOGIT) dg = mul(dg, u[kHold ? j : 0]);
+                if (CHECK && (m.begin >> j & 1)) {
+                    const int s = __shfl_sync(0xffffffffu, m.seq, j);
+                    if (a.dinit_state) store_floats<V>(a.dinit_state + (size_t)s * d + c, e, count);
+                }
+                if (plain) {
+                    *reinterpret_cast<uint32_t*>(qdx) = Pk::put(dx);
+                    *reinterpret_cast<uint32_t*>(qdg) = Pk::put(dg);
+                } else if (m.valid >> j & 1) {
+                    store_row<T>(qdx, dx, whole, count);
+                    store_row<T>(qdg, dg, whole, count);
+                }
+                qdx -= sdx;
+                qdg -= sdg;
             }
         };
-        char* qdx = pdx + (t0 + kSeg - 1) * sdx + lane * 4;
-        char* qdg = pdg + (t0 + kSeg - 1) * sdg + lane * 4;
-        const bool plain = whole && m.valid == kAll;
-#pragma unroll
-        for (int j = kSeg - 1; j >= 0; --j) {
-            F dx, dg;
-            gradients(j, dx, dg);
-            if (plain) {
-                *reinterpret_cast<uint32_t*>(qdx) = Pk::put(dx);
-                *reinterpret_cast<uint32_t*>(qdg) = Pk::put(dg);
-            } else if (m.valid >> j & 1) {
-                store_row<T>(qdx, dx, whole, count);
-                store_row<T>(qdg, dg, whole, count);
-            }
-            qdx -= sdx;
-            qdg -= sdg;
-        }
+        if (inside) [[likely]] gradients(std::false_type{});
+        else gradients(std::true_type{});
     }
     // the carry behind the first tile is the initial state's gradient, in every thread
     if (!PACKED && a.dinit_state && rank == 0 && warp == 0)
@@ -267,12 +267,17 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const TileArgs ta) {
 
 template <typename T, bool LOGIT>
 cudaError_t dispatch_bwd(const GatedArgs& a, cudaStream_t st) {
-    auto go = [&](auto comp, auto packed, auto ckpt) {
-        constexpr bool C = decltype(comp)::value, K = decltype(packed)::value, Q = decltype(ckpt)::value;
-        return launch_tiles<T>(scan_bwd_kernel<T, LOGIT, C, K, Q>, a, kBwdBlocks, kBwdSmem<T, Q>, st);
-    };
     using Y = std::true_type;
     using N = std::false_type;
+    TileArgs t = tile_args<T>(a);
+    auto go = [&](auto comp, auto packed, auto ckpt) {
+        constexpr bool C = decltype(comp)::value, K = decltype(packed)::value, Q = decltype(ckpt)::value;
+        constexpr int bytes = kBwdSegBytes<T, Q>;
+        constexpr int W = kBwdWarps<Q>;
+        t.cluster = cluster_size((long long)t.strips * a.batch, t.blocks, W, kBwdBlocks<Q>);
+        return launch_strips(scan_bwd_kernel<T, LOGIT, C, K, Q>, a, t, W,
+                             kMeetingBytes<kChannels<T>, W> + kFwdMapBytes<kChannels<T>, W> + W * kBwdSlots * bytes, st);
+    };
     auto packed = [&](auto comp, auto ckpt) { return a.cu ? go(comp, Y{}, ckpt) : go(comp, N{}, ckpt); };
     auto input = [&](auto ckpt) { return a.complement ? packed(Y{}, ckpt) : packed(N{}, ckpt); };
     return a.x_q ? input(Y{}) : input(N{});

@@ -1,4 +1,4 @@
-// Launches of the tile kernels: alignments, and how many CTAs share a strip.
+// Launches of the scan kernels: alignments, and how many warps share a strip.
 #pragma once
 
 #include <cmath>
@@ -8,18 +8,14 @@
 namespace ssd {
 namespace gated {
 
-constexpr int kFwdBlocks = 4;  // resident CTAs per SM the kernels are compiled for
-constexpr int kBwdBlocks = 3;
-constexpr int kFwdStages = 2;  // segments in shared memory per warp: the current one and the next
-constexpr int kBwdStages = 2;
-
 struct TileArgs {
     int cluster;  // CTAs per strip
-    int strips;   // strips of 32 lanes per row
+    int strips;   // strips per row
     int blocks;   // checkpoint blocks per row
-    // what the start of every row is a multiple of (bytes): 16, 4, 2 or 1
-    int align_x, align_gate, align_dy, align_codes;
-    int pair_out, pair_codes;  // outputs can be written as whole words (codes: pairs of bytes)
+    int spans;    // spans per row
+    // what the start of every row is a multiple of (bytes): 16, 4 or less
+    int align_x, align_gate, align_dy;
+    int whole_out, whole_codes;  // outputs can be written as whole words (codes: pairs of bytes)
 };
 
 inline int alignment(const GatedRows& r, int elem) {
@@ -31,9 +27,27 @@ inline int alignment(const GatedRows& r, int elem) {
 
 inline bool word_rows(const GatedRows& r, int elem) { return !r.ptr || alignment(r, elem) >= 4; }
 
-// CTAs per strip.  Every CTA of a strip runs for as long as the strip does, so what counts is how
-// full the last wave of CTAs is; among equals the smallest cluster wins (fewest to wait for).
-inline int cluster_size(long long units, int tiles, int blocks_per_sm) {
+template <typename T>
+TileArgs tile_args(const GatedArgs& a) {
+    constexpr int elem = sizeof(T), V = kChannels<T>;
+    TileArgs t{};
+    t.strips = (a.channels + 32 * V - 1) / (32 * V);
+    t.spans = (a.seqlen + kSpan - 1) / kSpan;
+    t.blocks = (a.seqlen + kBlock - 1) / kBlock;
+    t.align_x = alignment(a.x, elem);
+    t.align_gate = alignment(a.gate, elem);
+    t.align_dy = alignment(a.dy, elem);
+    t.whole_out = word_rows(a.y, elem) && word_rows(a.dx, elem) && word_rows(a.dgate, elem);
+    auto all = [](auto... p) { return (reinterpret_cast<uintptr_t>(p) | ...); };
+    if (a.x_q && !a.x.ptr) {  // backward from codes, rows of one byte per channel
+        t.align_x = alignment({a.x_q, 0, a.channels}, 1);
+        t.align_gate = alignment({a.gate_q, 0, a.channels}, 1);
+    }
+    t.whole_codes = (all(a.x_q, a.gate_q, a.x_e, a.gate_e) | a.channels) % 2 == 0;
+    return t;
+}
+
+inline int sm_count() {
     static const int sms = [] {
         int dev = 0, n = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -41,42 +55,46 @@ inline int cluster_size(long long units, int tiles, int blocks_per_sm) {
             n = 148;
         return n;
     }();
-    const double room = (double)sms * blocks_per_sm;
+    return sms;
+}
+
+// CTAs per strip, the R with the least waves(R) * steps(R) * (1 + the meeting's share of a step).
+// Every CTA of a strip stays for as long as the strip takes, so waves of CTAs count whole.  A
+// cluster's meeting adds 0.2 + 0.08 R of a step (measured on strips of 20011 and 65521 tokens: a
+// step of 1.5 us alone grows to 1.9 with 2 CTAs, 2.7 with 8, 4.5 with 16), so with strips for all
+// SMs R = 1 is best (256 strips of 2048 bf16 tokens: 38 us with 1, 46 with 2, 54 with 3), with
+// fewer a larger one (80 strips: 239, 237, 177 us, and 251 with 4, whose CTAs need two waves; 16
+// strips: 1373 us with 1, 296 with 8, 214 with 12, 244 with 16).
+inline int cluster_size(long long strips, int segments, int warps, int per_sm) {
+    const double room = (double)sm_count() * per_sm;
+    const int tiles = (segments + warps - 1) / warps;
+    const int most = warps == 8 ? 12 : kMaxCluster;  // (clusters of 96 warps or fewer find their place)
     int best = 1;
-    double most = 0;
-    for (int r = 1; r <= kMaxCluster && (r == 1 || r <= tiles); ++r) {
-        const double waves = units * r / room;
-        const double full = waves <= 1 ? waves : waves / std::ceil(waves);
-        if (full > most * 1.02) {
-            most = full;
+    double least = 0;
+    for (int r = 1; r <= most && r <= tiles; ++r) {
+        const double cost = std::ceil(strips * r / room) * ((tiles + r - 1) / r) *
+                            (r > 1 ? 1.2 + 0.08 * r : 1.0);
+        if (r == 1 || cost < 0.97 * least) {
+            least = cost;
             best = r;
         }
     }
     return best;
 }
 
-template <typename T, typename K>
-cudaError_t launch_tiles(K kernel, const GatedArgs& a, int blocks_per_sm, int smem, cudaStream_t st) {
-    constexpr int elem = sizeof(T), V = kChannels<T>;
-    const int tiles = (a.seqlen + kTile - 1) / kTile;
-    TileArgs t{};
-    t.strips = (a.channels + 32 * V - 1) / (32 * V);
-    t.blocks = (a.seqlen + kBlock - 1) / kBlock;
-    const long long units = (long long)t.strips * a.batch;
-    t.cluster = cluster_size(units, tiles, blocks_per_sm);
-    t.align_x = alignment(a.x, elem);
-    t.align_gate = alignment(a.gate, elem);
-    t.align_dy = alignment(a.dy, elem);
-    t.pair_out = word_rows(a.y, elem) && word_rows(a.dx, elem) && word_rows(a.dgate, elem);
-    const uintptr_t codes = reinterpret_cast<uintptr_t>(a.x_q) | reinterpret_cast<uintptr_t>(a.gate_q) |
-                            a.channels;
-    t.align_codes = codes % 16 == 0 ? 16 : codes % 4 == 0 ? 4 : codes % 2 == 0 ? 2 : 1;
-    t.pair_codes = (codes | reinterpret_cast<uintptr_t>(a.x_e) | reinterpret_cast<uintptr_t>(a.gate_e)) % 2 == 0;
+// One launch of `warps` warps per CTA and t.cluster CTAs per strip.
+template <typename K>
+cudaError_t launch_strips(K kernel, const GatedArgs& a, const TileArgs& t, int warps, int smem,
+                          cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    if (t.cluster > 8) {  // beyond the portable size
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * t.cluster));
-    cfg.blockDim = dim3(kTileThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>((long long)t.strips * a.batch * t.cluster));
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr{};

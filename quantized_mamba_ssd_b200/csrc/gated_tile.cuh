@@ -1,13 +1,17 @@
-// What the forward and the backward scan share: the tile, the joins of its parts, the loads.
+// What the forward and the backward scan share: the walk along a strip, the joins of its parts, the
+// copies.
 //
-// A cluster of R CTAs takes one strip of 32 * V channels of one row and walks its tokens in steps
-// of R tiles, one tile of 64 tokens per CTA, one segment of 16 tokens per warp, V channels per
-// lane.  A thread reduces its segment to the affine map carry -> A carry + B; the maps of a tile
-// meet in shared memory, those of a step are sent to every CTA of the cluster (distributed shared
-// memory), and each thread then computes the carry into its own segment and, redundantly, the
-// carry into the next step.  So a step costs one cluster barrier, every input is read once, no
-// CTA waits on memory flags, and the order of all sums is fixed.
+// A strip is the channels of 32 lanes (128 bytes of a token).  W warps of each of R CTAs of a
+// cluster share a strip and walk it in steps of W R segments of 16 tokens: each warp reduces its
+// segment to the affine map carry -> A carry + B, the maps meet in shared memory (with R > 1 those
+// of whole CTAs are sent to every CTA of the cluster, through distributed shared memory), and each
+// warp then computes the carry into its own segment - and, redundantly, the carry into the next
+// step.  Inputs are copied ahead asynchronously, each warp's own segments into its own shared
+// memory.  So every input is read once, no CTA waits on memory flags, and the order of all sums is
+// fixed.
 #pragma once
+
+#include <type_traits>
 
 #include "gated.cuh"
 #include "gated_kernels.h"
@@ -15,14 +19,10 @@
 namespace ssd {
 namespace gated {
 
-constexpr int kWarps = 4;
-constexpr int kSeg = kBlock;               // tokens per warp: a checkpoint block stays in a thread
-constexpr uint32_t kAll = (1u << kSeg) - 1;  // every token of a segment
-constexpr int kTile = kWarps * kSeg;       // tokens per CTA and step
-constexpr int kTileThreads = 32 * kWarps;
-constexpr int kRowBytes = 128;             // a token's channels of one warp
-constexpr int kMaxCluster = 8;
-static_assert(kTile == kSpan, "the backward starts every tile from a saved state");
+constexpr int kSub = kBlock;                 // tokens of a segment: one checkpoint block
+constexpr uint32_t kAll = (1u << kSub) - 1;  // each of them
+constexpr int kRowBytes = 128;  // a token's channels of one warp
+constexpr int kMaxCluster = 16;  // (above 8: not on every part, but on this one)
 
 // ---------------------------------------------------------------------------------------
 // the channels of one token and lane: one 32-bit word, so that a warp's row is 128 bytes
@@ -70,18 +70,6 @@ __device__ __forceinline__ void store_row(char* p, Vec<kChannels<T>> f, bool who
     }
 }
 
-template <int V>
-__device__ __forceinline__ void store_bytes(uint8_t* p, const int (&q)[V], bool whole, int count) {
-    if (V == 2 && whole) {
-        *reinterpret_cast<uint16_t*>(p) =
-            static_cast<uint16_t>((q[0] & 0xff) | (q[V - 1] & 0xff) << 8);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (v < count) p[v] = static_cast<uint8_t>(q[v]);
-    }
-}
-
 // Floats of the lane's channels; 0 from a null pointer and for channels that do not exist.
 template <int V>
 __device__ __forceinline__ Vec<V> load_floats(const float* p, int count) {
@@ -99,7 +87,7 @@ __device__ __forceinline__ void store_floats(float* p, Vec<V> f, int count) {
 }
 
 // ---------------------------------------------------------------------------------------
-// asynchronous copies of a warp's segment, kSeg rows of W bytes, into its own shared memory
+// asynchronous copies of kSub rows of W bytes into a warp's own shared memory
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -113,62 +101,169 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int b
                  : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+template <int AHEAD> __device__ __forceinline__ void copy_wait() {  // all but the last AHEAD commits
+    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
 }
 
-// Rows at src + j * pitch (bytes); rows from `rows` on and bytes from `width` on become 0 and are
-// not read.  `align` is what base and pitch are multiples of: 16, 4, or less.
+// Room for kSub rows: the rows, and behind them one more word of each for rows that start inside
+// a word.
+template <int W> constexpr int kSubBytes = kSub * W + kSub * 4;
+
+// Rows at src + j * pitch (bytes); rows from `rows` on and bytes from `width` on become 0.  Where
+// base and pitch are multiples of 16 (`align`) the pieces are 16 bytes, else words, and where they
+// are not multiples of 4 either the words are those that hold the rows' bytes: realign_rows, once
+// they are here, moves each row to the start of its place.  Nothing but words that hold bytes of
+// the rows is read.
+template <int W>
+__device__ __noinline__ void stage_rows_any(uint32_t to, const char* src, long long pitch, int rows,
+                                            int width, int align) {
+    const int lane = threadIdx.x & 31;
+    if (align == 16) {
+        constexpr int kPer = W / 16, kStep = 32 / kPer;
+        const int row = lane / kPer, at = lane % kPer * 16;
+        for (int i = 0; i < kSub; i += kStep) {
+            const int bytes = row + i < rows ? max(0, min(16, width - at)) : 0;
+            copy_async16(to + (row + i) * W + at, bytes ? src + (row + i) * pitch + at : src, bytes);
+        }
+        return;
+    }
+    constexpr int kPer = W / 4, kStep = 32 / kPer;
+    const int row = lane / kPer, at = lane % kPer * 4;
+    const char* none = src - (reinterpret_cast<uintptr_t>(src) & 3);  // an address for copies of nothing
+#pragma unroll 4
+    for (int i = 0; i < kSub; i += kStep) {
+        const char* p = src + (row + i) * pitch;
+        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+        const int bytes = row + i < rows ? max(0, min(4, shift + width - at)) : 0;
+        copy_async4(to + (row + i) * W + at, bytes ? p - shift + at : none, bytes);
+    }
+    if (align < 4 && lane < kSub) {
+        const char* p = src + lane * pitch;
+        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+        const int bytes = lane < rows ? max(0, min(4, shift + width - W)) : 0;
+        copy_async4(to + kSub * W + lane * 4, bytes ? p - shift + W : none, bytes);
+    }
+}
+
 template <int W>
 __device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int rows,
                                            int width, int align) {
-    const int lane = threadIdx.x & 31;
-    char* to = static_cast<char*>(dst);
-    if (align == 16) {
-        constexpr int kPer = W / 16;   // pieces per row
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if (align == 16 && rows == kSub && width >= W) [[likely]] {
+        constexpr int kPer = W / 16;      // pieces per row
         constexpr int kStep = 32 / kPer;  // rows per instruction
-        const int row = lane / kPer, at = lane % kPer * 16;
-        const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(to)) + row * W + at;
+        const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
+        const uint32_t d = to + row * W + at;
         const char* p = src + row * pitch + at;
-        if (rows == kSeg && width >= W) {
 #pragma unroll
-            for (int i = 0; i < kSeg / kStep; ++i) {
-                copy_async16(d + i * kStep * W, p);
-                p += kStep * pitch;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kSeg / kStep; ++i) {
-                const int bytes = row + i * kStep < rows ? max(0, min(16, width - at)) : 0;
-                copy_async16(d + i * kStep * W, bytes ? p : src, bytes);
-                p += kStep * pitch;
-            }
-        }
-    } else if (align == 4) {
-        constexpr int kPer = W / 4;
-#pragma unroll
-        for (int i = 0; i < kSeg * kPer / 32; ++i) {
-            const int row = (lane + 32 * i) / kPer, at = (lane + 32 * i) % kPer * 4;
-            const int bytes = row < rows ? max(0, min(4, width - at)) : 0;
-            copy_async4(static_cast<uint32_t>(__cvta_generic_to_shared(to + row * W + at)),
-                        bytes ? src + row * pitch + at : src, bytes);
-        }
-    } else if (align == 2) {
-        constexpr int kPer = W / 2;
-#pragma unroll 16
-        for (int i = 0; i < kSeg * kPer / 32; ++i) {
-            const int row = (lane + 32 * i) / kPer, at = (lane + 32 * i) % kPer * 2;
-            const bool in = row < rows && at < width;
-            *reinterpret_cast<uint16_t*>(to + row * W + at) =
-                in ? __ldg(reinterpret_cast<const uint16_t*>(src + row * pitch + at)) : uint16_t(0);
+        for (int i = 0; i < kSub / kStep; ++i) {
+            copy_async16(d + i * kStep * W, p);
+            p += kStep * pitch;
         }
     } else {
-#pragma unroll 16
-        for (int i = 0; i < kSeg * W / 32; ++i) {
-            const int row = (lane + 32 * i) / W, at = (lane + 32 * i) % W;
-            const bool in = row < rows && at < width;
-            to[row * W + at] = in ? __ldg(src + row * pitch + at) : char(0);
+        // out of line: code that is not run would push the hot loop out of the instruction cache
+        stage_rows_any<W>(to, src, pitch, rows, width, align);
+    }
+}
+
+// After the copies of rows that are not aligned to words (align < 4): the same rows, moved.
+template <int W>
+__device__ __noinline__ void realign_rows(void* dst, const char* src, long long pitch) {
+    constexpr int kPer = W / 4, kStep = 32 / kPer;
+    const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer;
+    uint32_t* w = static_cast<uint32_t*>(dst);
+#pragma unroll 4
+    for (int i = 0; i < kSub / kStep; ++i) {
+        const int r = row + i * kStep;
+        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src + r * pitch) & 3);
+        const uint32_t lo = w[r * kPer + at];
+        uint32_t hi = __shfl_down_sync(0xffffffffu, lo, 1, kPer);
+        if (at == kPer - 1) hi = w[kSub * kPer + r];
+        w[r * kPer + at] = __funnelshift_r(lo, hi, 8 * shift);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------------------------------
+// 8-bit codes of one checkpoint block of every lane's channels, from the staged rows
+// ---------------------------------------------------------------------------------------
+// 16-bit values stay pairs: limits, magnitudes and their maximum are two-wide instructions on
+// them (all exact: 16 and 127 scales are numbers of the type; 127 scales of a subnormal fp16 block
+// round to within its numbers' distance, which no value of the block lies between).
+template <typename T> __device__ __forceinline__ auto both(float a, float b) {
+    if constexpr (std::is_same<T, __half>::value) return __floats2half2_rn(a, b);
+    else return __floats2bfloat162_rn(a, b);
+}
+
+template <typename T, bool GATE, bool LOGIT>
+__device__ __forceinline__ void code_rows(const uint32_t* r, uint32_t valid, int8_t* q, uint8_t* e,
+                                          int d, bool whole, int count) {
+    constexpr int V = kChannels<T>;
+    uint8_t* out = reinterpret_cast<uint8_t*>(q);
+    if constexpr (V == 1) {
+        auto held = [&](int j) {
+            const float v = __uint_as_float(r[j * 32]);
+            return GATE ? held_gate<LOGIT>(v) : v;
+        };
+        uint32_t top = 0;  // bits of the magnitudes: their order, NaN on top
+#pragma unroll 4
+        for (int j = 0; j < kSub; ++j)
+            if (valid >> j & 1) top = max(top, __float_as_uint(fabsf(held(j))));
+        const uint32_t ex = scale_exp(top);
+        const float inv = inv_scale_of(ex);
+#pragma unroll 4
+        for (int j = 0; j < kSub; ++j, out += d)
+            if ((valid >> j & 1) && count) *out = static_cast<uint8_t>(code_of(held(j), inv));
+        if (count) *e = static_cast<uint8_t>(ex);
+    } else {
+        using H2 = decltype(both<T>(0.f, 0.f));
+        auto pair = [&](int j) {
+            const uint32_t w = r[j * 32];
+            return *reinterpret_cast<const H2*>(&w);
+        };
+        auto held = [&](H2 v) {
+            if constexpr (GATE) v = __hmax2_nan(v, both<T>(-16.f, -16.f));
+            if constexpr (GATE && LOGIT) v = __hmin2_nan(v, both<T>(16.f, 16.f));
+            return v;
+        };
+        H2 top = both<T>(0.f, 0.f);
+        if (valid == kAll) {
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) top = __hmax2_nan(top, __habs2(held(pair(j))));
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kSub; ++j)
+                if (valid >> j & 1) top = __hmax2_nan(top, __habs2(held(pair(j))));
         }
+        const uint32_t e0 = scale_exp(__float_as_uint(static_cast<float>(top.x)) & 0x7fffffffu);
+        const uint32_t e1 = scale_exp(__float_as_uint(static_cast<float>(top.y)) & 0x7fffffffu);
+        Vec<2> inv;
+        inv.x = make_float2(inv_scale_of(e0), inv_scale_of(e1));
+        const H2 most = both<T>(e0 == kExpNaN ? 0.f : 127.f * scale_of(e0),
+                                e1 == kExpNaN ? 0.f : 127.f * scale_of(e1));
+        const H2 least = __hneg2(most);
+        // 1.5 * 2^23 + the exact product, rounded once to an integer: its low byte is the code
+        const Vec<2> magic = splat<2>(12582912.f);
+        auto code = [&](int j) {
+            const H2 v = __hmax2(__hmin2(held(pair(j)), most), least);
+            const Vec<2> f = fma(Pack<T>::get(*reinterpret_cast<const uint32_t*>(&v)), inv, magic);
+            return __byte_perm(__float_as_uint(f.x.x), __float_as_uint(f.x.y), 0x0040) & 0xffffu;
+        };
+        if (valid == kAll && whole) {
+#pragma unroll
+            for (int j = 0; j < kSub; ++j, out += d)
+                *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(code(j));
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kSub; ++j, out += d) {
+                if (!(valid >> j & 1)) continue;
+                const uint32_t w = code(j);
+                if (count > 0) out[0] = static_cast<uint8_t>(w);
+                if (count > 1) out[1] = static_cast<uint8_t>(w >> 8);
+            }
+        }
+        if (count > 0) e[0] = static_cast<uint8_t>(e0);
+        if (count > 1) e[1] = static_cast<uint8_t>(e1);
     }
 }
 
@@ -223,11 +318,14 @@ __device__ __forceinline__ Map<V> join(const Map<V>& first, const Map<V>& second
 // ---------------------------------------------------------------------------------------
 // clusters
 // ---------------------------------------------------------------------------------------
-// All threads of all CTAs of the cluster meet.  Only the threads that sent maps release: a release
-// waits for every write the thread has in flight, its rows of the last step included.
-__device__ __forceinline__ void cluster_barrier(bool sent) {
+// All threads of all CTAs of the cluster meet: arrive, then wait.  Only the threads that sent maps
+// release: a release waits for every write the thread has in flight, its rows of the last step
+// included.
+__device__ __forceinline__ void cluster_arrive(bool sent) {
     if (sent) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -271,45 +369,88 @@ struct MapSlots {
         }
         return m;
     }
-    static __device__ __forceinline__ void send(const float* s, int run, int lane, int rank,
-                                                const Map<V>& m) {
-        store_remote(remote_smem(s + run * kFloats + lane * 4, rank), words(m));
-    }
-    // The map of a whole tile: its warps' runs, written in the order of the recurrence.
-    template <bool PACKED>
-    static __device__ __forceinline__ Map<V> join_runs(const float* s, int lane) {
-        Map<V> all = read(s, 0, lane);
+    // The map of runs `from` to `to` - 1 of N; the loads do not wait for the joins.
+    template <bool PACKED, int N>
+    static __device__ __forceinline__ Map<V> join_runs(const float* s, int from, int to, int lane) {
+        Map<V> m[N];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) all = join<PACKED>(all, read(s, i, lane));
+        for (int i = 0; i < N; ++i) m[i] = read(s, i, lane);
+        Map<V> all = identity_map<V>();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i >= from && i < to) all = join<PACKED>(all, m[i]);
         return all;
     }
-    // `carry` through runs 0 .. n - 1; returns what run `which` receives.
-    template <bool PACKED>
+    // `carry` through runs 0 .. n - 1 <= N; returns what run `which` receives.
+    template <bool PACKED, int N>
     static __device__ __forceinline__ Vec<V> carry_through(const float* s, int n, int which,
                                                            int lane, Vec<V>& carry) {
         Vec<V> mine = carry;
-        for (int i = 0; i < n; ++i) {
-            if (i == which) mine = carry;
-            carry = through<PACKED>(read(s, i, lane), carry);
+#pragma unroll
+        for (int g = 0; g < N; g += 8) {
+            if (g >= n) break;
+            Map<V> m[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (g + i < N) m[i] = read(s, g + i, lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (g + i >= N || g + i >= n) break;
+                if (g + i == which) mine = carry;
+                carry = through<PACKED>(m[i], carry);
+            }
         }
         return mine;
     }
-    // h through the runs before `to`
+};
+
+// Where the parts of a step meet: the maps of the CTA's warps and, sent by every CTA of the
+// cluster, those of whole tiles.  Two of each, used in turn: a buffer is written again two steps
+// later, when the step between has seen every reader past it.
+template <int V, int W>
+struct Meeting {
+    using Slots = MapSlots<V>;
+    float segs[2][W * Slots::kFloats];
+    float tiles[2][kMaxCluster * Slots::kFloats];
+
+    // Every warp of the cluster gives the map of its part and gets the carry into it; `carry` goes
+    // on to the next step.  `order`: the warp's place in the recurrence (0 first).
     template <bool PACKED>
-    static __device__ __forceinline__ Vec<V> carry_into(const float* s, int to, int lane, Vec<V> h) {
-        for (int i = 0; i < to; ++i) h = through<PACKED>(read(s, i, lane), h);
-        return h;
+    __device__ __forceinline__ Vec<V> meet(int k, int order, int R, int rank, const Map<V>& part,
+                                           Vec<V>& carry) {
+        const int lane = threadIdx.x & 31;
+        float* seg = segs[k & 1];
+        float* tile = tiles[k & 1];
+        Slots::write(seg, order, lane, part);
+        __syncthreads();
+        if (R == 1) return Slots::template carry_through<PACKED, W>(seg, W, order, lane, carry);
+        const bool sends = order == W - 1;
+        Map<V> before;  // from the tile's start to this warp's part
+        if (sends) {
+            before = Slots::template join_runs<PACKED, W>(seg, 0, W - 1, lane);
+            const Map<V> all = join<PACKED>(before, part);
+            for (int r = 0; r < R; ++r)
+                store_remote(remote_smem(tile + rank * Slots::kFloats + lane * 4, r), Slots::words(all));
+        }
+        cluster_arrive(sends);
+        if (!sends) before = Slots::template join_runs<PACKED, W>(seg, 0, order, lane);
+        cluster_wait();
+        const Vec<V> mine = Slots::template carry_through<PACKED, kMaxCluster>(tile, R, rank, lane, carry);
+        return through<PACKED>(before, mine);
     }
 };
+
+template <int V, int W>
+constexpr int kMeetingBytes = (sizeof(Meeting<V, W>) + 127) / 128 * 128;
 
 // ---------------------------------------------------------------------------------------
 // where the tokens of a segment stand in packed rows
 // ---------------------------------------------------------------------------------------
-// Bit j is token t0 + j.  `held` keeps the bounds of the last sequence met: a segment inside it
-// needs no search.
+// Bit j is token t0 + j.  `held` keeps the bounds of the last sequence met: tokens inside it
+// need no search.
 struct Marks {
     uint32_t valid, begin, end;  // in a sequence; its first token; its last token
-    int seq;                     // lane j < kSeg: the sequence of token t0 + j
+    int seq;                     // lane j < kSub: the sequence of token t0 + j
 };
 
 struct Held {
@@ -320,7 +461,7 @@ __device__ __forceinline__ Marks marks_of(const int32_t* __restrict__ cu, int ns
                                           Held& held) {
     Marks m;
     const int lane = threadIdx.x & 31;
-    if (n == kSeg && t0 > held.from && t0 + kSeg < held.to) {
+    if (n == kSub && t0 > held.from && t0 + kSub < held.to) {
         m.valid = kAll;
         m.begin = m.end = 0;
         m.seq = held.seq;
@@ -339,8 +480,8 @@ __device__ __forceinline__ Marks marks_of(const int32_t* __restrict__ cu, int ns
     m.begin = __ballot_sync(0xffffffffu, s >= 0 && t == from);
     m.end = __ballot_sync(0xffffffffu, s >= 0 && t + 1 == to);
     m.seq = s;
-    // the sequence of the segment's middle token is as good a guess as any for the next segment
-    const int src = kSeg / 2;
+    // the sequence of the middle token is as good a guess as any for the next ones
+    const int src = kSub / 2;
     held.seq = __shfl_sync(0xffffffffu, s, src);
     held.from = __shfl_sync(0xffffffffu, from, src);
     held.to = __shfl_sync(0xffffffffu, to, src);
