@@ -1,7 +1,10 @@
 // 8-bit activation checkpoints: blocks of 16 tokens of one channel as int8 codes with one
 // power-of-two scale, and back.
-#include "gated.cuh"
-#include "gated_kernels.h"
+//
+// Pure streaming.  A thread takes the 16 tokens of a few neighbouring channels, so that a block
+// never leaves it: 16 independent loads in flight, the largest magnitude and the codes in
+// registers, 16 stores.
+#include "gated_tile.cuh"
 
 namespace ssd {
 
@@ -11,61 +14,191 @@ using namespace gated;
 
 constexpr int kThreads = 128;
 
-template <typename T>
+// Channels of a thread: 8 bytes of a 16-bit or fp32 row, or one channel where the rows do not allow
+// that (their starts or the codes' are not multiples of 8 bytes / as many channels).
+template <typename T, bool WIDE> constexpr int kGroup = WIDE ? 8 / sizeof(T) : 1;
+
+template <int N> struct Word;
+template <> struct Word<1> { using U = uint8_t; };
+template <> struct Word<2> { using U = uint16_t; };
+template <> struct Word<4> { using U = uint32_t; };
+template <> struct Word<8> { using U = uint2; };
+
+// N values of type T as one load or store
+template <typename T, int N> union Values {
+    typename Word<N * sizeof(T)>::U word;
+    T v[N];
+    __device__ Values() {}
+};
+
+// Two neighbouring 16-bit channels of a block, word `k` of the thread's rows.
+template <typename T> struct Pair {
+    using H2 = decltype(both<T>(0.f, 0.f));
+    uint32_t e0, e1;
+    H2 most;
+    Vec<2> inv;
+    static __device__ __forceinline__ H2 as(uint32_t w) { return *reinterpret_cast<const H2*>(&w); }
+    __device__ __forceinline__ Pair(const Values<T, 4> (&in)[kBlock], int k) {
+        H2 top = both<T>(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) top = __hmax2_nan(top, __habs2(as(k ? in[j].word.y : in[j].word.x)));
+        block_scales<T>(top, e0, e1, most, inv);
+    }
+    __device__ __forceinline__ uint32_t codes(uint32_t w) const { return block_codes<T>(as(w), most, inv); }
+};
+
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
-pack_kernel(GatedRows x, int seqlen, int d, int8_t* __restrict__ q, uint8_t* __restrict__ e) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= d) return;
+pack_kernel(GatedRows x, int batch, int seqlen, int d, int8_t* __restrict__ q,
+            uint8_t* __restrict__ e) {
+    constexpr int N = kGroup<T, WIDE>;
+    const int groups = d / N, chunks = (groups + kThreads - 1) / kThreads;
     const int blocks = (seqlen + kBlock - 1) / kBlock;
-    const int b = blockIdx.y / blocks, t0 = blockIdx.y % blocks * kBlock;
-    const int n = min(kBlock, seqlen - t0);
-    const T* src = static_cast<const T*>(x.ptr) + b * x.batch_stride + t0 * x.token_stride + c;
-    uint32_t top = 0;
-    for (int j = 0; j < n; ++j)
-        top = max(top, __float_as_uint(fabsf(static_cast<float>(src[j * x.token_stride]))));
-    const uint32_t ex = scale_exp(top);
-    const float inv = inv_scale_of(ex);
-    int8_t* dst = q + ((size_t)b * seqlen + t0) * d + c;
-    for (int j = 0; j < n; ++j)
-        dst[(size_t)j * d] = static_cast<int8_t>(code_of(static_cast<float>(src[j * x.token_stride]), inv));
-    e[(size_t)blockIdx.y * d + c] = static_cast<uint8_t>(ex);
+    const long long work = (long long)batch * blocks * chunks;
+    for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+        const long long row = w / chunks;  // one block of one batch row
+        const int g = static_cast<int>(w % chunks) * kThreads + threadIdx.x;
+        if (g >= groups) continue;
+        const int b = static_cast<int>(row / blocks), t0 = static_cast<int>(row % blocks) * kBlock;
+        const int n = min(kBlock, seqlen - t0), c = g * N;
+        const T* src = static_cast<const T*>(x.ptr) + b * x.batch_stride + t0 * x.token_stride + c;
+        Values<T, N> in[kBlock];
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) {
+            if (j < n) {
+                in[j].word = *reinterpret_cast<const decltype(in[j].word)*>(src + j * x.token_stride);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) in[j].v[i] = static_cast<T>(0.f);
+            }
+        }
+        Values<uint8_t, N> ex;
+        int8_t* dst = q + ((size_t)b * seqlen + t0) * d + c;
+        if constexpr (sizeof(T) == 2 && N == 4) {  // pairs stay pairs
+            Pair<T> lo(in, 0), hi(in, 1);
+            ex.v[0] = lo.e0;
+            ex.v[1] = lo.e1;
+            ex.v[2] = hi.e0;
+            ex.v[3] = hi.e1;
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j) {
+                if (j >= n) break;
+                *reinterpret_cast<uint32_t*>(dst + (size_t)j * d) =
+                    __byte_perm(lo.codes(in[j].word.x), hi.codes(in[j].word.y), 0x5410);
+            }
+        } else {
+            Values<int8_t, N> out[kBlock];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                uint32_t top = 0;  // bits of the magnitudes: their order, NaN on top
+#pragma unroll
+                for (int j = 0; j < kBlock; ++j)
+                    top = max(top, __float_as_uint(fabsf(static_cast<float>(in[j].v[i]))));
+                const uint32_t s = scale_exp(top);
+                ex.v[i] = static_cast<uint8_t>(s);
+                const Coder coder(s);
+#pragma unroll
+                for (int j = 0; j < kBlock; ++j)
+                    out[j].v[i] = static_cast<int8_t>(coder.code(static_cast<float>(in[j].v[i])));
+            }
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j) {
+                if (j >= n) break;
+                *reinterpret_cast<decltype(out[j].word)*>(dst + (size_t)j * d) = out[j].word;
+            }
+        }
+        *reinterpret_cast<decltype(ex.word)*>(e + (size_t)row * d + c) = ex.word;
+    }
+}
+
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads)
+unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, int batch, int seqlen,
+              int d, T* __restrict__ x) {
+    constexpr int N = kGroup<T, WIDE>;
+    const int groups = d / N, chunks = (groups + kThreads - 1) / kThreads;
+    const int blocks = (seqlen + kBlock - 1) / kBlock;
+    const long long work = (long long)batch * blocks * chunks;
+    for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+        const long long row = w / chunks;
+        const int g = static_cast<int>(w % chunks) * kThreads + threadIdx.x;
+        if (g >= groups) continue;
+        const int b = static_cast<int>(row / blocks), t0 = static_cast<int>(row % blocks) * kBlock;
+        const int n = min(kBlock, seqlen - t0), c = g * N;
+        const size_t at = ((size_t)b * seqlen + t0) * d + c;
+        Values<int8_t, N> in[kBlock];
+        Values<uint8_t, N> ex;
+        ex.word = *reinterpret_cast<const decltype(ex.word)*>(e + (size_t)row * d + c);
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j)
+            if (j < n) in[j].word = *reinterpret_cast<const decltype(in[j].word)*>(q + at + (size_t)j * d);
+        float scale[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) scale[i] = scale_of(ex.v[i]);
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) {
+            if (j >= n) break;
+            Values<T, N> out;
+#pragma unroll
+            for (int i = 0; i < N; ++i) out.v[i] = static_cast<T>(scale[i] * in[j].v[i]);
+            *reinterpret_cast<decltype(out.word)*>(x + at + (size_t)j * d) = out.word;
+        }
+    }
+}
+
+unsigned grid_of(int batch, int seqlen, int groups) {
+    const long long blocks = (seqlen + kBlock - 1) / kBlock;
+    const long long work = batch * blocks * ((groups + kThreads - 1) / kThreads);
+    return static_cast<unsigned>(work < (1 << 30) ? work : 1 << 30);
+}
+
+bool multiple(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+template <typename T>
+cudaError_t pack_as(const GatedRows& x, int batch, int seqlen, int d, int8_t* q, uint8_t* e,
+                    cudaStream_t st) {
+    constexpr int N = kGroup<T, true>;
+    const bool wide = d % N == 0 && multiple(x.ptr, 8) && x.batch_stride % N == 0 &&
+                      x.token_stride % N == 0 && multiple(q, N) && multiple(e, N);
+    if (wide)
+        pack_kernel<T, true><<<grid_of(batch, seqlen, d / N), kThreads, 0, st>>>(x, batch, seqlen, d, q, e);
+    else
+        pack_kernel<T, false><<<grid_of(batch, seqlen, d), kThreads, 0, st>>>(x, batch, seqlen, d, q, e);
+    return cudaGetLastError();
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, int seqlen, int d,
-              T* __restrict__ x) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= d) return;
-    const int blocks = (seqlen + kBlock - 1) / kBlock;
-    const int b = blockIdx.y / blocks, t0 = blockIdx.y % blocks * kBlock;
-    const int n = min(kBlock, seqlen - t0);
-    const float scale = scale_of(e[(size_t)blockIdx.y * d + c]);
-    const size_t at = ((size_t)b * seqlen + t0) * d + c;
-    for (int j = 0; j < n; ++j) x[at + (size_t)j * d] = static_cast<T>(scale * q[at + (size_t)j * d]);
+cudaError_t unpack_as(const int8_t* q, const uint8_t* e, int batch, int seqlen, int d, void* x,
+                      cudaStream_t st) {
+    constexpr int N = kGroup<T, true>;
+    T* out = static_cast<T*>(x);
+    if (d % N == 0 && multiple(x, 8) && multiple(q, N) && multiple(e, N))
+        unpack_kernel<T, true><<<grid_of(batch, seqlen, d / N), kThreads, 0, st>>>(q, e, batch, seqlen, d, out);
+    else
+        unpack_kernel<T, false><<<grid_of(batch, seqlen, d), kThreads, 0, st>>>(q, e, batch, seqlen, d, out);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt_pack(const GatedRows& x, int batch, int seqlen, int d, int io_dtype,
                              int8_t* q, uint8_t* e, cudaStream_t st) {
-    const dim3 grid((d + kThreads - 1) / kThreads, batch * ((seqlen + kBlock - 1) / kBlock));
-    if (io_dtype == SSD_IO_F32) pack_kernel<float><<<grid, kThreads, 0, st>>>(x, seqlen, d, q, e);
-    else if (io_dtype == SSD_IO_F16) pack_kernel<__half><<<grid, kThreads, 0, st>>>(x, seqlen, d, q, e);
-    else pack_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(x, seqlen, d, q, e);
-    return cudaGetLastError();
+    switch (io_dtype) {
+        case SSD_IO_F32: return pack_as<float>(x, batch, seqlen, d, q, e, st);
+        case SSD_IO_F16: return pack_as<__half>(x, batch, seqlen, d, q, e, st);
+        case SSD_IO_BF16: return pack_as<__nv_bfloat16>(x, batch, seqlen, d, q, e, st);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 cudaError_t launch_ckpt_unpack(const int8_t* q, const uint8_t* e, int batch, int seqlen, int d,
                                int io_dtype, void* x, cudaStream_t st) {
-    const dim3 grid((d + kThreads - 1) / kThreads, batch * ((seqlen + kBlock - 1) / kBlock));
-    if (io_dtype == SSD_IO_F32)
-        unpack_kernel<<<grid, kThreads, 0, st>>>(q, e, seqlen, d, static_cast<float*>(x));
-    else if (io_dtype == SSD_IO_F16)
-        unpack_kernel<<<grid, kThreads, 0, st>>>(q, e, seqlen, d, static_cast<__half*>(x));
-    else
-        unpack_kernel<<<grid, kThreads, 0, st>>>(q, e, seqlen, d, static_cast<__nv_bfloat16*>(x));
-    return cudaGetLastError();
+    switch (io_dtype) {
+        case SSD_IO_F32: return unpack_as<float>(q, e, batch, seqlen, d, x, st);
+        case SSD_IO_F16: return unpack_as<__half>(q, e, batch, seqlen, d, x, st);
+        case SSD_IO_BF16: return unpack_as<__nv_bfloat16>(q, e, batch, seqlen, d, x, st);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace ssd

@@ -9,24 +9,62 @@ using namespace gated;
 
 constexpr int kThreads = 128;
 
-template <typename T, bool LOGIT>
+// One token, in place: x, gate and the state are read, y and the state written.  A thread takes four
+// elements, 16 bytes of the state; the end that does not fill four, and tensors that do not start
+// at a multiple of theirs, go element by element.
+template <typename T, bool LOGIT, bool WIDE>
 __global__ void __launch_bounds__(kThreads) step_kernel(const GatedStepArgs a) {
-    constexpr int V = kChannels<T>;
-    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * V;
+    constexpr int V = kChannels<T>, N = WIDE ? 4 : V;
+    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * N;
     if (i >= a.count) return;
-    const int n = static_cast<int>(a.count - i < V ? a.count - i : V);
-    Vec<V> g = splat<V>(0.f), x = g, h = g;
-    for (int v = 0; v < n; ++v) {
-        g.set(v, static_cast<float>(static_cast<const T*>(a.gate)[i + v]));
-        x.set(v, static_cast<float>(static_cast<const T*>(a.x)[i + v]));
-        h.set(v, a.state[i + v]);
+    const T* x = static_cast<const T*>(a.x) + i;
+    const T* gate = static_cast<const T*>(a.gate) + i;
+    T* y = static_cast<T*>(a.y) + i;
+    float* state = a.state + i;
+    auto next = [&](Vec<V> h, Vec<V> in, Vec<V> g) {
+        const Decay<V> r = decay_of<LOGIT>(g);
+        if (a.complement) in = mul(r.u, in);
+        return step(r.a, r.lo, h, in);
+    };
+    if (WIDE && a.count - i >= 4) {
+        struct alignas(4 * sizeof(T)) Four { uint32_t w[4 / V]; };
+        const Four fx = *reinterpret_cast<const Four*>(x), fg = *reinterpret_cast<const Four*>(gate);
+        float4 h = *reinterpret_cast<const float4*>(state);
+        Four out;
+        if constexpr (V == 1) {
+            float* p = &h.x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                p[k] = next({p[k]}, Pack<T>::get(fx.w[k]), Pack<T>::get(fg.w[k])).x;
+                out.w[k] = __float_as_uint(p[k]);
+            }
+        } else {
+            Vec<V> lo, hi;
+            lo.x = make_float2(h.x, h.y);
+            hi.x = make_float2(h.z, h.w);
+            lo = next(lo, Pack<T>::get(fx.w[0]), Pack<T>::get(fg.w[0]));
+            hi = next(hi, Pack<T>::get(fx.w[1]), Pack<T>::get(fg.w[1]));
+            out.w[0] = Pack<T>::put(lo);
+            out.w[1] = Pack<T>::put(hi);
+            h = make_float4(lo[0], lo[1], hi[0], hi[1]);
+        }
+        *reinterpret_cast<float4*>(state) = h;
+        *reinterpret_cast<Four*>(y) = out;
+        return;
     }
-    const Decay<V> r = decay_of<LOGIT>(g);
-    if (a.complement) x = mul(r.u, x);
-    h = step(r.a, r.lo, h, x);
-    for (int v = 0; v < n; ++v) {
-        a.state[i + v] = h[v];
-        static_cast<T*>(a.y)[i + v] = static_cast<T>(h[v]);
+    for (long long k = 0; k < N && k < a.count - i; k += V) {
+        const int n = static_cast<int>(a.count - i - k < V ? a.count - i - k : V);
+        Vec<V> g = splat<V>(0.f), in = g, h = g;
+        for (int v = 0; v < n; ++v) {
+            g.set(v, static_cast<float>(gate[k + v]));
+            in.set(v, static_cast<float>(x[k + v]));
+            h.set(v, state[k + v]);
+        }
+        h = next(h, in, g);
+        for (int v = 0; v < n; ++v) {
+            state[k + v] = h[v];
+            y[k + v] = static_cast<T>(h[v]);
+        }
     }
 }
 
@@ -57,9 +95,15 @@ cudaError_t launch_gated_scan_bwd(const GatedArgs& a, cudaStream_t st) {
 cudaError_t launch_gated_step(const GatedStepArgs& a, cudaStream_t st) {
     return by_type(a.io_dtype, [&](auto zero) {
         using T = decltype(zero);
-        constexpr int per = kThreads * kChannels<T>;
-        const long long grid = (a.count + per - 1) / per;
-        (a.logit ? step_kernel<T, true> : step_kernel<T, false>)<<<(unsigned)grid, kThreads, 0, st>>>(a);
+        const uintptr_t halves = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gate) |
+                                 reinterpret_cast<uintptr_t>(a.y);
+        const bool wide = halves % (4 * sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+        const int per = kThreads * (wide ? 4 : kChannels<T>);
+        const unsigned grid = static_cast<unsigned>((a.count + per - 1) / per);
+        if (wide)
+            (a.logit ? step_kernel<T, true, true> : step_kernel<T, false, true>)<<<grid, kThreads, 0, st>>>(a);
+        else
+            (a.logit ? step_kernel<T, true, false> : step_kernel<T, false, false>)<<<grid, kThreads, 0, st>>>(a);
         return cudaGetLastError();
     });
 }

@@ -195,6 +195,24 @@ template <typename T> __device__ __forceinline__ auto both(float a, float b) {
     else return __floats2bfloat162_rn(a, b);
 }
 
+// Two channels' scale exponents, 127 scales as pairs of T, and the factors of their codes.
+template <typename T, typename H2>
+__device__ __forceinline__ void block_scales(H2 top, uint32_t& e0, uint32_t& e1, H2& most, Vec<2>& inv) {
+    e0 = scale_exp(__float_as_uint(static_cast<float>(top.x)) & 0x7fffffffu);
+    e1 = scale_exp(__float_as_uint(static_cast<float>(top.y)) & 0x7fffffffu);
+    const Coder c0(e0), c1(e1);
+    inv.x = make_float2(c0.inv, c1.inv);
+    most = both<T>(e0 == kExpNaN ? 0.f : 127.f * scale_of(e0), e1 == kExpNaN ? 0.f : 127.f * scale_of(e1));
+}
+
+// The codes of two channels in the low bytes of a word.
+template <typename T, typename H2>
+__device__ __forceinline__ uint32_t block_codes(H2 v, H2 most, Vec<2> inv) {
+    v = __hmax2(__hmin2(v, most), __hneg2(most));
+    const Vec<2> f = fma(Pack<T>::get(*reinterpret_cast<const uint32_t*>(&v)), inv, splat<2>(kCodeMagic));
+    return __byte_perm(__float_as_uint(f.x.x), __float_as_uint(f.x.y), 0x0040) & 0xffffu;
+}
+
 template <typename T, bool GATE, bool LOGIT>
 __device__ __forceinline__ void code_rows(const uint32_t* r, uint32_t valid, int8_t* q, uint8_t* e,
                                           int d, bool whole, int count) {
@@ -210,10 +228,10 @@ __device__ __forceinline__ void code_rows(const uint32_t* r, uint32_t valid, int
         for (int j = 0; j < kSub; ++j)
             if (valid >> j & 1) top = max(top, __float_as_uint(fabsf(held(j))));
         const uint32_t ex = scale_exp(top);
-        const float inv = inv_scale_of(ex);
+        const Coder coder(ex);
 #pragma unroll 4
         for (int j = 0; j < kSub; ++j, out += d)
-            if ((valid >> j & 1) && count) *out = static_cast<uint8_t>(code_of(held(j), inv));
+            if ((valid >> j & 1) && count) *out = static_cast<uint8_t>(coder.code(held(j)));
         if (count) *e = static_cast<uint8_t>(ex);
     } else {
         using H2 = decltype(both<T>(0.f, 0.f));
@@ -235,20 +253,11 @@ __device__ __forceinline__ void code_rows(const uint32_t* r, uint32_t valid, int
             for (int j = 0; j < kSub; ++j)
                 if (valid >> j & 1) top = __hmax2_nan(top, __habs2(held(pair(j))));
         }
-        const uint32_t e0 = scale_exp(__float_as_uint(static_cast<float>(top.x)) & 0x7fffffffu);
-        const uint32_t e1 = scale_exp(__float_as_uint(static_cast<float>(top.y)) & 0x7fffffffu);
+        uint32_t e0, e1;
+        H2 most;
         Vec<2> inv;
-        inv.x = make_float2(inv_scale_of(e0), inv_scale_of(e1));
-        const H2 most = both<T>(e0 == kExpNaN ? 0.f : 127.f * scale_of(e0),
-                                e1 == kExpNaN ? 0.f : 127.f * scale_of(e1));
-        const H2 least = __hneg2(most);
-        // 1.5 * 2^23 + the exact product, rounded once to an integer: its low byte is the code
-        const Vec<2> magic = splat<2>(12582912.f);
-        auto code = [&](int j) {
-            const H2 v = __hmax2(__hmin2(held(pair(j)), most), least);
-            const Vec<2> f = fma(Pack<T>::get(*reinterpret_cast<const uint32_t*>(&v)), inv, magic);
-            return __byte_perm(__float_as_uint(f.x.x), __float_as_uint(f.x.y), 0x0040) & 0xffffu;
-        };
+        block_scales<T>(top, e0, e1, most, inv);
+        auto code = [&](int j) { return block_codes<T>(held(pair(j)), most, inv); };
         if (valid == kAll && whole) {
 #pragma unroll
             for (int j = 0; j < kSub; ++j, out += d)

@@ -65,6 +65,8 @@ class SSDError(RuntimeError):
 def library() -> ctypes.CDLL:
     """Load ``libssd_i8.so`` (built by ``quantized_mamba_ssd_b200.build``) and declare types."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -512,6 +514,15 @@ def ssd_i8_chunk_scan_noalloc_status(stream=None) -> None:
 _IO_CODES = {t: code for code, t in IO_DTYPES.values()}
 
 
+def _raw_stream_of(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# handle of the current stream of GPU `dev`, without the Stream object around it (1.2 us of a
+# 9 us decode step) where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream_of)
+
+
 class GatedCkpt(NamedTuple):
     """8-bit checkpoints of x and gate: int8 codes of the tensors' shape and uint8 exponents with
     ceil(l / 16) in the place of the token dim (``ssd_i8_gated_ckpt_empty`` allocates one)."""
@@ -522,23 +533,40 @@ class GatedCkpt(NamedTuple):
     gate_e: torch.Tensor
 
 
-def _call(name: str, first: torch.Tensor, run, stream):
-    """``run(raw stream)``, a library call, with ``first``'s GPU as the current device.  Outputs
-    that ``run`` allocates belong to the stream the kernels run on."""
+def _gpu_of(first) -> int:
+    """Index of the GPU that a call's first tensor lives on."""
     if not isinstance(first, torch.Tensor) or not first.is_cuda:
         raise ValueError("the library's tensors must be CUDA tensors")
-    dev = first.get_device()
-    if stream is None:
-        if torch.cuda.current_device() == dev:
-            return run(torch.cuda.current_stream().cuda_stream)
-        with torch.cuda.device(dev):
-            return run(torch.cuda.current_stream().cuda_stream)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    if stream.device.index != dev:
-        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{dev}")
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        return run(stream.cuda_stream)
+    return first.get_device()
+
+
+@contextlib.contextmanager
+def _on(dev: int, stream):
+    """``dev`` as the current device and, if given, ``stream`` (a torch stream or a raw handle) as
+    the current stream: outputs that a call allocates then belong to the stream it runs on."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _refuse(t, name: str, dtype: torch.dtype, shape: tuple, dev: int, what: str):
+    """Why a tensor does not fit the call."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}{what}")
 
 
 def _flat(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
@@ -546,71 +574,63 @@ def _flat(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple
     """Pointer of a contiguous tensor on GPU ``dev`` (None passes)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev, " must be contiguous")
 
 
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> tuple:
     """Pointer, batch stride and token stride of [b, l, d] or [T, d] rows on GPU ``dev`` whose
     channels are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1 and t.numel():
-        raise ValueError(f"{name}: the channels (last dim) must be contiguous")
-    return t.data_ptr(), (st[0] if len(st) == 3 else 0), st[-2]
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev):
+        st = t.stride()
+        if st[-1] == 1 or shape[-1] <= 1 or not t.numel():
+            return t.data_ptr(), (st[0] if len(st) == 3 else 0), st[-2]
+    _refuse(t, name, dtype, shape, dev, ": the channels (last dim) must be contiguous")
 
 
-def _gated_shape(t: torch.Tensor, name: str, cu_seqlens) -> tuple:
-    """(batch, tokens, channels, sequences, pointer of cu_seqlens, their count or 0, GPU) of a
-    call on [b, l, d] rows, or on packed [T, d] rows with ``cu_seqlens``."""
-    dev = t.get_device()
+def _gated_shape(t: torch.Tensor, name: str, cu_seqlens, dev: int) -> tuple:
+    """(batch, tokens, channels, sequences, pointer of cu_seqlens, their count or 0) of a call on
+    [b, l, d] rows, or on packed [T, d] rows with ``cu_seqlens``."""
     if cu_seqlens is None:
         if t.dim() != 3:
             raise ValueError(f"{name} must be [b,l,d], or [T,d] with cu_seqlens")
         b, l, d = t.shape
-        return b, l, d, b, None, 0, dev
+        return b, l, d, b, None, 0
     if t.dim() != 2:
         raise ValueError(f"{name} must be [T,d] with cu_seqlens")
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be an int32 CUDA tensor of nseq + 1 token offsets")
     l, d = t.shape
     nseq = cu_seqlens.numel() - 1
-    return 1, l, d, nseq, _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev), nseq, dev
+    return 1, l, d, nseq, _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev), nseq
 
 
 def _io_code(t: torch.Tensor, name: str) -> int:
-    code = _IO_CODES.get(t.dtype)
+    code = _IO_CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
     if code is None:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+        raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor, got "
+                        f"{getattr(t, 'dtype', type(t))}")
     return code
 
 
 def _form(gate_form: str, input_form: str) -> int:
-    if gate_form not in GATE_FORMS or input_form not in INPUT_FORMS:
+    try:
+        return GATE_FORMS[gate_form] | INPUT_FORMS[input_form]
+    except (KeyError, TypeError):
         raise ValueError(f"gate_form is one of {tuple(GATE_FORMS)}, input_form one of "
-                         f"{tuple(INPUT_FORMS)}; got {gate_form!r}, {input_form!r}")
-    return GATE_FORMS[gate_form] | INPUT_FORMS[input_form]
+                         f"{tuple(INPUT_FORMS)}; got {gate_form!r}, {input_form!r}") from None
 
 
 def _per(n: int, shape: tuple) -> tuple:
     """``shape`` [.., l, d] with ceil(l / n) in the place of l."""
     return (*shape[:-2], -(-shape[-2] // n), shape[-1])
+
+
+def _like(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def _ckpt_ptrs(ckpt, shape: tuple, dev: int) -> tuple:
@@ -628,10 +648,8 @@ def ssd_i8_gated_ckpt_empty(x: torch.Tensor) -> GatedCkpt:
     if x.dim() not in (2, 3):
         raise ValueError("x must be [b,l,d] or [T,d]")
     e = _per(CKPT_BLOCK, x.shape)
-    def codes(shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=x.device)
-    return GatedCkpt(codes(x.shape, torch.int8), codes(e, torch.uint8),
-                     codes(x.shape, torch.int8), codes(e, torch.uint8))
+    return GatedCkpt(x.new_empty(x.shape, dtype=torch.int8), x.new_empty(e, dtype=torch.uint8),
+                     x.new_empty(x.shape, dtype=torch.int8), x.new_empty(e, dtype=torch.uint8))
 
 
 def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
@@ -651,43 +669,54 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
     For a backward pass: ``span_states`` f32 [b,ceil(l/64),d] ([ceil(T/64),d]) is written, and
     ``ckpt`` (``ssd_i8_gated_ckpt_empty``) receives x and gate in 8 bits.  Returns y, of x's shape
     and dtype; rows outside every packed sequence are left as they were."""
-    def run(raw):
-        b, l, d, seqs, cu, nseq, dev = _gated_shape(x, "x", cu_seqlens)
-        dt, shape = x.dtype, x.shape
-        code = _io_code(x, "x")
-        out = torch.empty(shape, dtype=dt, device=x.device) if y is None else y
-        q = (None,) * 4 if ckpt is None else _ckpt_ptrs(ckpt, shape, dev)
-        _check("ssd_i8_gated_scan", library().ssd_i8_gated_scan(
-            *_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev),
-            *_rows(out, "y", dt, shape, dev), b, l, d, cu, nseq, _form(gate_form, input_form),
-            code, _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
-            _flat(final_state, "final_state", torch.float32, (seqs, d), dev),
-            _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
-            *q, raw))
-        return out
-    return _call("ssd_i8_gated_scan", x, run, stream)
+    dev = _gpu_of(x)
+    if stream is not None or torch.cuda.current_device() != dev:
+        with _on(dev, stream):
+            return ssd_i8_gated_scan(x, gate, cu_seqlens, gate_form=gate_form,
+                                     input_form=input_form, init_state=init_state,
+                                     final_state=final_state, y=y, span_states=span_states,
+                                     ckpt=ckpt)
+    b, l, d, seqs, cu, nseq = _gated_shape(x, "x", cu_seqlens, dev)
+    code, dt, shape = _io_code(x, "x"), x.dtype, x.shape
+    form = _form(gate_form, input_form)
+    rows = (*_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev))
+    if y is None:
+        y = _like(x)
+    _check("ssd_i8_gated_scan", library().ssd_i8_gated_scan(
+        *rows, *_rows(y, "y", dt, shape, dev), b, l, d, cu, nseq, form, code,
+        _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
+        _flat(final_state, "final_state", torch.float32, (seqs, d), dev),
+        None if span_states is None else
+        _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
+        *((None,) * 4 if ckpt is None else _ckpt_ptrs(ckpt, shape, dev)), _raw_stream(dev)))
+    return y
 
 
 def _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form, init_state,
                dfinal_state, dinit_state, dx, dgate, stream):
-    def run(raw):
-        b, l, d, seqs, cu, nseq, dev = _gated_shape(dy, "dy", cu_seqlens)
-        dt, shape = dy.dtype, dy.shape
-        code = _io_code(dy, "dy")
-        if span_states is None:
-            raise TypeError("span_states must be the tensor that the forward call wrote")
-        o = [torch.empty(shape, dtype=dt, device=dy.device) if t is None else t
-             for t in (dx, dgate)]
-        _check(name, getattr(library(), name)(
-            *_rows(dy, "dy", dt, shape, dev), *inputs(dt, shape, dev),
-            *_rows(o[0], "dx", dt, shape, dev), *_rows(o[1], "dgate", dt, shape, dev),
-            b, l, d, cu, nseq, _form(gate_form, input_form), code,
-            _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
-            _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
-            _flat(dfinal_state, "dfinal_state", torch.float32, (seqs, d), dev),
-            _flat(dinit_state, "dinit_state", torch.float32, (seqs, d), dev), raw))
-        return o[0], o[1]
-    return _call(name, dy, run, stream)
+    dev = _gpu_of(dy)
+    if stream is not None or torch.cuda.current_device() != dev:
+        with _on(dev, stream):
+            return _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form,
+                              init_state, dfinal_state, dinit_state, dx, dgate, None)
+    b, l, d, seqs, cu, nseq = _gated_shape(dy, "dy", cu_seqlens, dev)
+    code, dt, shape = _io_code(dy, "dy"), dy.dtype, dy.shape
+    form = _form(gate_form, input_form)
+    if span_states is None:
+        raise TypeError("span_states must be the tensor that the forward call wrote")
+    rows = (*_rows(dy, "dy", dt, shape, dev), *inputs(dt, shape, dev))
+    if dx is None:
+        dx = _like(dy)
+    if dgate is None:
+        dgate = _like(dy)
+    _check(name, getattr(library(), name)(
+        *rows, *_rows(dx, "dx", dt, shape, dev), *_rows(dgate, "dgate", dt, shape, dev),
+        b, l, d, cu, nseq, form, code,
+        _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
+        _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
+        _flat(dfinal_state, "dfinal_state", torch.float32, (seqs, d), dev),
+        _flat(dinit_state, "dinit_state", torch.float32, (seqs, d), dev), _raw_stream(dev)))
+    return dx, dgate
 
 
 def ssd_i8_gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor,
@@ -732,20 +761,23 @@ def ssd_i8_gated_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, 
                       y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """One token of ``ssd_i8_gated_scan`` for a decode batch: state f32 [b,d] updated in place;
     x, gate [b,d], contiguous.  Returns y [b,d] of x's dtype."""
-    def run(raw):
-        if not isinstance(x, torch.Tensor):
-            raise TypeError("x must be a torch.Tensor")
-        dev, dt, shape = state.get_device(), x.dtype, state.shape
-        if len(shape) != 2:
-            raise ValueError("state must be [b,d]")
-        code = _io_code(x, "x")
-        out = torch.empty(shape, dtype=dt, device=state.device) if y is None else y
-        _check("ssd_i8_gated_step", library().ssd_i8_gated_step(
-            _flat(state, "state", torch.float32, shape, dev), _flat(x, "x", dt, shape, dev),
-            _flat(gate, "gate", dt, shape, dev), _flat(out, "y", dt, shape, dev), shape[0],
-            shape[1], _form(gate_form, input_form), code, raw))
-        return out
-    return _call("ssd_i8_gated_step", state, run, stream)
+    dev = _gpu_of(state)
+    if stream is not None or torch.cuda.current_device() != dev:
+        with _on(dev, stream):
+            return ssd_i8_gated_step(state, x, gate, gate_form=gate_form, input_form=input_form,
+                                     y=y)
+    shape = state.shape
+    if len(shape) != 2:
+        raise ValueError("state must be [b,d]")
+    code, dt, form = _io_code(x, "x"), x.dtype, _form(gate_form, input_form)
+    ps = _flat(state, "state", torch.float32, shape, dev)
+    px, pg = _flat(x, "x", dt, shape, dev), _flat(gate, "gate", dt, shape, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    _check("ssd_i8_gated_step", library().ssd_i8_gated_step(
+        ps, px, pg, _flat(y, "y", dt, shape, dev), shape[0], shape[1], form, code,
+        _raw_stream(dev)))
+    return y
 
 
 def ssd_i8_ckpt_pack(x: torch.Tensor, *, q: Optional[torch.Tensor] = None,
@@ -753,37 +785,42 @@ def ssd_i8_ckpt_pack(x: torch.Tensor, *, q: Optional[torch.Tensor] = None,
     """8-bit checkpoint of x [b,l,d] or [T,d] (float32, float16 or bfloat16, channels contiguous):
     (int8 codes of x's shape, uint8 exponents [b,ceil(l/16),d] or [ceil(T/16),d]); a value is
     code * 2^(exponent - 127) (see ``ssd_i8_ckpt_pack`` in include/ssd_i8.h)."""
-    def run(raw):
-        if x.dim() not in (2, 3):
-            raise ValueError("x must be [b,l,d] or [T,d]")
-        dev, shape = x.get_device(), x.shape
-        se = _per(CKPT_BLOCK, shape)
-        code = _io_code(x, "x")
-        qo = torch.empty(shape, dtype=torch.int8, device=x.device) if q is None else q
-        eo = torch.empty(se, dtype=torch.uint8, device=x.device) if e is None else e
-        _check("ssd_i8_ckpt_pack", library().ssd_i8_ckpt_pack(
-            *_rows(x, "x", x.dtype, shape, dev), shape[0] if len(shape) == 3 else 1, shape[-2],
-            shape[-1], code, _flat(qo, "q", torch.int8, shape, dev),
-            _flat(eo, "e", torch.uint8, se, dev), raw))
-        return qo, eo
-    return _call("ssd_i8_ckpt_pack", x, run, stream)
+    dev = _gpu_of(x)
+    if stream is not None or torch.cuda.current_device() != dev:
+        with _on(dev, stream):
+            return ssd_i8_ckpt_pack(x, q=q, e=e)
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [b,l,d] or [T,d]")
+    code, shape = _io_code(x, "x"), x.shape
+    rows, se = _rows(x, "x", x.dtype, shape, dev), _per(CKPT_BLOCK, shape)
+    if q is None:
+        q = x.new_empty(shape, dtype=torch.int8)
+    if e is None:
+        e = x.new_empty(se, dtype=torch.uint8)
+    _check("ssd_i8_ckpt_pack", library().ssd_i8_ckpt_pack(
+        *rows, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], code,
+        _flat(q, "q", torch.int8, shape, dev), _flat(e, "e", torch.uint8, se, dev),
+        _raw_stream(dev)))
+    return q, e
 
 
 def ssd_i8_ckpt_unpack(q: torch.Tensor, e: torch.Tensor, *, dtype: str = "bf16",
                        x: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of an 8-bit checkpoint as ``dtype`` ("f32", "f16" or "bf16"), of q's shape."""
-    def run(raw):
-        if q.dim() not in (2, 3):
-            raise ValueError("q must be [b,l,d] or [T,d]")
-        if dtype not in IO_DTYPES:
-            raise ValueError(f"dtype is one of {tuple(IO_DTYPES)}, got {dtype!r}")
-        code, dt = IO_DTYPES[dtype]
-        dev, shape = q.get_device(), q.shape
-        out = torch.empty(shape, dtype=dt, device=q.device) if x is None else x
-        _check("ssd_i8_ckpt_unpack", library().ssd_i8_ckpt_unpack(
-            _flat(q, "q", torch.int8, shape, dev),
-            _flat(e, "e", torch.uint8, _per(CKPT_BLOCK, shape), dev),
-            shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], code,
-            _flat(out, "x", dt, shape, dev), raw))
-        return out
-    return _call("ssd_i8_ckpt_unpack", q, run, stream)
+    dev = _gpu_of(q)
+    if stream is not None or torch.cuda.current_device() != dev:
+        with _on(dev, stream):
+            return ssd_i8_ckpt_unpack(q, e, dtype=dtype, x=x)
+    if q.dim() not in (2, 3):
+        raise ValueError("q must be [b,l,d] or [T,d]")
+    if dtype not in IO_DTYPES:
+        raise ValueError(f"dtype is one of {tuple(IO_DTYPES)}, got {dtype!r}")
+    (code, dt), shape = IO_DTYPES[dtype], q.shape
+    pq = _flat(q, "q", torch.int8, shape, dev)
+    pe = _flat(e, "e", torch.uint8, _per(CKPT_BLOCK, shape), dev)
+    if x is None:
+        x = q.new_empty(shape, dtype=dt)
+    _check("ssd_i8_ckpt_unpack", library().ssd_i8_ckpt_unpack(
+        pq, pe, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], code,
+        _flat(x, "x", dt, shape, dev), _raw_stream(dev)))
+    return x
