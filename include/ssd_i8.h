@@ -329,9 +329,11 @@ SSD_API ssd_status ssd_i8_chunk_cb(const int8_t *C, const int8_t *B, int batch, 
  *     optional ones are NULL (zero when read, not written).
  *   - No output may overlap an input or another output (SSD_ERR_INVALID_ARG where it does); the
  *     `state` of the step is both.
- *   - No workspace, no device-side waits other than hardware barriers, no atomics: results do not
- *     change from run to run.
- *   - Supported: channels >= 1, seqlen <= 2^31 - 65536 and batch * ceil(channels / 32) * 8 < 2^31
+ *   - The scans take ssd_i8_gated_scan_workspace_size(...) bytes of workspace, 256-byte aligned (0
+ *     bytes, and NULL, where there are enough channels to fill the machine).  Its contents need no
+ *     initialisation and mean nothing afterwards.  One workspace per concurrently running call.
+ *   - No CTA waits for another, and no atomics: results do not change from run to run.
+ *   - Supported: channels >= 1, seqlen <= 2^31 - 65536 and batch * ceil(channels / 32) * 64 < 2^31
  *     (else SSD_ERR_UNSUPPORTED).
  */
 typedef enum ssd_io_dtype { SSD_IO_F32 = 0, SSD_IO_F16 = 1, SSD_IO_BF16 = 3 } ssd_io_dtype;
@@ -341,6 +343,10 @@ typedef enum ssd_gate_form { SSD_GATE_LOG = 0, SSD_GATE_LOGIT = 1 } ssd_gate_for
 /* Tokens between the saved states, and tokens of one channel that share a checkpoint scale. */
 #define SSD_GATED_SPAN 64
 #define SSD_CKPT_BLOCK 16
+
+/* Bytes of workspace that the scans need for this problem, forward or backward; 0 on invalid sizes.
+ * (At most 64 maps of 512 bytes per 32 channels of a row.) */
+SSD_API size_t ssd_i8_gated_scan_workspace_size(int batch, int seqlen, int channels, int io_dtype);
 
 /*
  * Forward.
@@ -362,7 +368,8 @@ SSD_API ssd_status ssd_i8_gated_scan(const void *x, long long x_batch_stride,
                                      const int32_t *cu_seqlens, int nseq, int form, int io_dtype,
                                      const float *init_state, float *final_state,
                                      float *span_states, int8_t *ckpt_x, uint8_t *ckpt_x_exp,
-                                     int8_t *ckpt_gate, uint8_t *ckpt_gate_exp, void *stream);
+                                     int8_t *ckpt_gate, uint8_t *ckpt_gate_exp, void *workspace,
+                                     size_t workspace_bytes, void *stream);
 
 /*
  * Backward.  With dh_t = dy_t + a_{t+1} dh_{t+1} (dfinal_state at a sequence's end):
@@ -384,7 +391,8 @@ SSD_API ssd_status ssd_i8_gated_scan_bwd(const void *dy, long long dy_batch_stri
                                          int channels, const int32_t *cu_seqlens, int nseq,
                                          int form, int io_dtype, const float *init_state,
                                          const float *span_states, const float *dfinal_state,
-                                         float *dinit_state, void *stream);
+                                         float *dinit_state, void *workspace,
+                                         size_t workspace_bytes, void *stream);
 
 /*
  * Backward from the 8-bit checkpoints of the forward call: the formulas above with the decoded
@@ -401,7 +409,8 @@ SSD_API ssd_status ssd_i8_gated_scan_bwd_ckpt(const void *dy, long long dy_batch
                                               int channels, const int32_t *cu_seqlens, int nseq,
                                               int form, int io_dtype, const float *init_state,
                                               const float *span_states, const float *dfinal_state,
-                                              float *dinit_state, void *stream);
+                                              float *dinit_state, void *workspace,
+                                              size_t workspace_bytes, void *stream);
 
 /*
  * One token of the recurrence for every sequence of a decode batch, in place.

@@ -106,9 +106,13 @@ ssd_status shape_status(int batch, int seqlen, int channels, const int32_t* cu, 
     if (batch < 0 || seqlen < 0 || channels <= 0 || nseq < 0 || !form_ok(form) || !io_size(io_dtype))
         return SSD_ERR_INVALID_ARG;
     if (cu ? batch != 1 || !aligned(cu, 4) : nseq != 0) return SSD_ERR_INVALID_ARG;
-    if (seqlen > kMaxSeqlen || (long long)batch * ((channels + 31LL) / 32) * 8 > 0x7fffffffLL)
+    if (seqlen > kMaxSeqlen || (long long)batch * ((channels + 31LL) / 32) * 64 > 0x7fffffffLL)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
+}
+
+bool workspace_ok(const void* p, size_t bytes, size_t need) {
+    return need == 0 || (p && bytes >= need && aligned(p, 256));
 }
 
 // No token at all: the states pass through.
@@ -120,7 +124,7 @@ ssd_status pass_states(const float* from, float* to, size_t count, cudaStream_t 
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
-ssd_status run_bwd(ssd::GatedArgs& a, size_t elem, cudaStream_t st) {
+ssd_status run_bwd(ssd::GatedArgs& a, size_t elem, size_t workspace_bytes, cudaStream_t st) {
     const size_t seqs = a.cu ? a.nseq : a.batch, d = a.channels;
     if (!aligned(a.init_state, 4) || !aligned(a.span_states, 4) || !aligned(a.dfinal_state, 4) ||
         !aligned(a.dinit_state, 4))
@@ -157,6 +161,9 @@ ssd_status run_bwd(ssd::GatedArgs& a, size_t elem, cudaStream_t st) {
     r.flat(a.span_states, (size_t)a.batch * spans * d * 4, false);
     r.flat(a.init_state, state_bytes, false);
     if (a.cu) r.flat(a.cu, ((size_t)a.nseq + 1) * 4, false);
+    const size_t need = ssd_i8_gated_scan_workspace_size(a.batch, a.seqlen, a.channels, a.io_dtype);
+    if (!workspace_ok(a.workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
+    r.flat(a.workspace, need, true);
     if (r.clash()) return SSD_ERR_INVALID_ARG;
     return ssd::launch_gated_scan_bwd(a, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
@@ -165,6 +172,13 @@ ssd_status run_bwd(ssd::GatedArgs& a, size_t elem, cudaStream_t st) {
 
 extern "C" {
 
+size_t ssd_i8_gated_scan_workspace_size(int batch, int seqlen, int channels, int io_dtype) {
+    if (batch <= 0 || seqlen <= 0 ||
+        shape_status(batch, seqlen, channels, nullptr, 0, 0, io_dtype) != SSD_OK)
+        return 0;
+    return ssd::gated_workspace_bytes(batch, seqlen, channels, io_dtype);
+}
+
 ssd_status ssd_i8_gated_scan(const void* x, long long x_batch_stride, long long x_token_stride,
                              const void* gate, long long gate_batch_stride,
                              long long gate_token_stride, void* y, long long y_batch_stride,
@@ -172,7 +186,8 @@ ssd_status ssd_i8_gated_scan(const void* x, long long x_batch_stride, long long 
                              const int32_t* cu_seqlens, int nseq, int form, int io_dtype,
                              const float* init_state, float* final_state, float* span_states,
                              int8_t* ckpt_x, uint8_t* ckpt_x_exp, int8_t* ckpt_gate,
-                             uint8_t* ckpt_gate_exp, void* stream) {
+                             uint8_t* ckpt_gate_exp, void* workspace, size_t workspace_bytes,
+                             void* stream) {
     const ssd_status s = shape_status(batch, seqlen, channels, cu_seqlens, nseq, form, io_dtype);
     if (s != SSD_OK) return s;
     const bool ckpt = ckpt_x || ckpt_x_exp || ckpt_gate || ckpt_gate_exp;
@@ -208,7 +223,11 @@ ssd_status ssd_i8_gated_scan(const void* x, long long x_batch_stride, long long 
     r.flat(ckpt_x_exp, ne, true);
     r.flat(ckpt_gate_exp, ne, true);
     if (cu_seqlens) r.flat(cu_seqlens, ((size_t)nseq + 1) * 4, false);
+    const size_t need = ssd_i8_gated_scan_workspace_size(batch, seqlen, channels, io_dtype);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return SSD_ERR_WORKSPACE;
+    r.flat(workspace, need, true);
     if (r.clash()) return SSD_ERR_INVALID_ARG;
+    a.workspace = workspace;
     a.x_q = ckpt_x;
     a.x_e = ckpt_x_exp;
     a.gate_q = ckpt_gate;
@@ -237,7 +256,8 @@ ssd_status ssd_i8_gated_scan_bwd(const void* dy, long long dy_batch_stride,
                                  int batch, int seqlen, int channels, const int32_t* cu_seqlens,
                                  int nseq, int form, int io_dtype, const float* init_state,
                                  const float* span_states, const float* dfinal_state,
-                                 float* dinit_state, void* stream) {
+                                 float* dinit_state, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
     const ssd_status s = shape_status(batch, seqlen, channels, cu_seqlens, nseq, form, io_dtype);
     if (s != SSD_OK) return s;
     ssd::GatedArgs a{};
@@ -258,7 +278,8 @@ ssd_status ssd_i8_gated_scan_bwd(const void* dy, long long dy_batch_stride,
     a.span_states = const_cast<float*>(span_states);  // read by the backward kernels
     a.dfinal_state = dfinal_state;
     a.dinit_state = dinit_state;
-    return run_bwd(a, io_size(io_dtype), static_cast<cudaStream_t>(stream));
+    a.workspace = workspace;
+    return run_bwd(a, io_size(io_dtype), workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 ssd_status ssd_i8_gated_scan_bwd_ckpt(const void* dy, long long dy_batch_stride,
@@ -271,7 +292,8 @@ ssd_status ssd_i8_gated_scan_bwd_ckpt(const void* dy, long long dy_batch_stride,
                                       int channels, const int32_t* cu_seqlens, int nseq, int form,
                                       int io_dtype, const float* init_state,
                                       const float* span_states, const float* dfinal_state,
-                                      float* dinit_state, void* stream) {
+                                      float* dinit_state, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
     const ssd_status s = shape_status(batch, seqlen, channels, cu_seqlens, nseq, form, io_dtype);
     if (s != SSD_OK) return s;
     if (batch > 0 && seqlen > 0 && (!ckpt_x || !ckpt_x_exp || !ckpt_gate || !ckpt_gate_exp))
@@ -296,7 +318,8 @@ ssd_status ssd_i8_gated_scan_bwd_ckpt(const void* dy, long long dy_batch_stride,
     a.span_states = const_cast<float*>(span_states);
     a.dfinal_state = dfinal_state;
     a.dinit_state = dinit_state;
-    return run_bwd(a, io_size(io_dtype), static_cast<cudaStream_t>(stream));
+    a.workspace = workspace;
+    return run_bwd(a, io_size(io_dtype), workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 ssd_status ssd_i8_gated_step(float* state, const void* x, const void* gate, void* y, int batch,

@@ -120,11 +120,11 @@ __device__ __forceinline__ Decay<1> decay_of(Vec<1> gate) {
     const float g = gate.x;
     Decay<1> d;
     if constexpr (LOGIT) {
+        // the larger of a and 1 - a is 1 / (1 + t) with t = exp(-|gate|) <= 1, the other t times it
         const float t = expf(-fabsf(g));
-        const float r = __frcp_rn(1.f + t), tr = __fdiv_rn(t, 1.f + t);
+        const float r = fast_rcp(1.f + t), tr = t * r;
         d.a.x = g >= 0.f ? r : tr;
         d.u.x = g >= 0.f ? tr : r;
-        if (!(g == g)) d.a.x = d.u.x = g;
     } else {
         d.a.x = expf(g);
         d.u.x = -expm1f(g);
@@ -220,12 +220,7 @@ struct Coder {
 
 // What a checkpoint keeps of a gate: below -16 the decay (for logits, above 16 its complement)
 // is within 1.2e-7 of its limit, and masks of the lowest value must not set the block's scale.
-template <bool LOGIT>
-__device__ __forceinline__ float held_gate(float g) {
-    if (g < -16.f) g = -16.f;
-    if (LOGIT && g > 16.f) g = 16.f;
-    return g;
-}
+constexpr float kHeldGate = 16.f;
 
 }  // namespace gated
 }  // namespace ssd

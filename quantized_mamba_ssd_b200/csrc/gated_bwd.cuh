@@ -20,11 +20,26 @@ template <typename T, bool CKPT>
 constexpr int kBwdSegBytes = 2 * kSubBytes<kInRow<T, CKPT>> + kSubBytes<kRowBytes>;
 constexpr int kSpanSegs = kSpan / kSub;
 constexpr int kBwdSlots = 2;
-// Segments from codes are smaller: 8 warps of them fit twice into an SM's shared memory, where of
-// full ones only 4 warps fit three times.
-template <bool CKPT> constexpr int kBwdWarps = CKPT ? 8 : 4;
-template <bool CKPT> constexpr int kBwdBlocks = CKPT ? 2 : 3;
 template <int V, int W> constexpr int kFwdMapBytes = 2 * W * MapSlots<V>::kFloats * 4;
+
+// The lane's channels of one staged row: values, or codes times their scales.
+template <typename T, bool CKPT>
+__device__ __forceinline__ Vec<kChannels<T>> row_value(const uint8_t* r, Vec<kChannels<T>> scale) {
+    constexpr int V = kChannels<T>;
+    if constexpr (CKPT && V == 2) {
+        // code + 128 in the low byte of 2^23 is that number as a float; times a power of two, and
+        // less (2^23 + 128) of it, the value, all exact
+        const uint32_t q = *reinterpret_cast<const uint16_t*>(r) ^ 0x8080u;
+        Vec<2> f;
+        f.x = make_float2(__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7440)),
+                          __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7441)));
+        return fma(f, scale, mul(scale, splat<V>(-8388736.f)));
+    } else if constexpr (CKPT) {
+        return mul(Vec<1>{static_cast<float>(*reinterpret_cast<const int8_t*>(r))}, scale);
+    } else {
+        return Pack<T>::get(*reinterpret_cast<const uint32_t*>(r));
+    }
+}
 
 template <typename T, bool LOGIT, bool COMP, bool PACKED, bool CKPT>
 __global__ void __launch_bounds__(32 * kBwdWarps<CKPT>, kBwdBlocks<CKPT>)
@@ -37,11 +52,12 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     constexpr int W = kBwdWarps<CKPT>;
-    const int R = ta.cluster, rank = blockIdx.x % R, unit = blockIdx.x / R;
+    const int chunk = blockIdx.x % ta.chunks, unit = blockIdx.x / ta.chunks;
     const int d = a.channels, b = unit / ta.strips, c0 = unit % ta.strips * 32 * V;
     const int c = c0 + lane * V, count = max(0, min(V, d - c));
-    const bool whole = d - c0 >= 32 * V && ta.whole_out;
-    const int tiles = (ta.blocks + W - 1) / W, steps = (tiles + R - 1) / R;
+    const bool whole = ta.whole_out;
+    const int tiles = (ta.blocks + W - 1) / W, low = chunk * ta.chunk_tiles;  // the chunk's first tile
+    const int steps = min(tiles - low, ta.chunk_tiles);
     const size_t row0 = (size_t)b * a.seqlen;
 
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
@@ -65,13 +81,13 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
     const long long sdg = a.dgate.token_stride * sizeof(T);
 
     // the gradient's maps meet; the state's only serve the warps of the same tile
-    Meeting<V, W>& meeting = *reinterpret_cast<Meeting<V, W>*>(staged);
+    float* maps = reinterpret_cast<float*>(staged);
     float* fwds = reinterpret_cast<float*>(staged + kMeetingBytes<V, W>);
     uint8_t* own = staged + kMeetingBytes<V, W> + kFwdMapBytes<V, W> + warp * kBwdSlots * kBwdSegBytes<T, CKPT>;
-    // tiles of W segments from the last one down, below 0: nothing left for this CTA
-    auto start = [&](int k) { return ((tiles - 1 - (k * R + rank)) * W + warp) * kSub; };
+    // tiles of W segments, from the chunk's last one down
+    auto start = [&](int k) { return ((low + steps - 1 - k) * W + warp) * kSub; };
     auto stage = [&](int k) {
-        const int t = start(k), n = t < 0 ? 0 : max(0, min(kSub, a.seqlen - t));
+        const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
             uint8_t* to = own + k % kBwdSlots * kBwdSegBytes<T, CKPT>;
             stage_rows<kRow>(to, px + t * sx, sx, n, in_width, ta.align_x);
@@ -85,14 +101,16 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
     };
 
     F carry = PACKED ? splat<V>(0.f) : state_of(a.dfinal_state, b);
-    if (PACKED && a.dinit_state && rank == 0)  // sequences without a token
+    if (PACKED && a.dinit_state && chunk == 0)  // sequences without a token
         for (int s = warp; s < a.nseq; s += W)
             if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
                 store_floats<V>(a.dinit_state + (size_t)s * d + c, state_of(a.dfinal_state, s), count);
-    Held held;
     stage(0);
+    for (int i = ta.chunks - 1; i > chunk; --i)  // through the chunks behind this one
+        carry = through<PACKED>(MapSlots<V>::read(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, i, lane), carry);
+    Held held;
     for (int k = 0; k < steps; ++k) {
-        const int t0 = start(k), n = t0 < 0 ? 0 : max(0, min(kSub, a.seqlen - t0));
+        const int t0 = start(k), n = max(0, min(kSub, a.seqlen - t0));
         Marks m;
         m.valid = (1u << n) - 1;
         m.begin = m.end = 0;
@@ -134,21 +152,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                     }
                 }
         }
-        auto decoded = [&](const uint8_t* r, F scale, int j) {
-            if constexpr (CKPT && V == 2) {
-                // code + 128 in the low byte of 2^23 is that number as a float; times a power of
-                // two, and less (2^23 + 128) of it, the value, all exact
-                const uint32_t q = *reinterpret_cast<const uint16_t*>(r + j * kRow) ^ 0x8080u;
-                F f;
-                f.x = make_float2(__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7440)),
-                                  __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7441)));
-                return fma(f, scale, mul(scale, splat<V>(-8388736.f)));
-            } else if constexpr (CKPT) {
-                return mul(F{static_cast<float>(*reinterpret_cast<const int8_t*>(r + j * kRow))}, scale);
-            } else {
-                return Pk::get(*reinterpret_cast<const uint32_t*>(r + j * kRow));
-            }
-        };
+        auto decoded = [&](const uint8_t* r, F scale, int j) { return row_value<T, CKPT>(r + j * kRow, scale); };
         auto x_of = [&](int j) { return decoded(rx, scale_x, j); };
         auto gate_of = [&](int j) {
             F g = decoded(rg, scale_g, j);
@@ -168,7 +172,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         Map<V> fwd = identity_map<V>(), back = identity_map<V>();
         // segments inside one sequence, by far the most, go without the checks of every token
         const bool inside = !PACKED || !(m.begin | m.end);
-        auto maps = [&](auto checks) {
+        auto reduce = [&](auto checks) {
             constexpr bool CHECK = decltype(checks)::value;
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
@@ -193,8 +197,8 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                 if (!CHECK || !(m.end & ((1u << j) - 1))) back.B = step(fwd.A, fwd.L, dy, back.B);
             }
         };
-        if (inside) [[likely]] maps(std::false_type{});
-        else maps(std::true_type{});
+        if (inside) [[likely]] reduce(std::false_type{});
+        else reduce(std::true_type{});
         back.A = PACKED && m.end ? splat<V>(-1.f) : fwd.A;
         back.L = fwd.L;
         if (PACKED && m.begin) fwd.A = splat<V>(-1.f);
@@ -202,7 +206,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         float* states = fwds + (k & 1) * W * MapSlots<V>::kFloats;
         MapSlots<V>::write(states, warp, lane, fwd);
         // the gradient from behind the segment
-        F e = meeting.template meet<PACKED>(k, W - 1 - warp, R, rank, back, carry);
+        F e = meet<PACKED, W>(maps, k, W - 1 - warp, back, carry);
         // (the spans of a tile begin at multiples of kSpanSegs warps)
         const Map<V> into = MapSlots<V>::template join_runs<PACKED, W>(
             states, warp - warp % kSpanSegs, warp, lane);
@@ -247,8 +251,8 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                     if (a.dinit_state) store_floats<V>(a.dinit_state + (size_t)s * d + c, e, count);
                 }
                 if (plain) {
-                    *reinterpret_cast<uint32_t*>(qdx) = Pk::put(dx);
-                    *reinterpret_cast<uint32_t*>(qdg) = Pk::put(dg);
+                    store_row<T>(qdx, dx, true, count);
+                    store_row<T>(qdg, dg, true, count);
                 } else if (m.valid >> j & 1) {
                     store_row<T>(qdx, dx, whole, count);
                     store_row<T>(qdg, dg, whole, count);
@@ -260,9 +264,103 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         if (inside) [[likely]] gradients(std::false_type{});
         else gradients(std::true_type{});
     }
-    // the carry behind the first tile is the initial state's gradient, in every thread
-    if (!PACKED && a.dinit_state && rank == 0 && warp == 0)
+    // the carry behind the first tile is the initial state's gradient, in every thread of its CTA
+    if (!PACKED && a.dinit_state && chunk == 0 && warp == 0)
         store_floats<V>(a.dinit_state + (size_t)b * d + c, carry, count);
+}
+
+// The gradient's maps of all chunks but the first of every strip: each warp reduces a run of whole
+// segments of gate (or its codes) and dy, in the order of the tokens (see the scan's own map).
+constexpr int kBackSlots = 3;
+template <typename T, bool CKPT>
+constexpr int kBackSegBytes = kSubBytes<kInRow<T, CKPT>> + kSubBytes<kRowBytes>;
+
+template <typename T, bool LOGIT, bool PACKED, bool CKPT>
+__global__ void __launch_bounds__(32 * kMapWarps)
+chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
+    constexpr int V = kChannels<T>, W = kMapWarps, kRow = kInRow<T, CKPT>;
+    using Pk = Pack<T>;
+    using F = Vec<V>;
+    extern __shared__ __align__(128) uint8_t staged[];
+
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int chunk = 1 + blockIdx.x % (ta.chunks - 1), unit = blockIdx.x / (ta.chunks - 1);
+    const int d = a.channels, b = unit / ta.strips, c0 = unit % ta.strips * 32 * V;
+    const int c = c0 + lane * V, count = max(0, min(V, d - c));
+    // segments of the chunk, and of a warp (of full rows a tile has fewer than this CTA warps)
+    const int all_of_them = ta.chunk_tiles * kBwdWarps<CKPT>, each = (all_of_them + W - 1) / W;
+    const int first = chunk * all_of_them + warp * each, run = max(0, min(each, all_of_them - warp * each));
+
+    const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
+    const char* pg = CKPT ? reinterpret_cast<const char*>(a.gate_q) + (size_t)b * a.seqlen * d + c0
+                          : static_cast<const char*>(a.gate.ptr) + (b * a.gate.batch_stride + c0) * sizeof(T);
+    const long long sg = CKPT ? d : a.gate.token_stride * sizeof(T);
+    const char* pdy = static_cast<const char*>(a.dy.ptr) + (b * a.dy.batch_stride + c0) * sizeof(T);
+    const long long sdy = a.dy.token_stride * sizeof(T);
+    float* maps = reinterpret_cast<float*>(staged);
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kBackSlots * kBackSegBytes<T, CKPT>;
+    auto stage = [&](int k) {
+        const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
+        if (k < run && n > 0) {
+            uint8_t* to = own + k % kBackSlots * kBackSegBytes<T, CKPT>;
+            stage_rows<kRow>(to, pg + t * sg, sg, n, CKPT ? min(kRow, d - c0) : width, ta.align_gate);
+            stage_rows<kRowBytes>(to + kSubBytes<kRow>, pdy + t * sdy, sdy, n, width, ta.align_dy);
+        }
+        copy_commit();
+    };
+    Map<V> all = identity_map<V>();
+    bool closed = false;  // behind the first end nothing reaches the run's first token
+    Held held;
+#pragma unroll 1
+    for (int k = 0; k < kBackSlots - 1; ++k) stage(k);
+    for (int k = 0; k < run; ++k) {
+        const int t0 = (first + k) * kSub, n = max(0, min(kSub, a.seqlen - t0));
+        Marks m;
+        m.valid = (1u << n) - 1;
+        m.begin = m.end = 0;
+        if constexpr (PACKED) m = marks_of(a.cu, a.nseq, t0, n, held);
+        F scale;
+        if constexpr (CKPT)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                scale.set(v, n > 0 && v < count
+                                 ? scale_of(__ldg(a.gate_e + ((size_t)b * ta.blocks + first + k) * d + c + v)) : 0.f);
+        copy_wait<kBackSlots - 2>();
+        __syncwarp();
+        stage(k + kBackSlots - 1);
+        uint8_t* here = own + k % kBackSlots * kBackSegBytes<T, CKPT>;
+        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRow>(here, pg + t0 * sg, sg);
+        if (ta.align_dy < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + kSubBytes<kRow>, pdy + t0 * sdy, sdy);
+        const uint8_t* rg = here + lane * (kRow / 32);
+        const uint32_t* rdy = reinterpret_cast<const uint32_t*>(here + kSubBytes<kRow>) + lane;
+        auto token = [&](int j, F dy) {
+            extend(all, decay_of<LOGIT>(row_value<T, CKPT>(rg + j * kRow, scale)));
+            if (!PACKED || !closed) all.B = step(all.A, all.L, dy, all.B);
+        };
+        if (m.valid == kAll && !m.end) [[likely]] {
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) token(j, Pk::get(rdy[j * 32]));
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kSub; ++j) {
+                if (!(m.valid >> j & 1)) continue;
+                F dy = Pk::get(rdy[j * 32]);
+                const bool ends = PACKED && (m.end >> j & 1);
+                if (ends) {
+                    const int s = __shfl_sync(0xffffffffu, m.seq, j);
+                    dy = add(dy, load_floats<V>(a.dfinal_state ? a.dfinal_state + (size_t)s * d + c : nullptr, count));
+                }
+                token(j, dy);
+                closed |= ends;
+            }
+        }
+    }
+    if (closed) all.A = splat<V>(-1.f);
+    MapSlots<V>::write(maps, W - 1 - warp, lane, all);
+    __syncthreads();
+    if (warp == 0)
+        MapSlots<V>::write(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, chunk, lane,
+                           MapSlots<V>::template join_runs<PACKED, W>(maps, 0, W, lane));
 }
 
 template <typename T, bool LOGIT>
@@ -273,10 +371,20 @@ cudaError_t dispatch_bwd(const GatedArgs& a, cudaStream_t st) {
     auto go = [&](auto comp, auto packed, auto ckpt) {
         constexpr bool C = decltype(comp)::value, K = decltype(packed)::value, Q = decltype(ckpt)::value;
         constexpr int bytes = kBwdSegBytes<T, Q>;
-        constexpr int W = kBwdWarps<Q>;
-        t.cluster = cluster_size((long long)t.strips * a.batch, t.blocks, W, kBwdBlocks<Q>);
-        return launch_strips(scan_bwd_kernel<T, LOGIT, C, K, Q>, a, t, W,
-                             kMeetingBytes<kChannels<T>, W> + kFwdMapBytes<kChannels<T>, W> + W * kBwdSlots * bytes, st);
+        constexpr int W = kBwdWarps<Q>, V = kChannels<T>;
+        const long long units = (long long)t.strips * a.batch;
+        const Chunks ch = chunks_of(units, t.blocks, W, kBwdBlocks<Q>);
+        t.chunks = ch.count;
+        t.chunk_tiles = ch.tiles;
+        t.maps = static_cast<float*>(a.workspace);
+        if (t.chunks > 1) {
+            const cudaError_t e = launch_ctas(chunk_back_kernel<T, LOGIT, K, Q>, units * (t.chunks - 1), kMapWarps,
+                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kBackSlots * kBackSegBytes<T, Q>,
+                                              st, a, t);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_ctas(scan_bwd_kernel<T, LOGIT, C, K, Q>, units * t.chunks, W,
+                           kMeetingBytes<V, W> + kFwdMapBytes<V, W> + W * kBwdSlots * bytes, st, a, t);
     };
     auto packed = [&](auto comp, auto ckpt) { return a.cu ? go(comp, Y{}, ckpt) : go(comp, N{}, ckpt); };
     auto input = [&](auto ckpt) { return a.complement ? packed(Y{}, ckpt) : packed(N{}, ckpt); };

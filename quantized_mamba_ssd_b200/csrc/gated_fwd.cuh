@@ -13,7 +13,7 @@ namespace gated {
 
 // A warp's staged segment: x and gate.
 constexpr int kFwdSegBytes = 2 * kSubBytes<kRowBytes>;
-constexpr int kFwdWarps = 8, kFwdSlots = 2, kFwdBlocks = 2;
+constexpr int kFwdSlots = 2;
 
 template <typename T, bool LOGIT, bool COMP, bool PACKED>
 __global__ void __launch_bounds__(32 * kFwdWarps, kFwdBlocks)
@@ -27,11 +27,12 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
     // the same in all lanes
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     constexpr int W = kFwdWarps;
-    const int R = ta.cluster, rank = blockIdx.x % R, unit = blockIdx.x / R;
+    const int chunk = blockIdx.x % ta.chunks, unit = blockIdx.x / ta.chunks;
     const int d = a.channels, b = unit / ta.strips, c0 = unit % ta.strips * 32 * V;
     const int c = c0 + lane * V, count = max(0, min(V, d - c));
-    const bool full = d - c0 >= 32 * V, whole = full && ta.whole_out, whole_codes = full && ta.whole_codes;
-    const int steps = (ta.blocks + R * W - 1) / (R * W);
+    const bool whole = ta.whole_out, whole_codes = ta.whole_codes;
+    const int first = chunk * ta.chunk_tiles * W;  // segment
+    const int steps = (min(ta.blocks - first, ta.chunk_tiles * W) + W - 1) / W;
     const size_t row0 = (size_t)b * a.seqlen;
 
     const char* px = static_cast<const char*>(a.x.ptr) + (b * a.x.batch_stride + c0) * sizeof(T);
@@ -41,9 +42,9 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
     const long long sy = a.y.token_stride * sizeof(T);
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
 
-    Meeting<V, W>& meeting = *reinterpret_cast<Meeting<V, W>*>(staged);
+    float* maps = reinterpret_cast<float*>(staged);
     uint8_t* own = staged + kMeetingBytes<V, W> + warp * kFwdSlots * kFwdSegBytes;
-    auto start = [&](int k) { return ((k * R + rank) * W + warp) * kSub; };
+    auto start = [&](int k) { return (first + k * W + warp) * kSub; };
     auto stage = [&](int k) {  // this warp's segment of step k
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
@@ -58,12 +59,14 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
     };
 
     F carry = PACKED ? splat<V>(0.f) : init_of(b);
-    if (PACKED && a.final_state && rank == 0)  // sequences without a token
+    if (PACKED && a.final_state && chunk == 0)  // sequences without a token
         for (int s = warp; s < a.nseq; s += W)
             if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
                 store_floats<V>(a.final_state + (size_t)s * d + c, init_of(s), count);
+    stage(0);
+    for (int i = 0; i < chunk; ++i)  // through the chunks before this one
+        carry = through<PACKED>(MapSlots<V>::read(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, i, lane), carry);
     Held held;
-    for (int k = 0; k < kFwdSlots - 1; ++k) stage(k);
     for (int k = 0; k < steps; ++k) {
         const int t0 = start(k), n = max(0, min(kSub, a.seqlen - t0));
         Marks m;
@@ -88,8 +91,9 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         }
         if (a.x_q && n > 0) {
             const size_t at = (row0 + t0) * d + c, be = ((size_t)b * ta.blocks + t0 / kBlock) * d + c;
-            code_rows<T, false, false>(rx, m.valid, a.x_q + at, a.x_e + be, d, whole_codes, count);
-            code_rows<T, true, LOGIT>(rg, m.valid, a.gate_q + at, a.gate_e + be, d, whole_codes, count);
+            code_rows<T>(rx, m.valid, -INFINITY, INFINITY, a.x_q + at, a.x_e + be, d, whole_codes, count);
+            code_rows<T>(rg, m.valid, -kHeldGate, LOGIT ? kHeldGate : INFINITY, a.gate_q + at, a.gate_e + be, d,
+                         whole_codes, count);
         }
 
         // The state behind token j is P[j] carry + B[j] (P with its low part Q in fp32): from the
@@ -115,7 +119,7 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         if (!PACKED || !m.begin) [[likely]] map(std::false_type{});
         else map(std::true_type{});
         if (PACKED && m.begin) seg.A = splat<V>(-1.f);
-        F h = meeting.template meet<PACKED>(k, warp, R, rank, seg, carry);
+        F h = meet<PACKED, W>(maps, k, warp, seg, carry);
         if (a.span_states && n > 0 && t0 % kSpan == 0) {
             const bool none = PACKED && (!(m.valid & 1) || (m.begin & 1));
             store_floats<V>(a.span_states + ((size_t)b * ta.spans + t0 / kSpan) * d + c,
@@ -141,7 +145,7 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         if (whole && m.valid == kAll) [[likely]] {
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
-                *reinterpret_cast<uint32_t*>(qy) = Pk::put(step(P[j], Q[V == 1 ? j : 0], h, B[j]));
+                store_row<T>(qy, step(P[j], Q[V == 1 ? j : 0], h, B[j]), true, count);
                 qy += sy;
             }
         } else {
@@ -153,9 +157,91 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
             }
         }
     }
-    // the carry behind the last tile is the final state, in every thread of the cluster
-    if (!PACKED && a.final_state && rank == 0 && warp == 0)
+    // the carry behind the last tile is the final state, in every thread of its CTA
+    if (!PACKED && a.final_state && chunk == ta.chunks - 1 && warp == 0)
         store_floats<V>(a.final_state + (size_t)b * d + c, carry, count);
+}
+
+// The maps of all chunks but the last of every strip: each warp reduces a run of whole segments.
+constexpr int kMapSlots = 3;
+template <typename T, bool LOGIT, bool COMP, bool PACKED>
+__global__ void __launch_bounds__(32 * kMapWarps)
+chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
+    constexpr int V = kChannels<T>, W = kMapWarps;
+    using Pk = Pack<T>;
+    using F = Vec<V>;
+    extern __shared__ __align__(128) uint8_t staged[];
+
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int chunk = blockIdx.x % (ta.chunks - 1), unit = blockIdx.x / (ta.chunks - 1);
+    const int d = a.channels, b = unit / ta.strips, c0 = unit % ta.strips * 32 * V;
+    const int c = c0 + lane * V, count = max(0, min(V, d - c));
+    const int run = ta.chunk_tiles * kFwdWarps / W;  // segments of a warp
+    const int first = chunk * ta.chunk_tiles * kFwdWarps + warp * run;
+
+    const char* px = static_cast<const char*>(a.x.ptr) + (b * a.x.batch_stride + c0) * sizeof(T);
+    const char* pg = static_cast<const char*>(a.gate.ptr) + (b * a.gate.batch_stride + c0) * sizeof(T);
+    const long long sx = a.x.token_stride * sizeof(T), sg = a.gate.token_stride * sizeof(T);
+    const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
+    float* maps = reinterpret_cast<float*>(staged);
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kMapSlots * kFwdSegBytes;
+    auto stage = [&](int k) {
+        const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
+        if (k < run && n > 0) {
+            uint8_t* to = own + k % kMapSlots * kFwdSegBytes;
+            stage_rows<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
+            stage_rows<kRowBytes>(to + kSubBytes<kRowBytes>, pg + t * sg, sg, n, width, ta.align_gate);
+        }
+        copy_commit();
+    };
+    Map<V> all = identity_map<V>();
+    bool begins = false;
+    Held held;
+#pragma unroll 1
+    for (int k = 0; k < kMapSlots - 1; ++k) stage(k);
+    for (int k = 0; k < run; ++k) {
+        const int t0 = (first + k) * kSub, n = max(0, min(kSub, a.seqlen - t0));
+        Marks m;
+        m.valid = (1u << n) - 1;
+        m.begin = m.end = 0;
+        if constexpr (PACKED) m = marks_of(a.cu, a.nseq, t0, n, held);
+        copy_wait<kMapSlots - 2>();
+        __syncwarp();
+        stage(k + kMapSlots - 1);
+        uint8_t* here = own + k % kMapSlots * kFwdSegBytes;
+        if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here, px + t0 * sx, sx);
+        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + kSubBytes<kRowBytes>, pg + t0 * sg, sg);
+        const uint32_t* rx = reinterpret_cast<const uint32_t*>(here) + lane;
+        const uint32_t* rg = reinterpret_cast<const uint32_t*>(here + kSubBytes<kRowBytes>) + lane;
+        auto token = [&](int j) {
+            F in = Pk::get(rx[j * 32]);
+            const Decay<V> r = decay_of<LOGIT>(Pk::get(rg[j * 32]));
+            if constexpr (COMP) in = mul(r.u, in);
+            all.B = step(r.a, r.lo, all.B, in);
+            extend(all, r);
+        };
+        if (m.valid == kAll && !m.begin) [[likely]] {
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) token(j);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kSub; ++j) {
+                if (!(m.valid >> j & 1)) continue;
+                if (PACKED && (m.begin >> j & 1)) {
+                    const int s = __shfl_sync(0xffffffffu, m.seq, j);
+                    all.B = load_floats<V>(a.init_state ? a.init_state + (size_t)s * d + c : nullptr, count);
+                    begins = true;
+                }
+                token(j);
+            }
+        }
+    }
+    if (begins) all.A = splat<V>(-1.f);
+    MapSlots<V>::write(maps, warp, lane, all);
+    __syncthreads();
+    if (warp == 0)
+        MapSlots<V>::write(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, chunk, lane,
+                           MapSlots<V>::template join_runs<PACKED, W>(maps, 0, W, lane));
 }
 
 template <typename T>
@@ -163,11 +249,21 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
     using Y = std::true_type;
     using N = std::false_type;
     TileArgs t = tile_args<T>(a);
-    t.cluster = cluster_size((long long)t.strips * a.batch, t.blocks, kFwdWarps, kFwdBlocks);
+    const long long units = (long long)t.strips * a.batch;
+    const Chunks ch = chunks_of(units, t.blocks, kFwdWarps, kFwdBlocks);
+    t.chunks = ch.count;
+    t.chunk_tiles = ch.tiles;
+    t.maps = static_cast<float*>(a.workspace);
     auto go = [&](auto logit, auto comp, auto packed) {
         constexpr bool L = decltype(logit)::value, C = decltype(comp)::value, K = decltype(packed)::value;
-        return launch_strips(scan_kernel<T, L, C, K>, a, t, kFwdWarps,
-                             kMeetingBytes<kChannels<T>, kFwdWarps> + kFwdWarps * kFwdSlots * kFwdSegBytes, st);
+        constexpr int V = kChannels<T>;
+        if (t.chunks > 1) {
+            const cudaError_t e = launch_ctas(chunk_map_kernel<T, L, C, K>, units * (t.chunks - 1), kMapWarps,
+                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kMapSlots * kFwdSegBytes, st, a, t);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_ctas(scan_kernel<T, L, C, K>, units * t.chunks, kFwdWarps,
+                           kMeetingBytes<V, kFwdWarps> + kFwdWarps * kFwdSlots * kFwdSegBytes, st, a, t);
     };
     auto packed = [&](auto logit, auto comp) { return a.cu ? go(logit, comp, Y{}) : go(logit, comp, N{}); };
     if (a.logit) return a.complement ? packed(Y{}, Y{}) : packed(Y{}, N{});

@@ -2,6 +2,7 @@
 // the kernels).
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -34,6 +35,7 @@ struct GatedArgs {
     float* span_states;  // [batch, ceil(seqlen / 64), channels]
     const float* dfinal_state;
     float* dinit_state;
+    void* workspace;  // gated_workspace_bytes
 };
 
 struct GatedStepArgs {
@@ -45,6 +47,8 @@ struct GatedStepArgs {
     int logit, complement, io_dtype;
 };
 
+// Workspace of the scans (the larger of the forward's and the backwards').
+size_t gated_workspace_bytes(int batch, int seqlen, int channels, int io_dtype);
 cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_gated_scan_bwd(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_gated_step(const GatedStepArgs& a, cudaStream_t stream);

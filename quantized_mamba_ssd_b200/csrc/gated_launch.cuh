@@ -8,14 +8,25 @@
 namespace ssd {
 namespace gated {
 
+constexpr int kFwdWarps = 8, kFwdBlocks = 2;  // of a CTA; CTAs per SM
+// Backward: segments from codes are smaller, 8 warps of them fit twice into an SM's shared memory,
+// where of full ones 4 warps fit three times.
+template <bool CKPT> constexpr int kBwdWarps = CKPT ? 8 : 4;
+template <bool CKPT> constexpr int kBwdBlocks = CKPT ? 2 : 3;
+constexpr int kMapWarps = 8;  // of the kernel that leaves the chunks' maps
+constexpr int kMaxChunks = 64;
+
 struct TileArgs {
-    int cluster;  // CTAs per strip
-    int strips;   // strips per row
-    int blocks;   // checkpoint blocks per row
-    int spans;    // spans per row
+    int strips;       // strips per row
+    int blocks;       // segments (checkpoint blocks) per row
+    int spans;        // spans per row
+    int chunks;       // CTAs per strip
+    int chunk_tiles;  // tiles of a chunk (the last one's may be fewer)
+    float* maps;      // workspace: [strip of all rows][chunk][map of 32 lanes]
     // what the start of every row is a multiple of (bytes): 16, 4 or less
     int align_x, align_gate, align_dy;
-    int whole_out, whole_codes;  // outputs can be written as whole words (codes: pairs of bytes)
+    // outputs are written as whole words (codes: pairs of bytes): aligned, and no lane has a part
+    int whole_out, whole_codes;
 };
 
 inline int alignment(const GatedRows& r, int elem) {
@@ -37,7 +48,7 @@ TileArgs tile_args(const GatedArgs& a) {
     t.align_x = alignment(a.x, elem);
     t.align_gate = alignment(a.gate, elem);
     t.align_dy = alignment(a.dy, elem);
-    t.whole_out = word_rows(a.y, elem) && word_rows(a.dx, elem) && word_rows(a.dgate, elem);
+    t.whole_out = a.channels % V == 0 && word_rows(a.y, elem) && word_rows(a.dx, elem) && word_rows(a.dgate, elem);
     auto all = [](auto... p) { return (reinterpret_cast<uintptr_t>(p) | ...); };
     if (a.x_q && !a.x.ptr) {  // backward from codes, rows of one byte per channel
         t.align_x = alignment({a.x_q, 0, a.channels}, 1);
@@ -58,53 +69,43 @@ inline int sm_count() {
     return sms;
 }
 
-// CTAs per strip, the R with the least waves(R) * steps(R) * (1 + the meeting's share of a step).
-// Every CTA of a strip stays for as long as the strip takes, so waves of CTAs count whole.  A
-// cluster's meeting adds 0.2 + 0.08 R of a step (measured on strips of 20011 and 65521 tokens: a
-// step of 1.5 us alone grows to 1.9 with 2 CTAs, 2.7 with 8, 4.5 with 16), so with strips for all
-// SMs R = 1 is best (256 strips of 2048 bf16 tokens: 38 us with 1, 46 with 2, 54 with 3), with
-// fewer a larger one (80 strips: 239, 237, 177 us, and 251 with 4, whose CTAs need two waves; 16
-// strips: 1373 us with 1, 296 with 8, 214 with 12, 244 with 16).
-inline int cluster_size(long long strips, int segments, int warps, int per_sm) {
+struct Chunks {
+    int count, tiles;  // chunks per strip, tiles per chunk
+};
+
+// Chunks per strip: the count with the least time by a model in steps of the scan (1.4 to 2 us).
+// A scan of S chunks takes ceil(tiles / S) steps and one to begin, times its CTAs per place (and
+// about 0.4 of the last wave's gaps), and its steps are 1.4 times as long with the SMs full as with
+// them empty; with S > 1 the maps before it take 0.85 of that again, and the second launch and its
+// start about 5 steps.  Measured, forward, bf16 and fp16: 16 strips of 512 tiles 760 us whole and
+// 155 in 16 chunks, 40 of 64 tiles 119 and 62 (6), 80 of 157 tiles 236 and 188 (3), 202 (6), 196
+// (8); 256 strips of 16 tiles 37 whole, 54 in 2 chunks; 75 fp32 strips of 10 tiles 29 whole, 40 in
+// 3 chunks.
+inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm) {
     const double room = (double)sm_count() * per_sm;
     const int tiles = (segments + warps - 1) / warps;
-    const int most = warps == 8 ? 12 : kMaxCluster;  // (clusters of 96 warps or fewer find their place)
-    int best = 1;
+    Chunks best{1, tiles};
     double least = 0;
-    for (int r = 1; r <= most && r <= tiles; ++r) {
-        const double cost = std::ceil(strips * r / room) * ((tiles + r - 1) / r) *
-                            (r > 1 ? 1.2 + 0.08 * r : 1.0);
-        if (r == 1 || cost < 0.97 * least) {
+    for (int s = 1; s <= kMaxChunks && s <= tiles; ++s) {
+        const int each = (tiles + s - 1) / s;
+        if ((tiles + each - 1) / each != s) continue;  // some chunk would be empty
+        const double full = strips * s / room;
+        const double scan = (full <= 1 ? 1.0 : full + 0.4) * (each + 1) * (1 + 0.4 * std::fmin(1.0, full));
+        const double cost = s == 1 ? scan : scan * 1.85 + 5;
+        if (s == 1 || cost < 0.97 * least) {
             least = cost;
-            best = r;
+            best = {s, each};
         }
     }
     return best;
 }
 
-// One launch of `warps` warps per CTA and t.cluster CTAs per strip.
-template <typename K>
-cudaError_t launch_strips(K kernel, const GatedArgs& a, const TileArgs& t, int warps, int smem,
-                          cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename K, typename... A>
+cudaError_t launch_ctas(K kernel, long long ctas, int warps, int smem, cudaStream_t st, A... args) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    if (t.cluster > 8) {  // beyond the portable size
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((long long)t.strips * a.batch * t.cluster));
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = t.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, a, t);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    kernel<<<static_cast<unsigned>(ctas), 32 * warps, smem, st>>>(args...);
+    return cudaGetLastError();
 }
 
 }  // namespace gated

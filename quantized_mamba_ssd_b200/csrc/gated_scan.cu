@@ -1,4 +1,6 @@
 // Gated linear recurrence: the choice of the scan kernels by type, and the decode step.
+#include <algorithm>
+
 #include "gated_launch.cuh"
 
 namespace ssd {
@@ -79,6 +81,18 @@ cudaError_t by_type(int io_dtype, F f) {
 }
 
 }  // namespace
+
+size_t gated_workspace_bytes(int batch, int seqlen, int channels, int io_dtype) {
+    const int lanes = io_dtype == SSD_IO_F32 ? 32 : 64;  // channels of a strip
+    const long long units = (long long)((channels + lanes - 1) / lanes) * batch;
+    const int segments = (seqlen + kSub - 1) / kSub;
+    auto bytes = [&](int warps, int per_sm) {
+        const int n = chunks_of(units, segments, warps, per_sm).count;
+        return n > 1 ? (size_t)units * n * MapSlots<1>::kFloats * sizeof(float) : 0;
+    };
+    return std::max({bytes(kFwdWarps, kFwdBlocks), bytes(kBwdWarps<false>, kBwdBlocks<false>),
+                     bytes(kBwdWarps<true>, kBwdBlocks<true>)});
+}
 
 cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t st) {
     return by_type(a.io_dtype, [&](auto zero) { return launch_gated_scan_as<decltype(zero)>(a, st); });

@@ -1,14 +1,19 @@
 // What the forward and the backward scan share: the walk along a strip, the joins of its parts, the
 // copies.
 //
-// A strip is the channels of 32 lanes (128 bytes of a token).  W warps of each of R CTAs of a
-// cluster share a strip and walk it in steps of W R segments of 16 tokens: each warp reduces its
-// segment to the affine map carry -> A carry + B, the maps meet in shared memory (with R > 1 those
-// of whole CTAs are sent to every CTA of the cluster, through distributed shared memory), and each
-// warp then computes the carry into its own segment - and, redundantly, the carry into the next
-// step.  Inputs are copied ahead asynchronously, each warp's own segments into its own shared
-// memory.  So every input is read once, no CTA waits on memory flags, and the order of all sums is
-// fixed.
+// A strip is the channels of 32 lanes (128 bytes of a token).  The W warps of a CTA share a strip
+// and walk it in steps of W segments of 16 tokens: each warp reduces its segment to the affine map
+// carry -> A carry + B, the maps meet in shared memory, and each warp then computes the carry into
+// its own segment - and, redundantly, the carry into the next step.  Inputs are copied ahead
+// asynchronously, each warp's own segments into its own shared memory, and are read once.
+//
+// With too few strips for the machine a strip is cut into chunks of tokens with a CTA each.  A
+// kernel before the scan then walks all chunks but the last one of each strip (no meetings: a warp
+// reduces a run of tokens to its map as it streams by) and leaves their maps in the workspace,
+// where the scan composes the carry into its chunk.  That reads two of the inputs twice, often from
+// the L2 cache; the alternatives cost more: in a cluster whose CTAs share a strip every step waits
+// for a meeting of them all (a step of 1.5 us became 2.9 us with 3 CTAs and 4.8 us with 12).
+// The order of all sums is fixed, and no CTA waits for another.
 #pragma once
 
 #include <type_traits>
@@ -22,7 +27,6 @@ namespace gated {
 constexpr int kSub = kBlock;                 // tokens of a segment: one checkpoint block
 constexpr uint32_t kAll = (1u << kSub) - 1;  // each of them
 constexpr int kRowBytes = 128;  // a token's channels of one warp
-constexpr int kMaxCluster = 16;  // (above 8: not on every part, but on this one)
 
 // ---------------------------------------------------------------------------------------
 // the channels of one token and lane: one 32-bit word, so that a warp's row is 128 bytes
@@ -54,13 +58,14 @@ template <> struct Pack<__nv_bfloat16> {
     }
 };
 
-// Row pointers may be aligned to less than that word, and the last strip may be narrower: `whole`
-// (the same in all lanes) says that neither is so; `count` is how many of the lane's channels exist.
+// Row pointers may be aligned to less than that word, and a lane may have some of its channels only:
+// `whole` (the same in all lanes) says that neither is so; `count` is how many of the lane's
+// channels exist.
 template <typename T>
 __device__ __forceinline__ void store_row(char* p, Vec<kChannels<T>> f, bool whole, int count) {
     const uint32_t r = Pack<T>::put(f);
     if (whole) {
-        *reinterpret_cast<uint32_t*>(p) = r;
+        if (count) *reinterpret_cast<uint32_t*>(p) = r;
     } else if (sizeof(T) == 2) {
         uint16_t* h = reinterpret_cast<uint16_t*>(p);
         if (count > 0) h[0] = static_cast<uint16_t>(r);
@@ -92,9 +97,6 @@ __device__ __forceinline__ void store_floats(float* p, Vec<V> f, int count) {
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
-}
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -149,16 +151,18 @@ template <int W>
 __device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int rows,
                                            int width, int align) {
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    if (align == 16 && rows == kSub && width >= W) [[likely]] {
+    if (align == 16 && rows == kSub) [[likely]] {
         constexpr int kPer = W / 16;      // pieces per row
         constexpr int kStep = 32 / kPer;  // rows per instruction
         const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
+        const int bytes = max(0, min(16, width - at));
         const uint32_t d = to + row * W + at;
-        const char* p = src + row * pitch + at;
+        const char* p = bytes ? src + row * pitch + at : src;
+        const long long by = bytes ? kStep * pitch : 0;
 #pragma unroll
         for (int i = 0; i < kSub / kStep; ++i) {
-            copy_async16(d + i * kStep * W, p);
-            p += kStep * pitch;
+            copy_async16(d + i * kStep * W, p, bytes);
+            p += by;
         }
     } else {
         // out of line: code that is not run would push the hot loop out of the instruction cache
@@ -205,68 +209,81 @@ __device__ __forceinline__ void block_scales(H2 top, uint32_t& e0, uint32_t& e1,
     most = both<T>(e0 == kExpNaN ? 0.f : 127.f * scale_of(e0), e1 == kExpNaN ? 0.f : 127.f * scale_of(e1));
 }
 
-// The codes of two channels in the low bytes of a word.
+// The codes of two channels in the two low bytes of a word (the others are not theirs).
 template <typename T, typename H2>
 __device__ __forceinline__ uint32_t block_codes(H2 v, H2 most, Vec<2> inv) {
     v = __hmax2(__hmin2(v, most), __hneg2(most));
     const Vec<2> f = fma(Pack<T>::get(*reinterpret_cast<const uint32_t*>(&v)), inv, splat<2>(kCodeMagic));
-    return __byte_perm(__float_as_uint(f.x.x), __float_as_uint(f.x.y), 0x0040) & 0xffffu;
+    return __byte_perm(__float_as_uint(f.x.x), __float_as_uint(f.x.y), 0x0040);
 }
 
-template <typename T, bool GATE, bool LOGIT>
-__device__ __forceinline__ void code_rows(const uint32_t* r, uint32_t valid, int8_t* q, uint8_t* e,
-                                          int d, bool whole, int count) {
+// `floor` and `ceil` limit the values first (a gate's; infinities limit nothing, NaN stays).  Out of
+// line: x and gate share the code, and scans without checkpoints do without it in their loop.
+template <typename T>
+__device__ __noinline__ void code_rows(const uint32_t* r, uint32_t valid, float floor, float ceil,
+                                       int8_t* q, uint8_t* e, int d, bool whole, int count) {
     constexpr int V = kChannels<T>;
     uint8_t* out = reinterpret_cast<uint8_t*>(q);
     if constexpr (V == 1) {
         auto held = [&](int j) {
-            const float v = __uint_as_float(r[j * 32]);
-            return GATE ? held_gate<LOGIT>(v) : v;
-        };
-        uint32_t top = 0;  // bits of the magnitudes: their order, NaN on top
-#pragma unroll 4
-        for (int j = 0; j < kSub; ++j)
-            if (valid >> j & 1) top = max(top, __float_as_uint(fabsf(held(j))));
-        const uint32_t ex = scale_exp(top);
-        const Coder coder(ex);
-#pragma unroll 4
-        for (int j = 0; j < kSub; ++j, out += d)
-            if ((valid >> j & 1) && count) *out = static_cast<uint8_t>(coder.code(held(j)));
-        if (count) *e = static_cast<uint8_t>(ex);
-    } else {
-        using H2 = decltype(both<T>(0.f, 0.f));
-        auto pair = [&](int j) {
-            const uint32_t w = r[j * 32];
-            return *reinterpret_cast<const H2*>(&w);
-        };
-        auto held = [&](H2 v) {
-            if constexpr (GATE) v = __hmax2_nan(v, both<T>(-16.f, -16.f));
-            if constexpr (GATE && LOGIT) v = __hmin2_nan(v, both<T>(16.f, 16.f));
+            float v = __uint_as_float(r[j * 32]);
+            if (v < floor) v = floor;
+            if (v > ceil) v = ceil;
             return v;
         };
-        H2 top = both<T>(0.f, 0.f);
+        uint32_t top = 0;  // bits of the magnitudes: their order, NaN on top
         if (valid == kAll) {
+            float v[kSub];
 #pragma unroll
-            for (int j = 0; j < kSub; ++j) top = __hmax2_nan(top, __habs2(held(pair(j))));
+            for (int j = 0; j < kSub; ++j) {
+                v[j] = held(j);
+                top = max(top, __float_as_uint(fabsf(v[j])));
+            }
+            const Coder coder(scale_exp(top));
+            if (count)
+#pragma unroll
+                for (int j = 0; j < kSub; ++j, out += d) *out = static_cast<uint8_t>(coder.code(v[j]));
         } else {
 #pragma unroll 1
             for (int j = 0; j < kSub; ++j)
-                if (valid >> j & 1) top = __hmax2_nan(top, __habs2(held(pair(j))));
-        }
-        uint32_t e0, e1;
-        H2 most;
-        Vec<2> inv;
-        block_scales<T>(top, e0, e1, most, inv);
-        auto code = [&](int j) { return block_codes<T>(held(pair(j)), most, inv); };
-        if (valid == kAll && whole) {
-#pragma unroll
+                if (valid >> j & 1) top = max(top, __float_as_uint(fabsf(held(j))));
+            const Coder coder(scale_exp(top));
+#pragma unroll 1
             for (int j = 0; j < kSub; ++j, out += d)
-                *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(code(j));
+                if ((valid >> j & 1) && count) *out = static_cast<uint8_t>(coder.code(held(j)));
+        }
+        if (count) *e = static_cast<uint8_t>(scale_exp(top));
+    } else {
+        using H2 = decltype(both<T>(0.f, 0.f));
+        const H2 lowest = both<T>(floor, floor), highest = both<T>(ceil, ceil);
+        auto held = [&](int j) {
+            const uint32_t w = r[j * 32];
+            return __hmin2_nan(__hmax2_nan(*reinterpret_cast<const H2*>(&w), lowest), highest);
+        };
+        H2 top = both<T>(0.f, 0.f), most;
+        uint32_t e0, e1;
+        Vec<2> inv;
+        if (valid == kAll && whole) {
+            H2 v[kSub];
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+                v[j] = held(j);
+                top = __hmax2_nan(top, __habs2(v[j]));
+            }
+            block_scales<T>(top, e0, e1, most, inv);
+            if (count)
+#pragma unroll
+                for (int j = 0; j < kSub; ++j, out += d)
+                    *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(block_codes<T>(v[j], most, inv));
         } else {
+#pragma unroll 1
+            for (int j = 0; j < kSub; ++j)
+                if (valid >> j & 1) top = __hmax2_nan(top, __habs2(held(j)));
+            block_scales<T>(top, e0, e1, most, inv);
 #pragma unroll 1
             for (int j = 0; j < kSub; ++j, out += d) {
                 if (!(valid >> j & 1)) continue;
-                const uint32_t w = code(j);
+                const uint32_t w = block_codes<T>(held(j), most, inv);
                 if (count > 0) out[0] = static_cast<uint8_t>(w);
                 if (count > 1) out[1] = static_cast<uint8_t>(w >> 8);
             }
@@ -324,34 +341,6 @@ __device__ __forceinline__ Map<V> join(const Map<V>& first, const Map<V>& second
     return r;
 }
 
-// ---------------------------------------------------------------------------------------
-// clusters
-// ---------------------------------------------------------------------------------------
-// All threads of all CTAs of the cluster meet: arrive, then wait.  Only the threads that sent maps
-// release: a release waits for every write the thread has in flight, its rows of the last step
-// included.
-__device__ __forceinline__ void cluster_arrive(bool sent) {
-    if (sent) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Address of this CTA's shared-memory word `p` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t remote_smem(const void* p, int rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void store_remote(uint32_t addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
-                 "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-
 // Maps of runs, [run][lane] as four floats each: A and B of two channels, or A, B and L of one.
 template <int V>
 struct MapSlots {
@@ -390,67 +379,37 @@ struct MapSlots {
             if (i >= from && i < to) all = join<PACKED>(all, m[i]);
         return all;
     }
-    // `carry` through runs 0 .. n - 1 <= N; returns what run `which` receives.
+    // `carry` through runs 0 .. N - 1; returns what run `which` receives.
     template <bool PACKED, int N>
-    static __device__ __forceinline__ Vec<V> carry_through(const float* s, int n, int which,
-                                                           int lane, Vec<V>& carry) {
+    static __device__ __forceinline__ Vec<V> carry_through(const float* s, int which, int lane,
+                                                           Vec<V>& carry) {
+        Map<V> m[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) m[i] = read(s, i, lane);
         Vec<V> mine = carry;
 #pragma unroll
-        for (int g = 0; g < N; g += 8) {
-            if (g >= n) break;
-            Map<V> m[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (g + i < N) m[i] = read(s, g + i, lane);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (g + i >= N || g + i >= n) break;
-                if (g + i == which) mine = carry;
-                carry = through<PACKED>(m[i], carry);
-            }
+        for (int i = 0; i < N; ++i) {
+            if (i == which) mine = carry;
+            carry = through<PACKED>(m[i], carry);
         }
         return mine;
     }
 };
 
-// Where the parts of a step meet: the maps of the CTA's warps and, sent by every CTA of the
-// cluster, those of whole tiles.  Two of each, used in turn: a buffer is written again two steps
-// later, when the step between has seen every reader past it.
-template <int V, int W>
-struct Meeting {
-    using Slots = MapSlots<V>;
-    float segs[2][W * Slots::kFloats];
-    float tiles[2][kMaxCluster * Slots::kFloats];
+// One step's meeting: every warp of the CTA gives the map of its segment and gets the carry into
+// it; `carry` goes on to the next step.  `order`: the warp's place in the recurrence (0 first).
+// The maps of two steps are kept in turn: a buffer is written again two steps later, when the
+// barrier of the step between has seen every reader past it.
+template <int V, int W> constexpr int kMeetingBytes = 2 * W * MapSlots<V>::kFloats * 4;
 
-    // Every warp of the cluster gives the map of its part and gets the carry into it; `carry` goes
-    // on to the next step.  `order`: the warp's place in the recurrence (0 first).
-    template <bool PACKED>
-    __device__ __forceinline__ Vec<V> meet(int k, int order, int R, int rank, const Map<V>& part,
-                                           Vec<V>& carry) {
-        const int lane = threadIdx.x & 31;
-        float* seg = segs[k & 1];
-        float* tile = tiles[k & 1];
-        Slots::write(seg, order, lane, part);
-        __syncthreads();
-        if (R == 1) return Slots::template carry_through<PACKED, W>(seg, W, order, lane, carry);
-        const bool sends = order == W - 1;
-        Map<V> before;  // from the tile's start to this warp's part
-        if (sends) {
-            before = Slots::template join_runs<PACKED, W>(seg, 0, W - 1, lane);
-            const Map<V> all = join<PACKED>(before, part);
-            for (int r = 0; r < R; ++r)
-                store_remote(remote_smem(tile + rank * Slots::kFloats + lane * 4, r), Slots::words(all));
-        }
-        cluster_arrive(sends);
-        if (!sends) before = Slots::template join_runs<PACKED, W>(seg, 0, order, lane);
-        cluster_wait();
-        const Vec<V> mine = Slots::template carry_through<PACKED, kMaxCluster>(tile, R, rank, lane, carry);
-        return through<PACKED>(before, mine);
-    }
-};
-
-template <int V, int W>
-constexpr int kMeetingBytes = (sizeof(Meeting<V, W>) + 127) / 128 * 128;
+template <bool PACKED, int W, int V>
+__device__ __forceinline__ Vec<V> meet(float* maps, int k, int order, const Map<V>& part, Vec<V>& carry) {
+    const int lane = threadIdx.x & 31;
+    float* m = maps + (k & 1) * W * MapSlots<V>::kFloats;
+    MapSlots<V>::write(m, order, lane, part);
+    __syncthreads();
+    return MapSlots<V>::template carry_through<PACKED, W>(m, order, lane, carry);
+}
 
 // ---------------------------------------------------------------------------------------
 // where the tokens of a segment stand in packed rows

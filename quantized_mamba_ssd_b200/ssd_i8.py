@@ -32,7 +32,8 @@ EXPORTED = ("ssd_i8_abi_version", "ssd_status_string", "ssd_i8_chunk_scan_worksp
             "ssd_i8_chunk_scan_varlen_workspace_size", "ssd_i8_chunk_scan_varlen",
             "ssd_i8_state_quantize", "ssd_i8_state_update_q8", "ssd_i8_chunk_scan_noalloc_status",
             "ssd_i8_gated_scan", "ssd_i8_gated_scan_bwd", "ssd_i8_gated_scan_bwd_ckpt",
-            "ssd_i8_gated_step", "ssd_i8_ckpt_pack", "ssd_i8_ckpt_unpack")
+            "ssd_i8_gated_step", "ssd_i8_ckpt_pack", "ssd_i8_ckpt_unpack",
+            "ssd_i8_gated_scan_workspace_size")
 
 # the gated recurrence: element types, forms of the gate and of the input (include/ssd_i8.h)
 IO_DTYPES = {"f32": (0, torch.float32), "f16": (1, torch.float16), "bf16": (3, torch.bfloat16)}
@@ -108,12 +109,15 @@ def library() -> ctypes.CDLL:
         lib.ssd_i8_chunk_scan_noalloc_status.argtypes = [vp]
         rows = [vp, ll, ll]
         lib.ssd_i8_gated_scan.restype = ci
-        lib.ssd_i8_gated_scan.argtypes = rows * 3 + [ci] * 3 + [vp, ci, ci, ci] + [vp] * 8
+        lib.ssd_i8_gated_scan.argtypes = rows * 3 + [ci] * 3 + [vp, ci, ci, ci] + [vp] * 8 + [sz, vp]
         lib.ssd_i8_gated_scan_bwd.restype = ci
-        lib.ssd_i8_gated_scan_bwd.argtypes = rows * 5 + [ci] * 3 + [vp, ci, ci, ci] + [vp] * 5
+        lib.ssd_i8_gated_scan_bwd.argtypes = (rows * 5 + [ci] * 3 + [vp, ci, ci, ci] + [vp] * 5 +
+                                              [sz, vp])
         lib.ssd_i8_gated_scan_bwd_ckpt.restype = ci
         lib.ssd_i8_gated_scan_bwd_ckpt.argtypes = (rows + [vp] * 4 + rows * 2 + [ci] * 3 +
-                                                   [vp, ci, ci, ci] + [vp] * 5)
+                                                   [vp, ci, ci, ci] + [vp] * 5 + [sz, vp])
+        lib.ssd_i8_gated_scan_workspace_size.restype = sz
+        lib.ssd_i8_gated_scan_workspace_size.argtypes = [ci] * 4
         lib.ssd_i8_gated_step.restype = ci
         lib.ssd_i8_gated_step.argtypes = [vp] * 4 + [ci] * 4 + [vp]
         lib.ssd_i8_ckpt_pack.restype = ci
@@ -633,6 +637,24 @@ def _like(x: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
+def _gated_workspace(workspace, like: torch.Tensor, b: int, l: int, d: int, code: int,
+                     dev: int) -> tuple:
+    """The workspace of a scan (allocated where the caller gave none), its pointer and its size."""
+    if workspace is None:
+        need = library().ssd_i8_gated_scan_workspace_size(b, l, d, code)
+        if not need:
+            return None, None, 0
+        workspace = like.new_empty(need, dtype=torch.uint8)
+    n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    return workspace, _flat(workspace, "workspace", torch.uint8, (n,), dev), n
+
+
+def ssd_i8_gated_scan_workspace_size(batch: int, seqlen: int, channels: int, dtype: str) -> int:
+    """Bytes of workspace of the gated scans, forward and backward ("f32", "f16" or "bf16")."""
+    return int(library().ssd_i8_gated_scan_workspace_size(batch, seqlen, channels,
+                                                          IO_DTYPES[dtype][0]))
+
+
 def _ckpt_ptrs(ckpt, shape: tuple, dev: int) -> tuple:
     if len(ckpt) != 4:
         raise ValueError("ckpt must hold x_q, x_e, gate_q and gate_e")
@@ -658,7 +680,8 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
                       final_state: Optional[torch.Tensor] = None,
                       y: Optional[torch.Tensor] = None,
                       span_states: Optional[torch.Tensor] = None,
-                      ckpt: Optional[GatedCkpt] = None, stream=None) -> torch.Tensor:
+                      ckpt: Optional[GatedCkpt] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gated linear recurrence h_t = a_t h_{t-1} + w_t x_t per channel, y_t = h_t (see
     ``ssd_i8_gated_scan`` in include/ssd_i8.h).
 
@@ -667,38 +690,41 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
     ``gate_form``: "log" (a = exp(gate)) or "logit" (a = sigmoid(gate)); ``input_form``: "plain"
     (w = 1) or "complement" (w = 1 - a).  init_state / final_state f32 [b,d] ([nseq,d] packed).
     For a backward pass: ``span_states`` f32 [b,ceil(l/64),d] ([ceil(T/64),d]) is written, and
-    ``ckpt`` (``ssd_i8_gated_ckpt_empty``) receives x and gate in 8 bits.  Returns y, of x's shape
-    and dtype; rows outside every packed sequence are left as they were."""
+    ``ckpt`` (``ssd_i8_gated_ckpt_empty``) receives x and gate in 8 bits.  ``workspace`` is a uint8
+    CUDA tensor of at least ``ssd_i8_gated_scan_workspace_size`` bytes; one is allocated through
+    torch when omitted.  Returns y, of x's shape and dtype; rows outside every packed sequence are left as they were."""
     dev = _gpu_of(x)
     if stream is not None or torch.cuda.current_device() != dev:
         with _on(dev, stream):
             return ssd_i8_gated_scan(x, gate, cu_seqlens, gate_form=gate_form,
                                      input_form=input_form, init_state=init_state,
                                      final_state=final_state, y=y, span_states=span_states,
-                                     ckpt=ckpt)
+                                     ckpt=ckpt, workspace=workspace)
     b, l, d, seqs, cu, nseq = _gated_shape(x, "x", cu_seqlens, dev)
     code, dt, shape = _io_code(x, "x"), x.dtype, x.shape
     form = _form(gate_form, input_form)
     rows = (*_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev))
     if y is None:
         y = _like(x)
+    ws, pws, nws = _gated_workspace(workspace, x, b, l, d, code, dev)
     _check("ssd_i8_gated_scan", library().ssd_i8_gated_scan(
         *rows, *_rows(y, "y", dt, shape, dev), b, l, d, cu, nseq, form, code,
         _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
         _flat(final_state, "final_state", torch.float32, (seqs, d), dev),
         None if span_states is None else
         _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
-        *((None,) * 4 if ckpt is None else _ckpt_ptrs(ckpt, shape, dev)), _raw_stream(dev)))
+        *((None,) * 4 if ckpt is None else _ckpt_ptrs(ckpt, shape, dev)), pws, nws,
+        _raw_stream(dev)))
     return y
 
 
 def _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form, init_state,
-               dfinal_state, dinit_state, dx, dgate, stream):
+               dfinal_state, dinit_state, dx, dgate, workspace, stream):
     dev = _gpu_of(dy)
     if stream is not None or torch.cuda.current_device() != dev:
         with _on(dev, stream):
             return _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form,
-                              init_state, dfinal_state, dinit_state, dx, dgate, None)
+                              init_state, dfinal_state, dinit_state, dx, dgate, workspace, None)
     b, l, d, seqs, cu, nseq = _gated_shape(dy, "dy", cu_seqlens, dev)
     code, dt, shape = _io_code(dy, "dy"), dy.dtype, dy.shape
     form = _form(gate_form, input_form)
@@ -709,13 +735,15 @@ def _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form,
         dx = _like(dy)
     if dgate is None:
         dgate = _like(dy)
+    ws, pws, nws = _gated_workspace(workspace, dy, b, l, d, code, dev)
     _check(name, getattr(library(), name)(
         *rows, *_rows(dx, "dx", dt, shape, dev), *_rows(dgate, "dgate", dt, shape, dev),
         b, l, d, cu, nseq, form, code,
         _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
         _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
         _flat(dfinal_state, "dfinal_state", torch.float32, (seqs, d), dev),
-        _flat(dinit_state, "dinit_state", torch.float32, (seqs, d), dev), _raw_stream(dev)))
+        _flat(dinit_state, "dinit_state", torch.float32, (seqs, d), dev), pws, nws,
+        _raw_stream(dev)))
     return dx, dgate
 
 
@@ -726,7 +754,8 @@ def ssd_i8_gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor,
                           dfinal_state: Optional[torch.Tensor] = None,
                           dinit_state: Optional[torch.Tensor] = None,
                           dx: Optional[torch.Tensor] = None,
-                          dgate: Optional[torch.Tensor] = None, stream=None) -> tuple:
+                          dgate: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """Gradients (dx, dgate) of ``ssd_i8_gated_scan`` for the gradient ``dy`` of its output.
 
     x, gate, cu_seqlens, the forms and init_state as in the forward call, span_states as it wrote
@@ -736,7 +765,8 @@ def ssd_i8_gated_scan_bwd(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor,
     def inputs(dt, shape, dev):
         return (*_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev))
     return _gated_bwd("ssd_i8_gated_scan_bwd", dy, inputs, span_states, cu_seqlens, gate_form,
-                      input_form, init_state, dfinal_state, dinit_state, dx, dgate, stream)
+                      input_form, init_state, dfinal_state, dinit_state, dx, dgate, workspace,
+                      stream)
 
 
 def ssd_i8_gated_scan_bwd_ckpt(dy: torch.Tensor, ckpt: GatedCkpt, span_states: torch.Tensor,
@@ -746,14 +776,15 @@ def ssd_i8_gated_scan_bwd_ckpt(dy: torch.Tensor, ckpt: GatedCkpt, span_states: t
                                dfinal_state: Optional[torch.Tensor] = None,
                                dinit_state: Optional[torch.Tensor] = None,
                                dx: Optional[torch.Tensor] = None,
-                               dgate: Optional[torch.Tensor] = None, stream=None) -> tuple:
+                               dgate: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """``ssd_i8_gated_scan_bwd`` from the 8-bit checkpoints that the forward call wrote, in the
     place of x and gate."""
     def inputs(dt, shape, dev):
         return _ckpt_ptrs(ckpt, shape, dev)
     return _gated_bwd("ssd_i8_gated_scan_bwd_ckpt", dy, inputs, span_states, cu_seqlens,
                       gate_form, input_form, init_state, dfinal_state, dinit_state, dx, dgate,
-                      stream)
+                      workspace, stream)
 
 
 def ssd_i8_gated_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, *,

@@ -26,22 +26,23 @@ def rows(at, l=8, d=4):
 
 def scan(lib, **over):
     a = dict(x=rows(GB), gate=rows(2 * GB), y=rows(3 * GB), batch=2, l=8, d=4, cu=None, nseq=0,
-             form=0, io=0, init=None, final=None, spans=None, q=[None] * 4)
+             form=0, io=0, init=None, final=None, spans=None, q=[None] * 4, ws=20 * GB, wsb=1 << 24)
     a.update(over)
     return lib.ssd_i8_gated_scan(*a["x"], *a["gate"], *a["y"], a["batch"], a["l"], a["d"],
                                  a["cu"], a["nseq"], a["form"], a["io"], a["init"], a["final"],
-                                 a["spans"], *a["q"], None)
+                                 a["spans"], *a["q"], a["ws"], a["wsb"], None)
 
 
 def bwd(lib, ckpt=False, **over):
     a = dict(dy=rows(GB), x=rows(2 * GB), gate=rows(3 * GB), dx=rows(4 * GB), dgate=rows(5 * GB),
              q=[6 * GB, 7 * GB, 8 * GB, 9 * GB], batch=2, l=8, d=4, cu=None, nseq=0, form=0, io=0,
-             init=None, spans=10 * GB, dfinal=None, dinit=None)
+             init=None, spans=10 * GB, dfinal=None, dinit=None, ws=20 * GB, wsb=1 << 24)
     a.update(over)
     ins = a["q"] if ckpt else a["x"] + a["gate"]
     f = lib.ssd_i8_gated_scan_bwd_ckpt if ckpt else lib.ssd_i8_gated_scan_bwd
     return f(*a["dy"], *ins, *a["dx"], *a["dgate"], a["batch"], a["l"], a["d"], a["cu"],
-             a["nseq"], a["form"], a["io"], a["init"], a["spans"], a["dfinal"], a["dinit"], None)
+             a["nseq"], a["form"], a["io"], a["init"], a["spans"], a["dfinal"], a["dinit"], a["ws"],
+             a["wsb"], None)
 
 
 SHAPES = [
@@ -51,7 +52,7 @@ SHAPES = [
     (dict(cu=11 * GB + 2, nseq=3, batch=1), 1),  # misaligned offsets
     (dict(form=2), 1), (dict(form=32), 1), (dict(io=2), 1), (dict(io=4), 1),
     (dict(l=0x7fffffff), 2),                 # token indices past 32 bits with the last tile
-    (dict(batch=1 << 28, d=4), 2),           # 2^31 blocks
+    (dict(batch=1 << 25, d=4), 2),           # 2^31 CTAs with 64 chunks a strip
 ]
 
 
@@ -95,6 +96,25 @@ def test_backward_refuses_its_inputs(lib):
         q[k] = None
         assert bwd(lib, True, q=q) == 1
     assert bwd(lib, True, dgate=rows(8 * GB)) == 1
+
+
+LONG = dict(batch=1, l=20000, d=4, x=rows(GB, 20000), gate=rows(2 * GB, 20000))
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(ws=None), 3), (dict(wsb=16), 3), (dict(ws=20 * GB + 128), 3),  # missing, small, misaligned
+])
+def test_workspace_is_checked(lib, over, status):
+    need = lib.ssd_i8_gated_scan_workspace_size(1, 20000, 4, 0)
+    assert need > 512 and need % 512 == 0 and need <= 64 * 512
+    assert scan(lib, **LONG, y=rows(3 * GB, 20000), **over) == status
+    assert scan(lib, **LONG, y=[20 * GB - 256, 80000, 4]) == 1  # y runs into the workspace
+    for ckpt in (False, True):
+        assert bwd(lib, ckpt, **LONG, dy=rows(15 * GB, 20000), dx=rows(4 * GB, 20000),
+                   dgate=rows(5 * GB, 20000), **over) == status
+    f = lib.ssd_i8_gated_scan_workspace_size
+    assert f(0, 20000, 4, 0) == f(1, -1, 4, 0) == f(1, 20000, 0, 0) == f(1, 20000, 4, 2) == 0
+    assert f(64, 4096, 8192, 3) == 0  # enough strips for every SM
 
 
 def test_nothing_to_do_is_ok(lib):
