@@ -45,7 +45,8 @@ template <typename T, bool LOGIT, bool COMP, bool PACKED, bool CKPT>
 __global__ void __launch_bounds__(32 * kBwdWarps<CKPT>, kBwdBlocks<CKPT>)
 scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
     constexpr int V = kChannels<T>, kRow = kInRow<T, CKPT>;
-    constexpr bool kHold = COMP || LOGIT;  // the gradients need 1 - a
+    constexpr bool kUsesU = COMP || LOGIT;          // the gradients need 1 - a
+    constexpr bool kStates = !kUsesU && !CKPT;  // the states stay in registers as maps of the carry
     using Pk = Pack<T>;
     using F = Vec<V>;
     extern __shared__ __align__(128) uint8_t staged[];
@@ -105,7 +106,8 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         for (int s = warp; s < a.nseq; s += W)
             if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
                 store_floats<V>(a.dinit_state + (size_t)s * d + c, state_of(a.dfinal_state, s), count);
-    stage(0);
+#pragma unroll 1
+    for (int k = 0; k < kBwdSlots - 1; ++k) stage(k);
     for (int i = ta.chunks - 1; i > chunk; --i)  // through the chunks behind this one
         carry = through<PACKED>(MapSlots<V>::read(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, i, lane), carry);
     Held held;
@@ -163,12 +165,11 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
 
         // The segment's maps, both in one pass: of the state, and of the gradient, which from behind
         // the segment reaches its first token through the product of the decays and from token j
-        // through the product up to j.  Where the gradients only need the decays, the state behind
-        // token j is kept as the product P[j] and the rest B[j], which together with the carry give
-        // it at once; where they need 1 - a as well, decays and 1 - a are kept instead and the
-        // states computed again (both together do not fit the registers of three CTAs).
-        F P[kHold ? 1 : kSub], Q[kHold || V == 2 ? 1 : kSub], B[kHold ? 1 : kSub];
-        F da[kSub], lo[V == 1 ? kSub : 1], u[kHold ? kSub : 1];
+        // through the product up to j.  Where registers allow it (kStates), the state behind token j
+        // is kept as the product P[j] and the rest B[j], which together with the carry give it at
+        // once; else the states are computed again from the decays, which are kept in either case.
+        F P[kStates ? kSub : 1], Q[kStates && V == 1 ? kSub : 1], B[kStates ? kSub : 1];
+        F da[kSub], lo[V == 1 ? kSub : 1], u[kUsesU ? kSub : 1];
         Map<V> fwd = identity_map<V>(), back = identity_map<V>();
         // segments inside one sequence, by far the most, go without the checks of every token
         const bool inside = !PACKED || !(m.begin | m.end);
@@ -184,11 +185,11 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                     dy = add(dy, state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j)));
                 da[j] = r.a;
                 if constexpr (V == 1) lo[j] = r.lo;
-                if constexpr (kHold) u[j] = r.u;
+                if constexpr (kUsesU) u[j] = r.u;
                 if constexpr (COMP) in = mul(r.u, in);
                 fwd.B = step(r.a, r.lo, fwd.B, in);
                 extend(fwd, r);
-                if constexpr (!kHold) {
+                if constexpr (kStates) {
                     P[j] = fwd.A;
                     B[j] = fwd.B;
                     if constexpr (V == 1) Q[j] = fwd.L;
@@ -221,11 +222,11 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
                 const bool begins = CHECK && (m.begin >> j & 1);
-                if constexpr (kHold) {
+                if constexpr (!kStates) {
                     F in = x_of(j);
                     if (begins) before = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
                     past[j] = COMP ? sub(before, in) : before;
-                    if constexpr (COMP) in = mul(u[j], in);
+                    if constexpr (COMP) in = mul(u[kUsesU ? j : 0], in);
                     before = step(da[j], lo[V == 1 ? j : 0], before, in);
                 } else {
                     constexpr int none = 0;
@@ -243,9 +244,9 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                     e = state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j));
                 const F dh = add(Pk::get(rdy[j * 32]), e);
                 e = step(da[j], lo[V == 1 ? j : 0], dh, splat<V>(0.f));
-                const F dx = COMP ? mul(u[kHold ? j : 0], dh) : dh;
+                const F dx = COMP ? mul(u[kUsesU ? j : 0], dh) : dh;
                 F dg = mul(e, past[j]);
-                if constexpr (LOGIT) dg = mul(dg, u[kHold ? j : 0]);
+                if constexpr (LOGIT) dg = mul(dg, u[kUsesU ? j : 0]);
                 if (CHECK && (m.begin >> j & 1)) {
                     const int s = __shfl_sync(0xffffffffu, m.seq, j);
                     if (a.dinit_state) store_floats<V>(a.dinit_state + (size_t)s * d + c, e, count);

@@ -13,7 +13,10 @@ namespace gated {
 
 // A warp's staged segment: x and gate.
 constexpr int kFwdSegBytes = 2 * kSubBytes<kRowBytes>;
-constexpr int kFwdSlots = 2;
+// Segments in shared memory per warp: the current one and those ahead.  Two ahead are better where
+// copies are of 16 bytes (128 strips of 4096 bf16 tokens 42 us, with one ahead 47), one where they
+// are of words, which pass through the L1 cache that the rest of the memory leaves (72 us, not 83).
+inline int fwd_slots(const TileArgs& t) { return t.align_x == 16 && t.align_gate == 16 ? 3 : 2; }
 
 template <typename T, bool LOGIT, bool COMP, bool PACKED>
 __global__ void __launch_bounds__(32 * kFwdWarps, kFwdBlocks)
@@ -43,12 +46,12 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
 
     float* maps = reinterpret_cast<float*>(staged);
-    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kFwdSlots * kFwdSegBytes;
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * ta.slots * kFwdSegBytes;
     auto start = [&](int k) { return (first + k * W + warp) * kSub; };
-    auto stage = [&](int k) {  // this warp's segment of step k
+    auto stage = [&](int k, int slot) {  // this warp's segment of step k
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
-            uint8_t* to = own + k % kFwdSlots * kFwdSegBytes;
+            uint8_t* to = own + slot * kFwdSegBytes;
             stage_rows<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
             stage_rows<kRowBytes>(to + kSubBytes<kRowBytes>, pg + t * sg, sg, n, width, ta.align_gate);
         }
@@ -63,7 +66,9 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         for (int s = warp; s < a.nseq; s += W)
             if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
                 store_floats<V>(a.final_state + (size_t)s * d + c, init_of(s), count);
-    stage(0);
+#pragma unroll 1
+    for (int k = 0; k < ta.slots - 1; ++k) stage(k, k);
+    int slot = 0, free_slot = ta.slots - 1;
     for (int i = 0; i < chunk; ++i)  // through the chunks before this one
         carry = through<PACKED>(MapSlots<V>::read(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, i, lane), carry);
     Held held;
@@ -73,10 +78,13 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         m.valid = (1u << n) - 1;
         m.begin = m.end = 0;
         if constexpr (PACKED) m = marks_of(a.cu, a.nseq, t0, n, held);
-        copy_wait<kFwdSlots - 2>();
+        if (ta.slots == 3) copy_wait<1>();
+        else copy_wait<0>();
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
-        stage(k + kFwdSlots - 1);
-        uint8_t* here = own + k % kFwdSlots * kFwdSegBytes;
+        stage(k + ta.slots - 1, free_slot);
+        uint8_t* here = own + slot * kFwdSegBytes;
+        free_slot = slot;
+        slot = slot + 1 == ta.slots ? 0 : slot + 1;
         if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here, px + t0 * sx, sx);
         if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + kSubBytes<kRowBytes>, pg + t0 * sg, sg);
         uint32_t* rx = reinterpret_cast<uint32_t*>(here) + lane;
@@ -254,6 +262,7 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
     t.chunks = ch.count;
     t.chunk_tiles = ch.tiles;
     t.maps = static_cast<float*>(a.workspace);
+    t.slots = fwd_slots(t);
     auto go = [&](auto logit, auto comp, auto packed) {
         constexpr bool L = decltype(logit)::value, C = decltype(comp)::value, K = decltype(packed)::value;
         constexpr int V = kChannels<T>;
@@ -263,7 +272,7 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
             if (e != cudaSuccess) return e;
         }
         return launch_ctas(scan_kernel<T, L, C, K>, units * t.chunks, kFwdWarps,
-                           kMeetingBytes<V, kFwdWarps> + kFwdWarps * kFwdSlots * kFwdSegBytes, st, a, t);
+                           kMeetingBytes<V, kFwdWarps> + kFwdWarps * t.slots * kFwdSegBytes, st, a, t);
     };
     auto packed = [&](auto logit, auto comp) { return a.cu ? go(logit, comp, Y{}) : go(logit, comp, N{}); };
     if (a.logit) return a.complement ? packed(Y{}, Y{}) : packed(Y{}, N{});

@@ -22,6 +22,7 @@ struct TileArgs {
     int spans;        // spans per row
     int chunks;       // CTAs per strip
     int chunk_tiles;  // tiles of a chunk (the last one's may be fewer)
+    int slots;        // forward: segments in shared memory per warp
     float* maps;      // workspace: [strip of all rows][chunk][map of 32 lanes]
     // what the start of every row is a multiple of (bytes): 16, 4 or less
     int align_x, align_gate, align_dy;

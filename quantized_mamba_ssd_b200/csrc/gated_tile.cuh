@@ -107,8 +107,7 @@ template <int AHEAD> __device__ __forceinline__ void copy_wait() {  // all but t
     asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
 }
 
-// Room for kSub rows: the rows, and behind them one more word of each for rows that start inside
-// a word.
+// Room for kSub rows, with one more word for each that starts inside a word.
 template <int W> constexpr int kSubBytes = kSub * W + kSub * 4;
 
 // Rows at src + j * pitch (bytes); rows from `rows` on and bytes from `width` on become 0.  Where
@@ -116,34 +115,60 @@ template <int W> constexpr int kSubBytes = kSub * W + kSub * 4;
 // are not multiples of 4 either the words are those that hold the rows' bytes: realign_rows, once
 // they are here, moves each row to the start of its place.  Nothing but words that hold bytes of
 // the rows is read.
-template <int W>
-__device__ __noinline__ void stage_rows_any(uint32_t to, const char* src, long long pitch, int rows,
-                                            int width, int align) {
-    const int lane = threadIdx.x & 31;
-    if (align == 16) {
-        constexpr int kPer = W / 16, kStep = 32 / kPer;
-        const int row = lane / kPer, at = lane % kPer * 16;
-        for (int i = 0; i < kSub; i += kStep) {
-            const int bytes = row + i < rows ? max(0, min(16, width - at)) : 0;
-            copy_async16(to + (row + i) * W + at, bytes ? src + (row + i) * pitch + at : src, bytes);
+//
+// The copies of words are out of line, as is all code that most calls do not run: it would push the
+// hot loop out of the instruction cache.  Where a row starts inside its word only depends on its
+// number modulo 4.  Rows that start inside words take one word more (a pitch of W + 4 bytes).
+template <int W, bool ALIGNED>
+__device__ __noinline__ void stage_words(uint32_t to, const char* src, long long pitch, int rows,
+                                         int width) {
+    constexpr int kPer = W / 4, kStep = 32 / kPer;  // words per row, rows per instruction
+    constexpr int kPitch = ALIGNED ? W : W + 4;
+    const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 4;
+    const char* p[4];
+    int bytes[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // the lane's rows row + k * kStep + 4 * kStep * i
+        const char* first = src + (row + k * kStep) * pitch;
+        const int shift = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(first) & 3);
+        p[k] = first - shift + at;
+        bytes[k] = max(0, min(4, shift + width - at));
+    }
+    const long long by = 4 * kStep * pitch;
+    to += row * kPitch + at;
+    if (rows == kSub) {
+#pragma unroll
+        for (int i = 0; i < kSub / kStep; ++i) {
+            copy_async4(to + i * kStep * kPitch, p[i % 4], bytes[i % 4]);
+            p[i % 4] += by;
         }
-        return;
-    }
-    constexpr int kPer = W / 4, kStep = 32 / kPer;
-    const int row = lane / kPer, at = lane % kPer * 4;
-    const char* none = src - (reinterpret_cast<uintptr_t>(src) & 3);  // an address for copies of nothing
+    } else {
+        const char* none = src - (reinterpret_cast<uintptr_t>(src) & 3);  // an address for copies of nothing
 #pragma unroll 4
-    for (int i = 0; i < kSub; i += kStep) {
-        const char* p = src + (row + i) * pitch;
-        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
-        const int bytes = row + i < rows ? max(0, min(4, shift + width - at)) : 0;
-        copy_async4(to + (row + i) * W + at, bytes ? p - shift + at : none, bytes);
+        for (int i = 0; i < kSub / kStep; ++i) {
+            const int n = row + i * kStep < rows ? bytes[i % 4] : 0;
+            copy_async4(to + i * kStep * kPitch, n ? p[i % 4] : none, n);
+            p[i % 4] += by;
+        }
     }
-    if (align < 4 && lane < kSub) {
-        const char* p = src + lane * pitch;
-        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
-        const int bytes = lane < rows ? max(0, min(4, shift + width - W)) : 0;
-        copy_async4(to + kSub * W + lane * 4, bytes ? p - shift + W : none, bytes);
+    if (!ALIGNED && lane < kSub) {  // the last word of each row
+        const char* first = src + lane * pitch;
+        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(first) & 3);
+        const int n = lane < rows ? max(0, min(4, shift + width - W)) : 0;
+        copy_async4(to - (row * kPitch + at) + lane * kPitch + W,
+                    n ? first - shift + W : src - (reinterpret_cast<uintptr_t>(src) & 3), n);
+    }
+}
+
+// The last rows of a tensor whose rows are aligned.
+template <int W>
+__device__ __noinline__ void stage_tail(uint32_t to, const char* src, long long pitch, int rows,
+                                        int width) {
+    constexpr int kPer = W / 16, kStep = 32 / kPer;
+    const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
+    for (int i = 0; i < kSub; i += kStep) {
+        const int bytes = row + i < rows ? max(0, min(16, width - at)) : 0;
+        copy_async16(to + (row + i) * W + at, bytes ? src + (row + i) * pitch + at : src, bytes);
     }
 }
 
@@ -164,9 +189,12 @@ __device__ __forceinline__ void stage_rows(void* dst, const char* src, long long
             copy_async16(d + i * kStep * W, p, bytes);
             p += by;
         }
+    } else if (align == 16) {
+        stage_tail<W>(to, src, pitch, rows, width);
+    } else if (align == 4) {
+        stage_words<W, true>(to, src, pitch, rows, width);
     } else {
-        // out of line: code that is not run would push the hot loop out of the instruction cache
-        stage_rows_any<W>(to, src, pitch, rows, width, align);
+        stage_words<W, false>(to, src, pitch, rows, width);
     }
 }
 
@@ -176,15 +204,20 @@ __device__ __noinline__ void realign_rows(void* dst, const char* src, long long 
     constexpr int kPer = W / 4, kStep = 32 / kPer;
     const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer;
     uint32_t* w = static_cast<uint32_t*>(dst);
-#pragma unroll 4
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src));
+    uint32_t shift[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        shift[k] = 8 * ((base + (row + k * kStep) * static_cast<uint32_t>(pitch)) & 3);
+    uint32_t v[kSub / kStep];
+#pragma unroll
     for (int i = 0; i < kSub / kStep; ++i) {
-        const int r = row + i * kStep;
-        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src + r * pitch) & 3);
-        const uint32_t lo = w[r * kPer + at];
-        uint32_t hi = __shfl_down_sync(0xffffffffu, lo, 1, kPer);
-        if (at == kPer - 1) hi = w[kSub * kPer + r];
-        w[r * kPer + at] = __funnelshift_r(lo, hi, 8 * shift);
+        const uint32_t* first = w + (row + i * kStep) * (kPer + 1) + at;
+        v[i] = __funnelshift_r(first[0], first[1], shift[i % 4]);
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kSub / kStep; ++i) w[i * 32 + lane] = v[i];
     __syncwarp();
 }
 
