@@ -108,8 +108,11 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                 store_floats<V>(a.dinit_state + (size_t)s * d + c, state_of(a.dfinal_state, s), count);
 #pragma unroll 1
     for (int k = 0; k < kBwdSlots - 1; ++k) stage(k);
-    for (int i = ta.chunks - 1; i > chunk; --i)  // through the chunks behind this one
-        carry = through<PACKED>(MapSlots<V>::read(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, i, lane), carry);
+    if (ta.chunks > 1) {
+        wait_for_previous_kernel();
+        carry = through_chunks<PACKED>(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, ta.chunks - 1,
+                                       ta.chunks - 1 - chunk, -1, lane, carry);
+    }
     Held held;
     for (int k = 0; k < steps; ++k) {
         const int t0 = start(k), n = max(0, min(kSub, a.seqlen - t0));
@@ -356,6 +359,7 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
             }
         }
     }
+    allow_next_kernel();
     if (closed) all.A = splat<V>(-1.f);
     MapSlots<V>::write(maps, W - 1 - warp, lane, all);
     __syncthreads();
@@ -374,18 +378,19 @@ cudaError_t dispatch_bwd(const GatedArgs& a, cudaStream_t st) {
         constexpr int bytes = kBwdSegBytes<T, Q>;
         constexpr int W = kBwdWarps<Q>, V = kChannels<T>;
         const long long units = (long long)t.strips * a.batch;
-        const Chunks ch = chunks_of(units, t.blocks, W, kBwdBlocks<Q>);
+        const Chunks ch = chunks_of(units, t.blocks, W, kBwdBlocks<Q>, t.align_gate == 16 && t.align_dy == 16);
         t.chunks = ch.count;
         t.chunk_tiles = ch.tiles;
         t.maps = static_cast<float*>(a.workspace);
         if (t.chunks > 1) {
             const cudaError_t e = launch_ctas(chunk_back_kernel<T, LOGIT, K, Q>, units * (t.chunks - 1), kMapWarps,
                                               kMeetingBytes<V, kMapWarps> + kMapWarps * kBackSlots * kBackSegBytes<T, Q>,
-                                              st, a, t);
+                                              false, st, a, t);
             if (e != cudaSuccess) return e;
         }
         return launch_ctas(scan_bwd_kernel<T, LOGIT, C, K, Q>, units * t.chunks, W,
-                           kMeetingBytes<V, W> + kFwdMapBytes<V, W> + W * kBwdSlots * bytes, st, a, t);
+                           kMeetingBytes<V, W> + kFwdMapBytes<V, W> + W * kBwdSlots * bytes, t.chunks > 1,
+                           st, a, t);
     };
     auto packed = [&](auto comp, auto ckpt) { return a.cu ? go(comp, Y{}, ckpt) : go(comp, N{}, ckpt); };
     auto input = [&](auto ckpt) { return a.complement ? packed(Y{}, ckpt) : packed(N{}, ckpt); };

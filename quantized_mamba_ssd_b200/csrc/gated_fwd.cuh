@@ -69,8 +69,10 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
 #pragma unroll 1
     for (int k = 0; k < ta.slots - 1; ++k) stage(k, k);
     int slot = 0, free_slot = ta.slots - 1;
-    for (int i = 0; i < chunk; ++i)  // through the chunks before this one
-        carry = through<PACKED>(MapSlots<V>::read(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, i, lane), carry);
+    if (ta.chunks > 1) {
+        wait_for_previous_kernel();
+        carry = through_chunks<PACKED>(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, 0, chunk, 1, lane, carry);
+    }
     Held held;
     for (int k = 0; k < steps; ++k) {
         const int t0 = start(k), n = max(0, min(kSub, a.seqlen - t0));
@@ -244,6 +246,7 @@ chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Ti
             }
         }
     }
+    allow_next_kernel();
     if (begins) all.A = splat<V>(-1.f);
     MapSlots<V>::write(maps, warp, lane, all);
     __syncthreads();
@@ -258,7 +261,7 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
     using N = std::false_type;
     TileArgs t = tile_args<T>(a);
     const long long units = (long long)t.strips * a.batch;
-    const Chunks ch = chunks_of(units, t.blocks, kFwdWarps, kFwdBlocks);
+    const Chunks ch = chunks_of(units, t.blocks, kFwdWarps, kFwdBlocks, t.align_x == 16 && t.align_gate == 16);
     t.chunks = ch.count;
     t.chunk_tiles = ch.tiles;
     t.maps = static_cast<float*>(a.workspace);
@@ -268,11 +271,11 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
         constexpr int V = kChannels<T>;
         if (t.chunks > 1) {
             const cudaError_t e = launch_ctas(chunk_map_kernel<T, L, C, K>, units * (t.chunks - 1), kMapWarps,
-                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kMapSlots * kFwdSegBytes, st, a, t);
+                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kMapSlots * kFwdSegBytes, false, st, a, t);
             if (e != cudaSuccess) return e;
         }
         return launch_ctas(scan_kernel<T, L, C, K>, units * t.chunks, kFwdWarps,
-                           kMeetingBytes<V, kFwdWarps> + kFwdWarps * t.slots * kFwdSegBytes, st, a, t);
+                           kMeetingBytes<V, kFwdWarps> + kFwdWarps * t.slots * kFwdSegBytes, t.chunks > 1, st, a, t);
     };
     auto packed = [&](auto logit, auto comp) { return a.cu ? go(logit, comp, Y{}) : go(logit, comp, N{}); };
     if (a.logit) return a.complement ? packed(Y{}, Y{}) : packed(Y{}, N{});

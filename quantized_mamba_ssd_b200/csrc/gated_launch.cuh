@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cmath>
+#include <map>
+#include <mutex>
 
 #include "gated_tile.cuh"
 
@@ -78,11 +80,11 @@ struct Chunks {
 // A scan of S chunks takes ceil(tiles / S) steps and one to begin, times its CTAs per place (and
 // about 0.4 of the last wave's gaps), and its steps are 1.4 times as long with the SMs full as with
 // them empty; with S > 1 the maps before it take 0.85 of that again, and the second launch and its
-// start about 5 steps.  Measured, forward, bf16 and fp16: 16 strips of 512 tiles 760 us whole and
+// start about 4 steps (2 of the longer ones of rows that are copied as words).  Measured, forward, bf16 and fp16: 16 strips of 512 tiles 760 us whole and
 // 155 in 16 chunks, 40 of 64 tiles 119 and 62 (6), 80 of 157 tiles 236 and 188 (3), 202 (6), 196
 // (8); 256 strips of 16 tiles 37 whole, 54 in 2 chunks; 75 fp32 strips of 10 tiles 29 whole, 40 in
 // 3 chunks.
-inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm) {
+inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm, bool wide) {
     const double room = (double)sm_count() * per_sm;
     const int tiles = (segments + warps - 1) / warps;
     Chunks best{1, tiles};
@@ -92,7 +94,7 @@ inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm) {
         if ((tiles + each - 1) / each != s) continue;  // some chunk would be empty
         const double full = strips * s / room;
         const double scan = (full <= 1 ? 1.0 : full + 0.4) * (each + 1) * (1 + 0.4 * std::fmin(1.0, full));
-        const double cost = s == 1 ? scan : scan * 1.85 + 5;
+        const double cost = s == 1 ? scan : scan * 1.85 + (wide ? 4 : 2);
         if (s == 1 || cost < 0.97 * least) {
             least = cost;
             best = {s, each};
@@ -101,12 +103,42 @@ inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm) {
     return best;
 }
 
-template <typename K, typename... A>
-cudaError_t launch_ctas(K kernel, long long ctas, int warps, int smem, cudaStream_t st, A... args) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Lets a kernel use all of an SM's shared memory, once per device.
+template <typename... P>
+cudaError_t allow_smem(void (*kernel)(P...)) {
+    constexpr int kMost = 227 << 10, kDevices = 64;
+    static std::mutex lock;
+    static std::map<void (*)(P...), uint64_t> done;  // the devices of each kernel
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(ctas), 32 * warps, smem, st>>>(args...);
-    return cudaGetLastError();
+    const std::lock_guard<std::mutex> hold(lock);
+    uint64_t& mask = done[kernel];
+    if (dev < kDevices && (mask >> dev & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e == cudaSuccess && dev < kDevices) mask |= 1ull << dev;
+    return e;
+}
+
+// `follows`: the launch may begin while the one before it on the stream ends (the kernel waits for
+// it where it needs its results).
+template <typename K, typename... A>
+cudaError_t launch_ctas(K kernel, long long ctas, int warps, int smem, bool follows, cudaStream_t st,
+                        A... args) {
+    cudaError_t e = allow_smem(kernel);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = follows ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace gated

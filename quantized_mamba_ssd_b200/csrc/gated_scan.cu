@@ -87,7 +87,9 @@ size_t gated_workspace_bytes(int batch, int seqlen, int channels, int io_dtype) 
     const long long units = (long long)((channels + lanes - 1) / lanes) * batch;
     const int segments = (seqlen + kSub - 1) / kSub;
     auto bytes = [&](int warps, int per_sm) {
-        const int n = chunks_of(units, segments, warps, per_sm).count;
+        // the alignment of the rows is not known here
+        const int n = std::max(chunks_of(units, segments, warps, per_sm, true).count,
+                               chunks_of(units, segments, warps, per_sm, false).count);
         return n > 1 ? (size_t)units * n * MapSlots<1>::kFloats * sizeof(float) : 0;
     };
     return std::max({bytes(kFwdWarps, kFwdBlocks), bytes(kBwdWarps<false>, kBwdBlocks<false>),

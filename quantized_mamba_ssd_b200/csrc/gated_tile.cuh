@@ -429,6 +429,31 @@ struct MapSlots {
     }
 };
 
+// `carry` through the maps of `n` chunks in the workspace, from chunk `from` on, upward (by 1) or
+// downward (by -1), eight loads at a time.
+template <bool PACKED, int V>
+__device__ __forceinline__ Vec<V> through_chunks(const float* maps, int from, int n, int by, int lane,
+                                                 Vec<V> carry) {
+    for (int i = 0; i < n; i += 8) {
+        Map<V> m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = MapSlots<V>::read(maps, from + by * min(i + j, n - 1), lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < n) carry = through<PACKED>(m[j], carry);
+    }
+    return carry;
+}
+
+// The scan may start while the kernel of its chunks' maps ends: that kernel allows it once a CTA is
+// through its tokens, and the scan waits, its first copies on their way, before it reads the maps.
+__device__ __forceinline__ void allow_next_kernel() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous_kernel() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // One step's meeting: every warp of the CTA gives the map of its segment and gets the carry into
 // it; `carry` goes on to the next step.  `order`: the warp's place in the recurrence (0 first).
 // The maps of two steps are kept in turn: a buffer is written again two steps later, when the

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -151,8 +152,6 @@ def _on_device_of(t: torch.Tensor):
 
 def _device_call(fn):
     """Decorator: the wrapped call marshals and launches on the GPU of its first tensor."""
-    import functools
-
     @functools.wraps(fn)
     def wrapper(first, *args, **kwargs):
         with _on_device_of(first):
@@ -637,11 +636,17 @@ def _like(x: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
+@functools.lru_cache(maxsize=4096)
+def _gated_workspace_need(b: int, l: int, d: int, code: int, dev: int) -> int:
+    """The library's answer for the current device ``dev``, which only depends on these numbers."""
+    return library().ssd_i8_gated_scan_workspace_size(b, l, d, code)
+
+
 def _gated_workspace(workspace, like: torch.Tensor, b: int, l: int, d: int, code: int,
                      dev: int) -> tuple:
     """The workspace of a scan (allocated where the caller gave none), its pointer and its size."""
     if workspace is None:
-        need = library().ssd_i8_gated_scan_workspace_size(b, l, d, code)
+        need = _gated_workspace_need(b, l, d, code, dev)
         if not need:
             return None, None, 0
         workspace = like.new_empty(need, dtype=torch.uint8)
