@@ -17,7 +17,9 @@ namespace gated {
 // A warp's staged segment: x and gate (rows of 128 bytes, or codes, one byte per channel) and dy.
 template <typename T, bool CKPT> constexpr int kInRow = CKPT ? 32 * kChannels<T> : kRowBytes;
 template <typename T, bool CKPT>
-constexpr int kBwdSegBytes = 2 * kSubBytes<kInRow<T, CKPT>> + kSubBytes<kRowBytes>;
+__host__ __device__ constexpr int bwd_seg_bytes(bool words) {
+    return 2 * sub_bytes<kInRow<T, CKPT>>(words) + sub_bytes<kRowBytes>(words);
+}
 constexpr int kSpanSegs = kSpan / kSub;
 constexpr int kBwdSlots = 2;
 template <int V, int W> constexpr int kFwdMapBytes = 2 * W * MapSlots<V>::kFloats * 4;
@@ -84,16 +86,17 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
     // the gradient's maps meet; the state's only serve the warps of the same tile
     float* maps = reinterpret_cast<float*>(staged);
     float* fwds = reinterpret_cast<float*>(staged + kMeetingBytes<V, W>);
-    uint8_t* own = staged + kMeetingBytes<V, W> + kFwdMapBytes<V, W> + warp * kBwdSlots * kBwdSegBytes<T, CKPT>;
+    const int seg_bytes = bwd_seg_bytes<T, CKPT>(ta.words), in_bytes = sub_bytes<kRow>(ta.words);
+    uint8_t* own = staged + kMeetingBytes<V, W> + kFwdMapBytes<V, W> + warp * kBwdSlots * seg_bytes;
     // tiles of W segments, from the chunk's last one down
     auto start = [&](int k) { return ((low + steps - 1 - k) * W + warp) * kSub; };
     auto stage = [&](int k) {
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
-            uint8_t* to = own + k % kBwdSlots * kBwdSegBytes<T, CKPT>;
+            uint8_t* to = own + k % kBwdSlots * seg_bytes;
             stage_rows<kRow>(to, px + t * sx, sx, n, in_width, ta.align_x);
-            stage_rows<kRow>(to + kSubBytes<kRow>, pg + t * sg, sg, n, in_width, ta.align_gate);
-            stage_rows<kRowBytes>(to + 2 * kSubBytes<kRow>, pdy + t * sdy, sdy, n, width, ta.align_dy);
+            stage_rows<kRow>(to + in_bytes, pg + t * sg, sg, n, in_width, ta.align_gate);
+            stage_rows<kRowBytes>(to + 2 * in_bytes, pdy + t * sdy, sdy, n, width, ta.align_dy);
         }
         copy_commit();
     };
@@ -135,13 +138,13 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         copy_wait<kBwdSlots - 2>();
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
         stage(k + kBwdSlots - 1);
-        uint8_t* here = own + k % kBwdSlots * kBwdSegBytes<T, CKPT>;
+        uint8_t* here = own + k % kBwdSlots * seg_bytes;
         if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRow>(here, px + t0 * sx, sx);
-        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRow>(here + kSubBytes<kRow>, pg + t0 * sg, sg);
-        if (ta.align_dy < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + 2 * kSubBytes<kRow>, pdy + t0 * sdy, sdy);
+        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRow>(here + in_bytes, pg + t0 * sg, sg);
+        if (ta.align_dy < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + 2 * in_bytes, pdy + t0 * sdy, sdy);
         uint8_t* rx = here + lane * (kRow / 32);
-        uint8_t* rg = rx + kSubBytes<kRow>;
-        uint32_t* rdy = reinterpret_cast<uint32_t*>(here + 2 * kSubBytes<kRow>) + lane;
+        uint8_t* rg = rx + in_bytes;
+        uint32_t* rdy = reinterpret_cast<uint32_t*>(here + 2 * in_bytes) + lane;
         if (m.valid != kAll) [[unlikely]] {
             // tokens of no sequence pass state and gradient on: x and dy 0, decay 1 (each lane
             // mends its own words)
@@ -240,7 +243,6 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                     else past[j] = step(P[i], Q[V == 1 ? i : 0], before, B[i]);
                 }
             }
-            const bool plain = whole && m.valid == kAll;
 #pragma unroll
             for (int j = kSub - 1; j >= 0; --j) {
                 if (CHECK && (m.end >> j & 1))
@@ -254,18 +256,15 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                     const int s = __shfl_sync(0xffffffffu, m.seq, j);
                     if (a.dinit_state) store_floats<V>(a.dinit_state + (size_t)s * d + c, e, count);
                 }
-                if (plain) {
-                    store_row<T>(qdx, dx, true, count);
-                    store_row<T>(qdg, dg, true, count);
-                } else if (m.valid >> j & 1) {
-                    store_row<T>(qdx, dx, whole, count);
-                    store_row<T>(qdg, dg, whole, count);
+                if (!CHECK || (m.valid >> j & 1)) {
+                    store_row<T>(qdx, dx, !CHECK || whole, count);
+                    store_row<T>(qdg, dg, !CHECK || whole, count);
                 }
                 qdx -= sdx;
                 qdg -= sdg;
             }
         };
-        if (inside) [[likely]] gradients(std::false_type{});
+        if (inside && whole && m.valid == kAll) [[likely]] gradients(std::false_type{});
         else gradients(std::true_type{});
     }
     // the carry behind the first tile is the initial state's gradient, in every thread of its CTA
@@ -277,7 +276,9 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
 // segments of gate (or its codes) and dy, in the order of the tokens (see the scan's own map).
 constexpr int kBackSlots = 3;
 template <typename T, bool CKPT>
-constexpr int kBackSegBytes = kSubBytes<kInRow<T, CKPT>> + kSubBytes<kRowBytes>;
+__host__ __device__ constexpr int back_seg_bytes(bool words) {
+    return sub_bytes<kInRow<T, CKPT>>(words) + sub_bytes<kRowBytes>(words);
+}
 
 template <typename T, bool LOGIT, bool PACKED, bool CKPT>
 __global__ void __launch_bounds__(32 * kMapWarps)
@@ -302,13 +303,14 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
     const char* pdy = static_cast<const char*>(a.dy.ptr) + (b * a.dy.batch_stride + c0) * sizeof(T);
     const long long sdy = a.dy.token_stride * sizeof(T);
     float* maps = reinterpret_cast<float*>(staged);
-    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kBackSlots * kBackSegBytes<T, CKPT>;
+    const int seg_bytes = back_seg_bytes<T, CKPT>(ta.words), in_bytes = sub_bytes<kRow>(ta.words);
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kBackSlots * seg_bytes;
     auto stage = [&](int k) {
         const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
         if (k < run && n > 0) {
-            uint8_t* to = own + k % kBackSlots * kBackSegBytes<T, CKPT>;
+            uint8_t* to = own + k % kBackSlots * seg_bytes;
             stage_rows<kRow>(to, pg + t * sg, sg, n, CKPT ? min(kRow, d - c0) : width, ta.align_gate);
-            stage_rows<kRowBytes>(to + kSubBytes<kRow>, pdy + t * sdy, sdy, n, width, ta.align_dy);
+            stage_rows<kRowBytes>(to + in_bytes, pdy + t * sdy, sdy, n, width, ta.align_dy);
         }
         copy_commit();
     };
@@ -332,11 +334,11 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
         copy_wait<kBackSlots - 2>();
         __syncwarp();
         stage(k + kBackSlots - 1);
-        uint8_t* here = own + k % kBackSlots * kBackSegBytes<T, CKPT>;
+        uint8_t* here = own + k % kBackSlots * seg_bytes;
         if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRow>(here, pg + t0 * sg, sg);
-        if (ta.align_dy < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + kSubBytes<kRow>, pdy + t0 * sdy, sdy);
+        if (ta.align_dy < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + in_bytes, pdy + t0 * sdy, sdy);
         const uint8_t* rg = here + lane * (kRow / 32);
-        const uint32_t* rdy = reinterpret_cast<const uint32_t*>(here + kSubBytes<kRow>) + lane;
+        const uint32_t* rdy = reinterpret_cast<const uint32_t*>(here + in_bytes) + lane;
         auto token = [&](int j, F dy) {
             extend(all, decay_of<LOGIT>(row_value<T, CKPT>(rg + j * kRow, scale)));
             if (!PACKED || !closed) all.B = step(all.A, all.L, dy, all.B);
@@ -375,16 +377,16 @@ cudaError_t dispatch_bwd(const GatedArgs& a, cudaStream_t st) {
     TileArgs t = tile_args<T>(a);
     auto go = [&](auto comp, auto packed, auto ckpt) {
         constexpr bool C = decltype(comp)::value, K = decltype(packed)::value, Q = decltype(ckpt)::value;
-        constexpr int bytes = kBwdSegBytes<T, Q>;
+        const int bytes = bwd_seg_bytes<T, Q>(t.words);
         constexpr int W = kBwdWarps<Q>, V = kChannels<T>;
         const long long units = (long long)t.strips * a.batch;
-        const Chunks ch = chunks_of(units, t.blocks, W, kBwdBlocks<Q>, t.align_gate == 16 && t.align_dy == 16);
+        const Chunks ch = chunks_of(units, t.blocks, W, kBwdBlocks<Q>, t.aligned);
         t.chunks = ch.count;
         t.chunk_tiles = ch.tiles;
         t.maps = static_cast<float*>(a.workspace);
         if (t.chunks > 1) {
             const cudaError_t e = launch_ctas(chunk_back_kernel<T, LOGIT, K, Q>, units * (t.chunks - 1), kMapWarps,
-                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kBackSlots * kBackSegBytes<T, Q>,
+                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kBackSlots * back_seg_bytes<T, Q>(t.words),
                                               false, st, a, t);
             if (e != cudaSuccess) return e;
         }

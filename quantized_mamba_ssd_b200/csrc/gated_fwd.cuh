@@ -12,11 +12,10 @@ namespace ssd {
 namespace gated {
 
 // A warp's staged segment: x and gate.
-constexpr int kFwdSegBytes = 2 * kSubBytes<kRowBytes>;
-// Segments in shared memory per warp: the current one and those ahead.  Two ahead are better where
-// copies are of 16 bytes (128 strips of 4096 bf16 tokens 42 us, with one ahead 47), one where they
-// are of words, which pass through the L1 cache that the rest of the memory leaves (72 us, not 83).
-inline int fwd_slots(const TileArgs& t) { return t.align_x == 16 && t.align_gate == 16 ? 3 : 2; }
+__host__ __device__ inline int fwd_seg_bytes(const TileArgs& t) { return 2 * sub_bytes<kRowBytes>(t.words); }
+// Segments in shared memory per warp: the current one and those ahead, as many as leave room for a
+// second CTA (128 strips of 4096 bf16 tokens: 42 us with two ahead, 47 with one).
+inline int fwd_slots(const TileArgs& t) { return t.aligned ? 3 : 2; }
 
 template <typename T, bool LOGIT, bool COMP, bool PACKED>
 __global__ void __launch_bounds__(32 * kFwdWarps, kFwdBlocks)
@@ -46,14 +45,15 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
 
     float* maps = reinterpret_cast<float*>(staged);
-    uint8_t* own = staged + kMeetingBytes<V, W> + warp * ta.slots * kFwdSegBytes;
+    const int seg_bytes = fwd_seg_bytes(ta), gate_at = seg_bytes / 2;
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * ta.slots * seg_bytes;
     auto start = [&](int k) { return (first + k * W + warp) * kSub; };
     auto stage = [&](int k, int slot) {  // this warp's segment of step k
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
-            uint8_t* to = own + slot * kFwdSegBytes;
+            uint8_t* to = own + slot * seg_bytes;
             stage_rows<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
-            stage_rows<kRowBytes>(to + kSubBytes<kRowBytes>, pg + t * sg, sg, n, width, ta.align_gate);
+            stage_rows<kRowBytes>(to + gate_at, pg + t * sg, sg, n, width, ta.align_gate);
         }
         copy_commit();
     };
@@ -84,13 +84,13 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         else copy_wait<0>();
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
         stage(k + ta.slots - 1, free_slot);
-        uint8_t* here = own + slot * kFwdSegBytes;
+        uint8_t* here = own + slot * seg_bytes;
         free_slot = slot;
         slot = slot + 1 == ta.slots ? 0 : slot + 1;
         if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here, px + t0 * sx, sx);
-        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + kSubBytes<kRowBytes>, pg + t0 * sg, sg);
+        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + gate_at, pg + t0 * sg, sg);
         uint32_t* rx = reinterpret_cast<uint32_t*>(here) + lane;
-        uint32_t* rg = reinterpret_cast<uint32_t*>(here + kSubBytes<kRowBytes>) + lane;
+        uint32_t* rg = reinterpret_cast<uint32_t*>(here + gate_at) + lane;
         if (m.valid != kAll) [[unlikely]] {
             // tokens of no sequence keep the state: x 0, decay 1 (each lane mends its own words)
             for (int j = 0; j < kSub; ++j)
@@ -194,13 +194,14 @@ chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Ti
     const long long sx = a.x.token_stride * sizeof(T), sg = a.gate.token_stride * sizeof(T);
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
     float* maps = reinterpret_cast<float*>(staged);
-    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kMapSlots * kFwdSegBytes;
+    const int seg_bytes = fwd_seg_bytes(ta), gate_at = seg_bytes / 2;
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kMapSlots * seg_bytes;
     auto stage = [&](int k) {
         const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
         if (k < run && n > 0) {
-            uint8_t* to = own + k % kMapSlots * kFwdSegBytes;
+            uint8_t* to = own + k % kMapSlots * seg_bytes;
             stage_rows<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
-            stage_rows<kRowBytes>(to + kSubBytes<kRowBytes>, pg + t * sg, sg, n, width, ta.align_gate);
+            stage_rows<kRowBytes>(to + gate_at, pg + t * sg, sg, n, width, ta.align_gate);
         }
         copy_commit();
     };
@@ -218,11 +219,11 @@ chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Ti
         copy_wait<kMapSlots - 2>();
         __syncwarp();
         stage(k + kMapSlots - 1);
-        uint8_t* here = own + k % kMapSlots * kFwdSegBytes;
+        uint8_t* here = own + k % kMapSlots * seg_bytes;
         if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here, px + t0 * sx, sx);
-        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + kSubBytes<kRowBytes>, pg + t0 * sg, sg);
+        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + gate_at, pg + t0 * sg, sg);
         const uint32_t* rx = reinterpret_cast<const uint32_t*>(here) + lane;
-        const uint32_t* rg = reinterpret_cast<const uint32_t*>(here + kSubBytes<kRowBytes>) + lane;
+        const uint32_t* rg = reinterpret_cast<const uint32_t*>(here + gate_at) + lane;
         auto token = [&](int j) {
             F in = Pk::get(rx[j * 32]);
             const Decay<V> r = decay_of<LOGIT>(Pk::get(rg[j * 32]));
@@ -261,7 +262,7 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
     using N = std::false_type;
     TileArgs t = tile_args<T>(a);
     const long long units = (long long)t.strips * a.batch;
-    const Chunks ch = chunks_of(units, t.blocks, kFwdWarps, kFwdBlocks, t.align_x == 16 && t.align_gate == 16);
+    const Chunks ch = chunks_of(units, t.blocks, kFwdWarps, kFwdBlocks, t.aligned);
     t.chunks = ch.count;
     t.chunk_tiles = ch.tiles;
     t.maps = static_cast<float*>(a.workspace);
@@ -271,11 +272,11 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
         constexpr int V = kChannels<T>;
         if (t.chunks > 1) {
             const cudaError_t e = launch_ctas(chunk_map_kernel<T, L, C, K>, units * (t.chunks - 1), kMapWarps,
-                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kMapSlots * kFwdSegBytes, false, st, a, t);
+                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kMapSlots * fwd_seg_bytes(t), false, st, a, t);
             if (e != cudaSuccess) return e;
         }
         return launch_ctas(scan_kernel<T, L, C, K>, units * t.chunks, kFwdWarps,
-                           kMeetingBytes<V, kFwdWarps> + kFwdWarps * t.slots * kFwdSegBytes, t.chunks > 1, st, a, t);
+                           kMeetingBytes<V, kFwdWarps> + kFwdWarps * t.slots * fwd_seg_bytes(t), t.chunks > 1, st, a, t);
     };
     auto packed = [&](auto logit, auto comp) { return a.cu ? go(logit, comp, Y{}) : go(logit, comp, N{}); };
     if (a.logit) return a.complement ? packed(Y{}, Y{}) : packed(Y{}, N{});

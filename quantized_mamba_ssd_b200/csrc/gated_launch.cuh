@@ -1,6 +1,7 @@
 // Launches of the scan kernels: alignments, and how many warps share a strip.
 #pragma once
 
+#include <algorithm>
 #include <cmath>
 #include <map>
 #include <mutex>
@@ -26,8 +27,9 @@ struct TileArgs {
     int chunk_tiles;  // tiles of a chunk (the last one's may be fewer)
     int slots;        // forward: segments in shared memory per warp
     float* maps;      // workspace: [strip of all rows][chunk][map of 32 lanes]
-    // what the start of every row is a multiple of (bytes): 16, 4 or less
-    int align_x, align_gate, align_dy;
+    // what the start of every row is a multiple of (bytes): 16, 4 or less; whether that is 16 for all
+    // inputs, and whether it is at least 4
+    int align_x, align_gate, align_dy, aligned, words;
     // outputs are written as whole words (codes: pairs of bytes): aligned, and no lane has a part
     int whole_out, whole_codes;
 };
@@ -36,7 +38,7 @@ inline int alignment(const GatedRows& r, int elem) {
     const unsigned long long all = reinterpret_cast<uintptr_t>(r.ptr) |
                                    (unsigned long long)r.batch_stride * elem |
                                    (unsigned long long)r.token_stride * elem;
-    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : elem;
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : elem;  // what the start of every row is a multiple of
 }
 
 inline bool word_rows(const GatedRows& r, int elem) { return !r.ptr || alignment(r, elem) >= 4; }
@@ -50,13 +52,16 @@ TileArgs tile_args(const GatedArgs& a) {
     t.blocks = (a.seqlen + kBlock - 1) / kBlock;
     t.align_x = alignment(a.x, elem);
     t.align_gate = alignment(a.gate, elem);
-    t.align_dy = alignment(a.dy, elem);
+    t.align_dy = alignment(a.dy, elem);  // (16 for an input that the call does not have)
     t.whole_out = a.channels % V == 0 && word_rows(a.y, elem) && word_rows(a.dx, elem) && word_rows(a.dgate, elem);
     auto all = [](auto... p) { return (reinterpret_cast<uintptr_t>(p) | ...); };
     if (a.x_q && !a.x.ptr) {  // backward from codes, rows of one byte per channel
         t.align_x = alignment({a.x_q, 0, a.channels}, 1);
         t.align_gate = alignment({a.gate_q, 0, a.channels}, 1);
     }
+    const int least = std::min({t.align_x, t.align_gate, t.align_dy});
+    t.aligned = least == 16;
+    t.words = least >= 4;
     t.whole_codes = (all(a.x_q, a.gate_q, a.x_e, a.gate_e) | a.channels) % 2 == 0;
     return t;
 }
@@ -80,11 +85,11 @@ struct Chunks {
 // A scan of S chunks takes ceil(tiles / S) steps and one to begin, times its CTAs per place (and
 // about 0.4 of the last wave's gaps), and its steps are 1.4 times as long with the SMs full as with
 // them empty; with S > 1 the maps before it take 0.85 of that again, and the second launch and its
-// start about 4 steps (2 of the longer ones of rows that are copied as words).  Measured, forward, bf16 and fp16: 16 strips of 512 tiles 760 us whole and
+// start about 4 steps (2 of the longer ones of rows that are not aligned).  Measured, forward, bf16 and fp16: 16 strips of 512 tiles 760 us whole and
 // 155 in 16 chunks, 40 of 64 tiles 119 and 62 (6), 80 of 157 tiles 236 and 188 (3), 202 (6), 196
 // (8); 256 strips of 16 tiles 37 whole, 54 in 2 chunks; 75 fp32 strips of 10 tiles 29 whole, 40 in
 // 3 chunks.
-inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm, bool wide) {
+inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm, bool aligned) {
     const double room = (double)sm_count() * per_sm;
     const int tiles = (segments + warps - 1) / warps;
     Chunks best{1, tiles};
@@ -94,7 +99,7 @@ inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm, b
         if ((tiles + each - 1) / each != s) continue;  // some chunk would be empty
         const double full = strips * s / room;
         const double scan = (full <= 1 ? 1.0 : full + 0.4) * (each + 1) * (1 + 0.4 * std::fmin(1.0, full));
-        const double cost = s == 1 ? scan : scan * 1.85 + (wide ? 4 : 2);
+        const double cost = s == 1 ? scan : scan * 1.85 + (aligned ? 4 : 2);
         if (s == 1 || cost < 0.97 * least) {
             least = cost;
             best = {s, each};
