@@ -94,9 +94,15 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
             uint8_t* to = own + k % kBwdSlots * seg_bytes;
-            stage_rows<kRow>(to, px + t * sx, sx, n, in_width, ta.align_x);
-            stage_rows<kRow>(to + in_bytes, pg + t * sg, sg, n, in_width, ta.align_gate);
-            stage_rows<kRowBytes>(to + 2 * in_bytes, pdy + t * sdy, sdy, n, width, ta.align_dy);
+            if (ta.aligned && n == kSub) [[likely]] {
+                stage_rows<kRow>(to, px + t * sx, sx, in_width);
+                stage_rows<kRow>(to + in_bytes, pg + t * sg, sg, in_width);
+                stage_rows<kRowBytes>(to + 2 * in_bytes, pdy + t * sdy, sdy, width);
+            } else {
+                stage_any<kRow>(to, px + t * sx, sx, n, in_width, ta.align_x);
+                stage_any<kRow>(to + in_bytes, pg + t * sg, sg, n, in_width, ta.align_gate);
+                stage_any<kRowBytes>(to + 2 * in_bytes, pdy + t * sdy, sdy, n, width, ta.align_dy);
+            }
         }
         copy_commit();
     };
@@ -139,9 +145,11 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
         stage(k + kBwdSlots - 1);
         uint8_t* here = own + k % kBwdSlots * seg_bytes;
-        if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRow>(here, px + t0 * sx, sx);
-        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRow>(here + in_bytes, pg + t0 * sg, sg);
-        if (ta.align_dy < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + 2 * in_bytes, pdy + t0 * sdy, sdy);
+        if (!ta.words && n) [[unlikely]] {
+            if (ta.align_x < 4) realign_rows<kRow>(here, px + t0 * sx, sx);
+            if (ta.align_gate < 4) realign_rows<kRow>(here + in_bytes, pg + t0 * sg, sg);
+            if (ta.align_dy < 4) realign_rows<kRowBytes>(here + 2 * in_bytes, pdy + t0 * sdy, sdy);
+        }
         uint8_t* rx = here + lane * (kRow / 32);
         uint8_t* rg = rx + in_bytes;
         uint32_t* rdy = reinterpret_cast<uint32_t*>(here + 2 * in_bytes) + lane;
@@ -309,8 +317,14 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
         const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
         if (k < run && n > 0) {
             uint8_t* to = own + k % kBackSlots * seg_bytes;
-            stage_rows<kRow>(to, pg + t * sg, sg, n, CKPT ? min(kRow, d - c0) : width, ta.align_gate);
-            stage_rows<kRowBytes>(to + in_bytes, pdy + t * sdy, sdy, n, width, ta.align_dy);
+            const int in_width = CKPT ? min(kRow, d - c0) : width;
+            if (ta.aligned && n == kSub) [[likely]] {
+                stage_rows<kRow>(to, pg + t * sg, sg, in_width);
+                stage_rows<kRowBytes>(to + in_bytes, pdy + t * sdy, sdy, width);
+            } else {
+                stage_any<kRow>(to, pg + t * sg, sg, n, in_width, ta.align_gate);
+                stage_any<kRowBytes>(to + in_bytes, pdy + t * sdy, sdy, n, width, ta.align_dy);
+            }
         }
         copy_commit();
     };
@@ -335,8 +349,10 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
         __syncwarp();
         stage(k + kBackSlots - 1);
         uint8_t* here = own + k % kBackSlots * seg_bytes;
-        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRow>(here, pg + t0 * sg, sg);
-        if (ta.align_dy < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + in_bytes, pdy + t0 * sdy, sdy);
+        if (!ta.words && n) [[unlikely]] {
+            if (ta.align_gate < 4) realign_rows<kRow>(here, pg + t0 * sg, sg);
+            if (ta.align_dy < 4) realign_rows<kRowBytes>(here + in_bytes, pdy + t0 * sdy, sdy);
+        }
         const uint8_t* rg = here + lane * (kRow / 32);
         const uint32_t* rdy = reinterpret_cast<const uint32_t*>(here + in_bytes) + lane;
         auto token = [&](int j, F dy) {

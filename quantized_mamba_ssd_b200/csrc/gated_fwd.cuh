@@ -52,8 +52,13 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
             uint8_t* to = own + slot * seg_bytes;
-            stage_rows<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
-            stage_rows<kRowBytes>(to + gate_at, pg + t * sg, sg, n, width, ta.align_gate);
+            if (ta.aligned && n == kSub) [[likely]] {
+                stage_rows<kRowBytes>(to, px + t * sx, sx, width);
+                stage_rows<kRowBytes>(to + gate_at, pg + t * sg, sg, width);
+            } else {
+                stage_any<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
+                stage_any<kRowBytes>(to + gate_at, pg + t * sg, sg, n, width, ta.align_gate);
+            }
         }
         copy_commit();
     };
@@ -87,8 +92,10 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         uint8_t* here = own + slot * seg_bytes;
         free_slot = slot;
         slot = slot + 1 == ta.slots ? 0 : slot + 1;
-        if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here, px + t0 * sx, sx);
-        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + gate_at, pg + t0 * sg, sg);
+        if (!ta.words && n) [[unlikely]] {
+            if (ta.align_x < 4) realign_rows<kRowBytes>(here, px + t0 * sx, sx);
+            if (ta.align_gate < 4) realign_rows<kRowBytes>(here + gate_at, pg + t0 * sg, sg);
+        }
         uint32_t* rx = reinterpret_cast<uint32_t*>(here) + lane;
         uint32_t* rg = reinterpret_cast<uint32_t*>(here + gate_at) + lane;
         if (m.valid != kAll) [[unlikely]] {
@@ -200,8 +207,13 @@ chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Ti
         const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
         if (k < run && n > 0) {
             uint8_t* to = own + k % kMapSlots * seg_bytes;
-            stage_rows<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
-            stage_rows<kRowBytes>(to + gate_at, pg + t * sg, sg, n, width, ta.align_gate);
+            if (ta.aligned && n == kSub) [[likely]] {
+                stage_rows<kRowBytes>(to, px + t * sx, sx, width);
+                stage_rows<kRowBytes>(to + gate_at, pg + t * sg, sg, width);
+            } else {
+                stage_any<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
+                stage_any<kRowBytes>(to + gate_at, pg + t * sg, sg, n, width, ta.align_gate);
+            }
         }
         copy_commit();
     };
@@ -220,8 +232,10 @@ chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Ti
         __syncwarp();
         stage(k + kMapSlots - 1);
         uint8_t* here = own + k % kMapSlots * seg_bytes;
-        if (ta.align_x < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here, px + t0 * sx, sx);
-        if (ta.align_gate < 4 && n) [[unlikely]] realign_rows<kRowBytes>(here + gate_at, pg + t0 * sg, sg);
+        if (!ta.words && n) [[unlikely]] {
+            if (ta.align_x < 4) realign_rows<kRowBytes>(here, px + t0 * sx, sx);
+            if (ta.align_gate < 4) realign_rows<kRowBytes>(here + gate_at, pg + t0 * sg, sg);
+        }
         const uint32_t* rx = reinterpret_cast<const uint32_t*>(here) + lane;
         const uint32_t* rg = reinterpret_cast<const uint32_t*>(here + gate_at) + lane;
         auto token = [&](int j) {

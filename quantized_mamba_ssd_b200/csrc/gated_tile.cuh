@@ -122,7 +122,7 @@ template <int W> __host__ __device__ constexpr int sub_bytes(bool words) {
 // What most calls do not run is out of line: it would push the hot loop out of the instruction
 // cache.
 template <int W>
-__device__ __noinline__ void stage_words(uint32_t to, const char* src, long long pitch, int rows,
+__device__ __forceinline__ void stage_words(uint32_t to, const char* src, long long pitch, int rows,
                                          int width) {
     constexpr int kPer = W / 4, kStep = 32 / kPer;  // words per row, rows per instruction
     const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 4;
@@ -146,7 +146,7 @@ __device__ __noinline__ void stage_words(uint32_t to, const char* src, long long
 }
 
 template <int W>
-__device__ __noinline__ void stage_pieces(uint32_t to, const char* src, long long pitch, int rows,
+__device__ __forceinline__ void stage_pieces(uint32_t to, const char* src, long long pitch, int rows,
                                           int width) {
     constexpr int kPer = W / 16, kStep = 32 / kPer, kPitch = W + 16;
     const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
@@ -170,7 +170,7 @@ __device__ __noinline__ void stage_pieces(uint32_t to, const char* src, long lon
 
 // The last rows of a tensor whose rows are aligned.
 template <int W>
-__device__ __noinline__ void stage_tail(uint32_t to, const char* src, long long pitch, int rows,
+__device__ __forceinline__ void stage_tail(uint32_t to, const char* src, long long pitch, int rows,
                                         int width) {
     constexpr int kPer = W / 16, kStep = 32 / kPer;
     const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
@@ -180,30 +180,31 @@ __device__ __noinline__ void stage_tail(uint32_t to, const char* src, long long 
     }
 }
 
+// kSub whole rows that are aligned to 16 bytes.
 template <int W>
-__device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int rows,
-                                           int width, int align) {
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    if (align == 16 && rows == kSub) [[likely]] {
-        constexpr int kPer = W / 16;      // pieces per row
-        constexpr int kStep = 32 / kPer;  // rows per instruction
-        const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
-        const int bytes = max(0, min(16, width - at));
-        const uint32_t d = to + row * W + at;
-        const char* p = bytes ? src + row * pitch + at : src;
-        const long long by = bytes ? kStep * pitch : 0;
+__device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int width) {
+    constexpr int kPer = W / 16;      // pieces per row
+    constexpr int kStep = 32 / kPer;  // rows per instruction
+    const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
+    const int bytes = max(0, min(16, width - at));
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + row * W + at;
+    const char* p = bytes ? src + row * pitch + at : src;
+    const long long by = bytes ? kStep * pitch : 0;
 #pragma unroll
-        for (int i = 0; i < kSub / kStep; ++i) {
-            copy_async16(d + i * kStep * W, p, bytes);
-            p += by;
-        }
-    } else if (align == 16) {
-        stage_tail<W>(to, src, pitch, rows, width);
-    } else if (align == 4) {
-        stage_words<W>(to, src, pitch, rows, width);
-    } else {
-        stage_pieces<W>(to, src, pitch, rows, width);
+    for (int i = 0; i < kSub / kStep; ++i) {
+        copy_async16(d + i * kStep * W, p, bytes);
+        p += by;
     }
+}
+
+// Any others.
+template <int W>
+__device__ __noinline__ void stage_any(void* dst, const char* src, long long pitch, int rows,
+                                       int width, int align) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if (align == 16) stage_tail<W>(to, src, pitch, rows, width);
+    else if (align == 4) stage_words<W>(to, src, pitch, rows, width);
+    else stage_pieces<W>(to, src, pitch, rows, width);
 }
 
 // After the copies of rows that are not aligned to words: the same rows, each at the start of its
