@@ -1,10 +1,16 @@
-// Backward gated scan (the tile scheme is described in gated_tile.cuh).
+// Backward gated scan (the walk along strips is described in gated_tile.cuh).
 //
 // The gradient E_t that a sequence's tokens from t on send to h_{t-1} obeys E_t = a_t (E_{t+1} +
-// dy_t), a recurrence of the same kind in the other direction: the cluster walks the tiles from the
-// last one down.  The states h_{t-1} that dgate needs are rebuilt inside each tile from the state
-// that the forward pass saved before it, so x, gate and dy are read once and dx and dgate written
-// once, and nothing depends on the rounding of y.
+// dy_t), a recurrence of the same kind in the other direction: strips are walked from the last tile
+// down.  The states h_{t-1} that dgate needs are rebuilt in each segment from the state that the
+// forward pass saved before its span, so x, gate and dy are read once and dx and dgate written once,
+// and nothing depends on the rounding of y.
+//
+// What bounds it (one B200, of the measured copy bandwidth 6.47 TB/s): with enough strips HBM - 8 x
+// 4096 x 5120 bf16 293 us, 89 %; 2 x 16384 x 8192 logits with 1 - a weights 493 us, 85 %; 4 x 2048 x
+// 4096 bf16 63 us, 83 %, fp32 137 us, 76 % - else, and from codes (66 us, 64 %), the instructions.
+// The hot loop has to stay small and contiguous: with the tokens' checks of sequence borders and of
+// odd rows inside it instead of in loops of their own, the second took 760 us.
 #pragma once
 
 #include <type_traits>
@@ -47,8 +53,8 @@ template <typename T, bool LOGIT, bool COMP, bool PACKED, bool CKPT>
 __global__ void __launch_bounds__(32 * kBwdWarps<CKPT>, kBwdBlocks<CKPT>)
 scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
     constexpr int V = kChannels<T>, kRow = kInRow<T, CKPT>;
-    constexpr bool kUsesU = COMP || LOGIT;          // the gradients need 1 - a
-    constexpr bool kStates = !kUsesU && !CKPT;  // the states stay in registers as maps of the carry
+    constexpr bool kUsesU = COMP || LOGIT;  // the gradients need 1 - a
+    constexpr bool kStates = !kUsesU;       // the states stay in registers as maps of the carry
     using Pk = Pack<T>;
     using F = Vec<V>;
     extern __shared__ __align__(128) uint8_t staged[];
@@ -78,8 +84,10 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         sg = a.gate.token_stride * sizeof(T);
     }
     const char* pdy = static_cast<const char*>(a.dy.ptr) + (b * a.dy.batch_stride + c0) * sizeof(T);
-    char* pdx = static_cast<char*>(const_cast<void*>(a.dx.ptr)) + (b * a.dx.batch_stride + c0) * sizeof(T);
-    char* pdg = static_cast<char*>(const_cast<void*>(a.dgate.ptr)) + (b * a.dgate.batch_stride + c0) * sizeof(T);
+    char* pdx = static_cast<char*>(const_cast<void*>(a.dx.ptr)) +
+                (b * a.dx.batch_stride + c0) * sizeof(T);
+    char* pdg = static_cast<char*>(const_cast<void*>(a.dgate.ptr)) +
+                (b * a.dgate.batch_stride + c0) * sizeof(T);
     const long long sdy = a.dy.token_stride * sizeof(T), sdx = a.dx.token_stride * sizeof(T);
     const long long sdg = a.dgate.token_stride * sizeof(T);
 
@@ -119,8 +127,8 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
     for (int k = 0; k < kBwdSlots - 1; ++k) stage(k);
     if (ta.chunks > 1) {
         wait_for_previous_kernel();
-        carry = through_chunks<PACKED>(ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats, ta.chunks - 1,
-                                       ta.chunks - 1 - chunk, -1, lane, carry);
+        const float* of_chunks = ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats;
+        carry = through_chunks<PACKED>(of_chunks, ta.chunks - 1, ta.chunks - 1 - chunk, -1, lane, carry);
     }
     Held held;
     for (int k = 0; k < steps; ++k) {
@@ -168,10 +176,9 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                     }
                 }
         }
-        auto decoded = [&](const uint8_t* r, F scale, int j) { return row_value<T, CKPT>(r + j * kRow, scale); };
-        auto x_of = [&](int j) { return decoded(rx, scale_x, j); };
+        auto x_of = [&](int j) { return row_value<T, CKPT>(rx + j * kRow, scale_x); };
         auto gate_of = [&](int j) {
-            F g = decoded(rg, scale_g, j);
+            F g = row_value<T, CKPT>(rg + j * kRow, scale_g);
             // no code stands for the logit of a decay of 1
             if (CKPT && LOGIT && !(m.valid >> j & 1)) g = splat<V>(INFINITY);
             return g;
@@ -328,6 +335,7 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
         }
         copy_commit();
     };
+    const size_t blk0 = (size_t)b * ta.blocks;
     Map<V> all = identity_map<V>();
     bool closed = false;  // behind the first end nothing reaches the run's first token
     Held held;
@@ -344,7 +352,8 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 scale.set(v, n > 0 && v < count
-                                 ? scale_of(__ldg(a.gate_e + ((size_t)b * ta.blocks + first + k) * d + c + v)) : 0.f);
+                                 ? scale_of(__ldg(a.gate_e + (blk0 + first + k) * d + c + v))
+                                 : 0.f);
         copy_wait<kBackSlots - 2>();
         __syncwarp();
         stage(k + kBackSlots - 1);
@@ -370,7 +379,8 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
                 const bool ends = PACKED && (m.end >> j & 1);
                 if (ends) {
                     const int s = __shfl_sync(0xffffffffu, m.seq, j);
-                    dy = add(dy, load_floats<V>(a.dfinal_state ? a.dfinal_state + (size_t)s * d + c : nullptr, count));
+                    dy = add(dy, load_floats<V>(
+                                     a.dfinal_state ? a.dfinal_state + (size_t)s * d + c : nullptr, count));
                 }
                 token(j, dy);
                 closed |= ends;
@@ -401,14 +411,15 @@ cudaError_t dispatch_bwd(const GatedArgs& a, cudaStream_t st) {
         t.chunk_tiles = ch.tiles;
         t.maps = static_cast<float*>(a.workspace);
         if (t.chunks > 1) {
-            const cudaError_t e = launch_ctas(chunk_back_kernel<T, LOGIT, K, Q>, units * (t.chunks - 1), kMapWarps,
-                                              kMeetingBytes<V, kMapWarps> + kMapWarps * kBackSlots * back_seg_bytes<T, Q>(t.words),
-                                              false, st, a, t);
+            const int smem = kMeetingBytes<V, kMapWarps> +
+                             kMapWarps * kBackSlots * back_seg_bytes<T, Q>(t.words);
+            const cudaError_t e = launch_ctas<chunk_back_kernel<T, LOGIT, K, Q>>(
+                units * (t.chunks - 1), kMapWarps, smem, false, st, a, t);
             if (e != cudaSuccess) return e;
         }
-        return launch_ctas(scan_bwd_kernel<T, LOGIT, C, K, Q>, units * t.chunks, W,
-                           kMeetingBytes<V, W> + kFwdMapBytes<V, W> + W * kBwdSlots * bytes, t.chunks > 1,
-                           st, a, t);
+        return launch_ctas<scan_bwd_kernel<T, LOGIT, C, K, Q>>(
+            units * t.chunks, W, kMeetingBytes<V, W> + kFwdMapBytes<V, W> + W * kBwdSlots * bytes,
+            t.chunks > 1, st, a, t);
     };
     auto packed = [&](auto comp, auto ckpt) { return a.cu ? go(comp, Y{}, ckpt) : go(comp, N{}, ckpt); };
     auto input = [&](auto ckpt) { return a.complement ? packed(Y{}, ckpt) : packed(N{}, ckpt); };

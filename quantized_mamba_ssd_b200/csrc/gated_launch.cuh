@@ -1,19 +1,20 @@
-// Launches of the scan kernels: alignments, and how many warps share a strip.
+// Launches of the scan kernels: alignments, and into how many chunks a strip is cut.
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
-#include <map>
-#include <mutex>
 
 #include "gated_tile.cuh"
 
 namespace ssd {
 namespace gated {
 
-constexpr int kFwdWarps = 8, kFwdBlocks = 2;  // of a CTA; CTAs per SM
-// Backward: segments from codes are smaller, 8 warps of them fit twice into an SM's shared memory,
-// where of full ones 4 warps fit three times.
+// Warps of a CTA and CTAs per SM.  Forward, 8 warps and 128 registers: with 4 warps twice as many
+// steps, each with a barrier (256 strips of 2048 bf16 tokens: 38 us, with 4 warps 48).  Backward,
+// 168 registers: 4 warps fit three times, 8 only once (63 us, 81); segments from codes are smaller,
+// 8 warps of them fit twice, with 128 registers (66 us, with 4 warps 89).
+constexpr int kFwdWarps = 8, kFwdBlocks = 2;
 template <bool CKPT> constexpr int kBwdWarps = CKPT ? 8 : 4;
 template <bool CKPT> constexpr int kBwdBlocks = CKPT ? 2 : 3;
 constexpr int kMapWarps = 8;  // of the kernel that leaves the chunks' maps
@@ -34,11 +35,12 @@ struct TileArgs {
     int whole_out, whole_codes;
 };
 
+// What the start of every row is a multiple of.
 inline int alignment(const GatedRows& r, int elem) {
     const unsigned long long all = reinterpret_cast<uintptr_t>(r.ptr) |
                                    (unsigned long long)r.batch_stride * elem |
                                    (unsigned long long)r.token_stride * elem;
-    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : elem;  // what the start of every row is a multiple of
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : elem;
 }
 
 inline bool word_rows(const GatedRows& r, int elem) { return !r.ptr || alignment(r, elem) >= 4; }
@@ -53,7 +55,8 @@ TileArgs tile_args(const GatedArgs& a) {
     t.align_x = alignment(a.x, elem);
     t.align_gate = alignment(a.gate, elem);
     t.align_dy = alignment(a.dy, elem);  // (16 for an input that the call does not have)
-    t.whole_out = a.channels % V == 0 && word_rows(a.y, elem) && word_rows(a.dx, elem) && word_rows(a.dgate, elem);
+    t.whole_out = a.channels % V == 0 && word_rows(a.y, elem) && word_rows(a.dx, elem) &&
+                  word_rows(a.dgate, elem);
     auto all = [](auto... p) { return (reinterpret_cast<uintptr_t>(p) | ...); };
     if (a.x_q && !a.x.ptr) {  // backward from codes, rows of one byte per channel
         t.align_x = alignment({a.x_q, 0, a.channels}, 1);
@@ -85,10 +88,10 @@ struct Chunks {
 // A scan of S chunks takes ceil(tiles / S) steps and one to begin, times its CTAs per place (and
 // about 0.4 of the last wave's gaps), and its steps are 1.4 times as long with the SMs full as with
 // them empty; with S > 1 the maps before it take 0.85 of that again, and the second launch and its
-// start about 4 steps (2 of the longer ones of rows that are not aligned).  Measured, forward, bf16 and fp16: 16 strips of 512 tiles 760 us whole and
-// 155 in 16 chunks, 40 of 64 tiles 119 and 62 (6), 80 of 157 tiles 236 and 188 (3), 202 (6), 196
-// (8); 256 strips of 16 tiles 37 whole, 54 in 2 chunks; 75 fp32 strips of 10 tiles 29 whole, 40 in
-// 3 chunks.
+// start about 4 steps (2 of the longer ones of rows that are not aligned).
+// Measured, forward, bf16 and fp16: 16 strips of 512 tiles 760 us whole and 155 in 16 chunks, 40 of
+// 64 tiles 119 and 62 (6), 80 of 157 tiles 236 and 188 (3), 202 (6), 196 (8); 256 strips of 16 tiles
+// 37 whole, 54 in 2 chunks; 75 fp32 strips of 10 tiles 29 whole, 40 in 3 chunks.
 inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm, bool aligned) {
     const double room = (double)sm_count() * per_sm;
     const int tiles = (segments + warps - 1) / warps;
@@ -108,30 +111,22 @@ inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm, b
     return best;
 }
 
-// Lets a kernel use all of an SM's shared memory, once per device.
-template <typename... P>
-cudaError_t allow_smem(void (*kernel)(P...)) {
+// Launches `kernel` with all of an SM's shared memory allowed (asked for once per device; nothing
+// here allocates or throws).  `follows`: the launch may begin while the one before it on the stream
+// ends (the kernel waits for it where it needs its results).
+template <auto kernel, typename... A>
+cudaError_t launch_ctas(long long ctas, int warps, int smem, bool follows, cudaStream_t st, A... args) {
     constexpr int kMost = 227 << 10, kDevices = 64;
-    static std::mutex lock;
-    static std::map<void (*)(P...), uint64_t> done;  // the devices of each kernel
+    static std::atomic<uint64_t> allowed{0};  // bit: device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const std::lock_guard<std::mutex> hold(lock);
-    uint64_t& mask = done[kernel];
-    if (dev < kDevices && (mask >> dev & 1)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-    if (e == cudaSuccess && dev < kDevices) mask |= 1ull << dev;
-    return e;
-}
-
-// `follows`: the launch may begin while the one before it on the stream ends (the kernel waits for
-// it where it needs its results).
-template <typename K, typename... A>
-cudaError_t launch_ctas(K kernel, long long ctas, int warps, int smem, bool follows, cudaStream_t st,
-                        A... args) {
-    cudaError_t e = allow_smem(kernel);
-    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < kDevices ? 1ull << dev : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (e != cudaSuccess) return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(32 * warps);
