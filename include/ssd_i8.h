@@ -311,13 +311,15 @@ SSD_API ssd_status ssd_i8_chunk_cb(const int8_t *C, const int8_t *B, int batch, 
  * Conventions of these entry points, beside those at the top of this file:
  *   - x, gate, y, dy, dx and dgate have one element type, an SSD_IO_* code.  States and their
  *     gradients are float.  All arithmetic is fp32; a 16-bit output is rounded once.
+ *   - Infinities and NaN stay in their sequence and channel.  A state that is not finite stays so up
+ *     to its sequence's end; whether as an infinity or as a NaN is not specified.
  *   - x, gate, y, dy, dx and dgate are rows of `channels` contiguous elements, one per (batch,
  *     token), at ptr + batch * batch_stride + token * token_stride (strides in elements, >= 0).
  *     Input rows may overlap (stride 0).  Output rows may not: either batch_stride >=
  *     (seqlen - 1) * token_stride + channels with token_stride >= channels, or token_stride >=
  *     (batch - 1) * batch_stride + channels with batch_stride >= channels.  Pointers are aligned
- *     to their element; 16-bit rows are read two channels at a time where every pointer is 4-byte
- *     aligned and channels and strides are even.
+ *     to their element; rows of inputs that all start at multiples of 16 bytes are read fastest,
+ *     then those at multiples of 4.
  *   - cu_seqlens NULL: `batch` sequences of `seqlen` tokens.  Otherwise DEVICE int32 [nseq + 1]:
  *     batch is 1 and sequence s is tokens [cu_seqlens[s], cu_seqlens[s + 1]) of the `seqlen`
  *     packed ones, non-decreasing offsets inside [0, seqlen].  Its contents are read on the device

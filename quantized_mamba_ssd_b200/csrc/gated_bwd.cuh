@@ -406,7 +406,7 @@ cudaError_t dispatch_bwd(const GatedArgs& a, cudaStream_t st) {
         const int bytes = bwd_seg_bytes<T, Q>(t.words);
         constexpr int W = kBwdWarps<Q>, V = kChannels<T>;
         const long long units = (long long)t.strips * a.batch;
-        const Chunks ch = chunks_of(units, t.blocks, W, kBwdBlocks<Q>, t.aligned);
+        const Chunks ch = chunks_of(Q ? Work::kFromCodes : Work::kPlain, units, t.blocks, W, kBwdBlocks<Q>, t.aligned);
         t.chunks = ch.count;
         t.chunk_tiles = ch.tiles;
         t.maps = static_cast<float*>(a.workspace);

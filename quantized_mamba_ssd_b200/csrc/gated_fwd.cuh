@@ -285,7 +285,8 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
     using N = std::false_type;
     TileArgs t = tile_args<T>(a);
     const long long units = (long long)t.strips * a.batch;
-    const Chunks ch = chunks_of(units, t.blocks, kFwdWarps, kFwdBlocks, t.aligned);
+    const Chunks ch = chunks_of(a.x_q ? Work::kToCodes : Work::kPlain, units, t.blocks, kFwdWarps, kFwdBlocks,
+                                a.x_q ? t.words : t.aligned);
     t.chunks = ch.count;
     t.chunk_tiles = ch.tiles;
     t.maps = static_cast<float*>(a.workspace);

@@ -3,7 +3,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cmath>
 
 #include "gated_tile.cuh"
 
@@ -84,26 +83,38 @@ struct Chunks {
     int count, tiles;  // chunks per strip, tiles per chunk
 };
 
-// Chunks per strip: the count with the least time by a model in steps of the scan (1.4 to 2 us).
-// A scan of S chunks takes ceil(tiles / S) steps and one to begin, times its CTAs per place (and
-// about 0.4 of the last wave's gaps), and its steps are 1.4 times as long with the SMs full as with
-// them empty; with S > 1 the maps before it take 0.85 of that again, and the second launch and its
-// start about 4 steps (2 of the longer ones of rows that are not aligned).
-// Measured, forward, bf16 and fp16: 16 strips of 512 tiles 760 us whole and 155 in 16 chunks, 40 of
-// 64 tiles 119 and 62 (6), 80 of 157 tiles 236 and 188 (3), 202 (6), 196 (8); 256 strips of 16 tiles
-// 37 whole, 54 in 2 chunks; 75 fp32 strips of 10 tiles 29 whole, 40 in 3 chunks.
-inline Chunks chunks_of(long long strips, int segments, int warps, int per_sm, bool aligned) {
-    const double room = (double)sm_count() * per_sm;
+// Chunks per strip: the count with the least time by a model in steps of the scan (1.4 to 2 us, from
+// and to codes 2 to 4).  A scan of S chunks takes ceil(tiles / S) steps and one to begin, times its
+// CTAs per place (and about 0.4 of the last wave's gaps), and its steps are 1.4 times as long with
+// the SMs full as with them empty; with S > 1 the maps before it take 0.85 of that again, and the
+// second launch and its start about 4 steps (2 of the longer ones of rows that are not aligned).
+// Beside the longer steps of a scan from or to codes both are less.  (`easy`: rows that are copied
+// in 16-byte pieces; of a scan to codes, in words.)  Only the counts that fill one to four waves are
+// looked at.
+// Measured, whole and in S chunks: forward 16 strips of 512 fp16 tiles 726 us, 133 (S = 18); 40 of
+// 64 tiles 85, 41 (7); 80 of 157 bf16 tiles 200, 186 (3), 182 (8); 128 of 32 tiles 44, 53 (2); 75 of
+// 10 fp32 tiles 19.4, 20.4 (8).  Forward with codes, 48 bf16 strips of 4 tiles 11.6, 8.7 (4); 128 of
+// 32 tiles 77, 82 (2).  Backward from codes 13.2, 9.3 and 103, 98; 75 of 10 fp32 tiles 44, 38 (3).
+enum class Work { kPlain, kToCodes, kFromCodes };
+inline Chunks chunks_of(Work work, long long strips, int segments, int warps, int per_sm, bool easy) {
+    const long long room = (long long)sm_count() * per_sm;
     const int tiles = (segments + warps - 1) / warps;
+    const double maps = work == Work::kPlain ? 1.85 : work == Work::kToCodes ? 1.6 : 1.4;
+    const double second = work == Work::kPlain ? (easy ? 4 : 2) : (easy ? 1 : 0);
+    auto time = [&](int s, int each) {
+        const double full = (double)(strips * s) / room;
+        const double scan = (full <= 1 ? 1 : full + 0.4) * (each + 1) * (1 + 0.4 * (full < 1 ? full : 1));
+        return s == 1 ? scan : scan * maps + second;
+    };
     Chunks best{1, tiles};
-    double least = 0;
-    for (int s = 1; s <= kMaxChunks && s <= tiles; ++s) {
-        const int each = (tiles + s - 1) / s;
-        if ((tiles + each - 1) / each != s) continue;  // some chunk would be empty
-        const double full = strips * s / room;
-        const double scan = (full <= 1 ? 1.0 : full + 0.4) * (each + 1) * (1 + 0.4 * std::fmin(1.0, full));
-        const double cost = s == 1 ? scan : scan * 1.85 + (aligned ? 4 : 2);
-        if (s == 1 || cost < 0.97 * least) {
+    double least = time(1, tiles);
+    for (int waves = 1; waves <= 4; ++waves) {
+        const long long most = std::min<long long>({waves * room / strips, kMaxChunks, tiles});
+        if (most < 2) continue;
+        const int each = (tiles + (int)most - 1) / (int)most;
+        const int s = (tiles + each - 1) / each;  // no chunk is empty
+        const double cost = time(s, each);
+        if (s > 1 && cost < 0.97 * least) {
             least = cost;
             best = {s, each};
         }

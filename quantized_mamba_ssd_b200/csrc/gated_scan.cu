@@ -86,14 +86,13 @@ size_t gated_workspace_bytes(int batch, int seqlen, int channels, int io_dtype) 
     const int lanes = io_dtype == SSD_IO_F32 ? 32 : 64;  // channels of a strip
     const long long units = (long long)((channels + lanes - 1) / lanes) * batch;
     const int segments = (seqlen + kSub - 1) / kSub;
-    auto bytes = [&](int warps, int per_sm) {
-        // the alignment of the rows is not known here
-        const int n = std::max(chunks_of(units, segments, warps, per_sm, true).count,
-                               chunks_of(units, segments, warps, per_sm, false).count);
-        return n > 1 ? (size_t)units * n * MapSlots<1>::kFloats * sizeof(float) : 0;
-    };
-    return std::max({bytes(kFwdWarps, kFwdBlocks), bytes(kBwdWarps<false>, kBwdBlocks<false>),
-                     bytes(kBwdWarps<true>, kBwdBlocks<true>)});
+    int n = 1;
+    for (bool easy : {false, true})  // the alignment of the rows is not known here
+        n = std::max({n, chunks_of(Work::kPlain, units, segments, kFwdWarps, kFwdBlocks, easy).count,
+                      chunks_of(Work::kToCodes, units, segments, kFwdWarps, kFwdBlocks, easy).count,
+                      chunks_of(Work::kPlain, units, segments, kBwdWarps<false>, kBwdBlocks<false>, easy).count,
+                      chunks_of(Work::kFromCodes, units, segments, kBwdWarps<true>, kBwdBlocks<true>, easy).count});
+    return n > 1 ? (size_t)units * n * MapSlots<1>::kFloats * sizeof(float) : 0;
 }
 
 cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t st) {

@@ -697,7 +697,8 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
     For a backward pass: ``span_states`` f32 [b,ceil(l/64),d] ([ceil(T/64),d]) is written, and
     ``ckpt`` (``ssd_i8_gated_ckpt_empty``) receives x and gate in 8 bits.  ``workspace`` is a uint8
     CUDA tensor of at least ``ssd_i8_gated_scan_workspace_size`` bytes; one is allocated through
-    torch when omitted.  Returns y, of x's shape and dtype; rows outside every packed sequence are left as they were."""
+    torch when omitted.  Returns y, of x's shape and dtype; rows outside every packed sequence are
+    left as they were."""
     dev = _gpu_of(x)
     if stream is not None or torch.cuda.current_device() != dev:
         with _on(dev, stream):
@@ -782,7 +783,7 @@ def ssd_i8_gated_scan_bwd_ckpt(dy: torch.Tensor, ckpt: GatedCkpt, span_states: t
                                dinit_state: Optional[torch.Tensor] = None,
                                dx: Optional[torch.Tensor] = None,
                                dgate: Optional[torch.Tensor] = None,
-                          workspace: Optional[torch.Tensor] = None, stream=None) -> tuple:
+                               workspace: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """``ssd_i8_gated_scan_bwd`` from the 8-bit checkpoints that the forward call wrote, in the
     place of x and gate."""
     def inputs(dt, shape, dev):
