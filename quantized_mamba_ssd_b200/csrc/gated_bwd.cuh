@@ -7,8 +7,8 @@
 // and nothing depends on the rounding of y.
 //
 // What bounds it (one B200, of the measured copy bandwidth 6.47 TB/s): with enough strips HBM - 8 x
-// 4096 x 5120 bf16 293 us, 89 %; 2 x 16384 x 8192 logits with 1 - a weights 493 us, 85 %; 4 x 2048 x
-// 4096 bf16 63 us, 83 %, fp32 137 us, 76 % - else, and from codes (66 us, 64 %), the instructions.
+// 4096 x 5120 bf16 294 us, 89 %; 2 x 16384 x 8192 logits with 1 - a weights 486 us, 86 %; 4 x 2048 x
+// 4096 bf16 63 us, 83 %, fp32 135 us, 77 % - else, and from codes (66 us, 64 %), the instructions.
 // The hot loop has to stay small and contiguous: with the tokens' checks of sequence borders and of
 // odd rows inside it instead of in loops of their own, the second took 760 us.
 #pragma once
@@ -22,22 +22,20 @@ namespace gated {
 
 // A warp's staged segment: x and gate (rows of 128 bytes, or codes, one byte per channel) and dy.
 template <typename T, bool CKPT> constexpr int kInRow = CKPT ? 32 * kChannels<T> : kRowBytes;
-template <typename T, bool CKPT>
-__host__ __device__ constexpr int bwd_seg_bytes(bool words) {
-    return 2 * sub_bytes<kInRow<T, CKPT>>(words) + sub_bytes<kRowBytes>(words);
-}
+template <typename T, bool CKPT, bool ANY>
+constexpr int kBwdSegBytes = 2 * kSubBytes<kInRow<T, CKPT>, ANY> + kSubBytes<kRowBytes, ANY>;
 constexpr int kSpanSegs = kSpan / kSub;
 constexpr int kBwdSlots = 2;
 template <int V, int W> constexpr int kFwdMapBytes = 2 * W * MapSlots<V>::kFloats * 4;
 
 // The lane's channels of one staged row: values, or codes times their scales.
-template <typename T, bool CKPT>
+template <typename T, bool CKPT, bool ANY>
 __device__ __forceinline__ Vec<kChannels<T>> row_value(const uint8_t* r, Vec<kChannels<T>> scale) {
     constexpr int V = kChannels<T>;
     if constexpr (CKPT && V == 2) {
         // code + 128 in the low byte of 2^23 is that number as a float; times a power of two, and
         // less (2^23 + 128) of it, the value, all exact
-        const uint32_t q = *reinterpret_cast<const uint16_t*>(r) ^ 0x8080u;
+        const uint32_t q = (ANY ? r[0] | r[1] << 8 : *reinterpret_cast<const uint16_t*>(r)) ^ 0x8080u;
         Vec<2> f;
         f.x = make_float2(__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7440)),
                           __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7441)));
@@ -45,11 +43,11 @@ __device__ __forceinline__ Vec<kChannels<T>> row_value(const uint8_t* r, Vec<kCh
     } else if constexpr (CKPT) {
         return mul(Vec<1>{static_cast<float>(*reinterpret_cast<const int8_t*>(r))}, scale);
     } else {
-        return Pack<T>::get(*reinterpret_cast<const uint32_t*>(r));
+        return Pack<T>::get(row_word<T, ANY>(r));
     }
 }
 
-template <typename T, bool LOGIT, bool COMP, bool PACKED, bool CKPT>
+template <typename T, bool LOGIT, bool COMP, bool PACKED, bool CKPT, bool ANY>
 __global__ void __launch_bounds__(32 * kBwdWarps<CKPT>, kBwdBlocks<CKPT>)
 scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
     constexpr int V = kChannels<T>, kRow = kInRow<T, CKPT>;
@@ -94,22 +92,24 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
     // the gradient's maps meet; the state's only serve the warps of the same tile
     float* maps = reinterpret_cast<float*>(staged);
     float* fwds = reinterpret_cast<float*>(staged + kMeetingBytes<V, W>);
-    const int seg_bytes = bwd_seg_bytes<T, CKPT>(ta.words), in_bytes = sub_bytes<kRow>(ta.words);
-    uint8_t* own = staged + kMeetingBytes<V, W> + kFwdMapBytes<V, W> + warp * kBwdSlots * seg_bytes;
+    constexpr int kSeg = kBwdSegBytes<T, CKPT, ANY>, kIn = kSubBytes<kRow, ANY>;
+    uint8_t* own = staged + kMeetingBytes<V, W> + kFwdMapBytes<V, W> + warp * kBwdSlots * kSeg;
+    const int qx = staged_pitch<kRow, ANY>(sx), qg = staged_pitch<kRow, ANY>(sg);
+    const int qdy = staged_pitch<kRowBytes, ANY>(sdy);
     // tiles of W segments, from the chunk's last one down
     auto start = [&](int k) { return ((low + steps - 1 - k) * W + warp) * kSub; };
     auto stage = [&](int k) {
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
-            uint8_t* to = own + k % kBwdSlots * seg_bytes;
-            if (ta.aligned && n == kSub) [[likely]] {
-                stage_rows<kRow>(to, px + t * sx, sx, in_width);
-                stage_rows<kRow>(to + in_bytes, pg + t * sg, sg, in_width);
-                stage_rows<kRowBytes>(to + 2 * in_bytes, pdy + t * sdy, sdy, width);
+            uint8_t* to = own + k % kBwdSlots * kSeg;
+            if (ANY || n == kSub) [[likely]] {
+                stage_rows<kRow, ANY>(to, px + t * sx, sx, n, in_width);
+                stage_rows<kRow, ANY>(to + kIn, pg + t * sg, sg, n, in_width);
+                stage_rows<kRowBytes, ANY>(to + 2 * kIn, pdy + t * sdy, sdy, n, width);
             } else {
-                stage_any<kRow>(to, px + t * sx, sx, n, in_width, ta.align_x);
-                stage_any<kRow>(to + in_bytes, pg + t * sg, sg, n, in_width, ta.align_gate);
-                stage_any<kRowBytes>(to + 2 * in_bytes, pdy + t * sdy, sdy, n, width, ta.align_dy);
+                stage_tail<kRow>(to, px + t * sx, sx, n, in_width);
+                stage_tail<kRow>(to + kIn, pg + t * sg, sg, n, in_width);
+                stage_tail<kRowBytes>(to + 2 * kIn, pdy + t * sdy, sdy, n, width);
             }
         }
         copy_commit();
@@ -152,33 +152,29 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         copy_wait<kBwdSlots - 2>();
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
         stage(k + kBwdSlots - 1);
-        uint8_t* here = own + k % kBwdSlots * seg_bytes;
-        if (!ta.words && n) [[unlikely]] {
-            if (ta.align_x < 4) realign_rows<kRow>(here, px + t0 * sx, sx);
-            if (ta.align_gate < 4) realign_rows<kRow>(here + in_bytes, pg + t0 * sg, sg);
-            if (ta.align_dy < 4) realign_rows<kRowBytes>(here + 2 * in_bytes, pdy + t0 * sdy, sdy);
-        }
-        uint8_t* rx = here + lane * (kRow / 32);
-        uint8_t* rg = rx + in_bytes;
-        uint32_t* rdy = reinterpret_cast<uint32_t*>(here + 2 * in_bytes) + lane;
+        uint8_t* here = own + k % kBwdSlots * kSeg;
+        uint8_t* rx = here + staged_start<ANY>(px + t0 * sx) + lane * (kRow / 32);
+        uint8_t* rg = here + kIn + staged_start<ANY>(pg + t0 * sg) + lane * (kRow / 32);
+        uint8_t* rdy = here + 2 * kIn + staged_start<ANY>(pdy + t0 * sdy) + lane * 4;
         if (m.valid != kAll) [[unlikely]] {
             // tokens of no sequence pass state and gradient on: x and dy 0, decay 1 (each lane
             // mends its own words)
             for (int j = 0; j < kSub; ++j)
                 if (!(m.valid >> j & 1)) {
-                    rdy[j * 32] = 0;
+                    set_row_word<T, ANY>(rdy + j * qdy, 0u);
                     if constexpr (CKPT) {
 #pragma unroll
-                        for (int v = 0; v < V; ++v) rx[j * kRow + v] = rg[j * kRow + v] = 0;
+                        for (int v = 0; v < V; ++v) rx[j * qx + v] = rg[j * qg + v] = 0;
                     } else {
-                        *reinterpret_cast<uint32_t*>(rx + j * kRow) = 0;
-                        *reinterpret_cast<uint32_t*>(rg + j * kRow) = LOGIT ? Pk::kInf : 0u;
+                        set_row_word<T, ANY>(rx + j * qx, 0u);
+                        set_row_word<T, ANY>(rg + j * qg, LOGIT ? Pk::kInf : 0u);
                     }
                 }
         }
-        auto x_of = [&](int j) { return row_value<T, CKPT>(rx + j * kRow, scale_x); };
+        auto dy_of = [&](int j) { return Pk::get(row_word<T, ANY>(rdy + j * qdy)); };
+        auto x_of = [&](int j) { return row_value<T, CKPT, ANY>(rx + j * qx, scale_x); };
         auto gate_of = [&](int j) {
-            F g = row_value<T, CKPT>(rg + j * kRow, scale_g);
+            F g = row_value<T, CKPT, ANY>(rg + j * qg, scale_g);
             // no code stands for the logit of a decay of 1
             if (CKPT && LOGIT && !(m.valid >> j & 1)) g = splat<V>(INFINITY);
             return g;
@@ -198,7 +194,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
             constexpr bool CHECK = decltype(checks)::value;
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
-                F in = x_of(j), dy = Pk::get(rdy[j * 32]);
+                F in = x_of(j), dy = dy_of(j);
                 const Decay<V> r = decay_of<LOGIT>(gate_of(j));
                 if (CHECK && (m.begin >> j & 1))
                     fwd.B = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
@@ -262,7 +258,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
             for (int j = kSub - 1; j >= 0; --j) {
                 if (CHECK && (m.end >> j & 1))
                     e = state_of(a.dfinal_state, __shfl_sync(0xffffffffu, m.seq, j));
-                const F dh = add(Pk::get(rdy[j * 32]), e);
+                const F dh = add(dy_of(j), e);
                 e = step(da[j], lo[V == 1 ? j : 0], dh, splat<V>(0.f));
                 const F dx = COMP ? mul(u[kUsesU ? j : 0], dh) : dh;
                 F dg = mul(e, past[j]);
@@ -289,13 +285,11 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
 
 // The gradient's maps of all chunks but the first of every strip: each warp reduces a run of whole
 // segments of gate (or its codes) and dy, in the order of the tokens (see the scan's own map).
-constexpr int kBackSlots = 3;
-template <typename T, bool CKPT>
-__host__ __device__ constexpr int back_seg_bytes(bool words) {
-    return sub_bytes<kInRow<T, CKPT>>(words) + sub_bytes<kRowBytes>(words);
-}
+template <bool ANY> constexpr int kBackSlots = ANY ? 2 : 3;
+template <typename T, bool CKPT, bool ANY>
+constexpr int kBackSegBytes = kSubBytes<kInRow<T, CKPT>, ANY> + kSubBytes<kRowBytes, ANY>;
 
-template <typename T, bool LOGIT, bool PACKED, bool CKPT>
+template <typename T, bool LOGIT, bool PACKED, bool CKPT, bool ANY>
 __global__ void __launch_bounds__(32 * kMapWarps)
 chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
     constexpr int V = kChannels<T>, W = kMapWarps, kRow = kInRow<T, CKPT>;
@@ -318,19 +312,19 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
     const char* pdy = static_cast<const char*>(a.dy.ptr) + (b * a.dy.batch_stride + c0) * sizeof(T);
     const long long sdy = a.dy.token_stride * sizeof(T);
     float* maps = reinterpret_cast<float*>(staged);
-    const int seg_bytes = back_seg_bytes<T, CKPT>(ta.words), in_bytes = sub_bytes<kRow>(ta.words);
-    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kBackSlots * seg_bytes;
+    constexpr int kSlots = kBackSlots<ANY>, kSeg = kBackSegBytes<T, CKPT, ANY>, kIn = kSubBytes<kRow, ANY>;
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kSlots * kSeg;
+    const int qg = staged_pitch<kRow, ANY>(sg), qdy = staged_pitch<kRowBytes, ANY>(sdy);
     auto stage = [&](int k) {
         const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
         if (k < run && n > 0) {
-            uint8_t* to = own + k % kBackSlots * seg_bytes;
-            const int in_width = CKPT ? min(kRow, d - c0) : width;
-            if (ta.aligned && n == kSub) [[likely]] {
-                stage_rows<kRow>(to, pg + t * sg, sg, in_width);
-                stage_rows<kRowBytes>(to + in_bytes, pdy + t * sdy, sdy, width);
+            uint8_t* to = own + k % kSlots * kSeg;
+            if (ANY || n == kSub) [[likely]] {
+                stage_rows<kRow, ANY>(to, pg + t * sg, sg, n, CKPT ? min(kRow, d - c0) : width);
+                stage_rows<kRowBytes, ANY>(to + kIn, pdy + t * sdy, sdy, n, width);
             } else {
-                stage_any<kRow>(to, pg + t * sg, sg, n, in_width, ta.align_gate);
-                stage_any<kRowBytes>(to + in_bytes, pdy + t * sdy, sdy, n, width, ta.align_dy);
+                stage_tail<kRow>(to, pg + t * sg, sg, n, CKPT ? min(kRow, d - c0) : width);
+                stage_tail<kRowBytes>(to + kIn, pdy + t * sdy, sdy, n, width);
             }
         }
         copy_commit();
@@ -340,7 +334,7 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
     bool closed = false;  // behind the first end nothing reaches the run's first token
     Held held;
 #pragma unroll 1
-    for (int k = 0; k < kBackSlots - 1; ++k) stage(k);
+    for (int k = 0; k < kSlots - 1; ++k) stage(k);
     for (int k = 0; k < run; ++k) {
         const int t0 = (first + k) * kSub, n = max(0, min(kSub, a.seqlen - t0));
         Marks m;
@@ -354,28 +348,25 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
                 scale.set(v, n > 0 && v < count
                                  ? scale_of(__ldg(a.gate_e + (blk0 + first + k) * d + c + v))
                                  : 0.f);
-        copy_wait<kBackSlots - 2>();
+        copy_wait<kSlots - 2>();
         __syncwarp();
-        stage(k + kBackSlots - 1);
-        uint8_t* here = own + k % kBackSlots * seg_bytes;
-        if (!ta.words && n) [[unlikely]] {
-            if (ta.align_gate < 4) realign_rows<kRow>(here, pg + t0 * sg, sg);
-            if (ta.align_dy < 4) realign_rows<kRowBytes>(here + in_bytes, pdy + t0 * sdy, sdy);
-        }
-        const uint8_t* rg = here + lane * (kRow / 32);
-        const uint32_t* rdy = reinterpret_cast<const uint32_t*>(here + in_bytes) + lane;
+        stage(k + kSlots - 1);
+        uint8_t* here = own + k % kSlots * kSeg;
+        const uint8_t* rg = here + staged_start<ANY>(pg + t0 * sg) + lane * (kRow / 32);
+        const uint8_t* rdy = here + kIn + staged_start<ANY>(pdy + t0 * sdy) + lane * 4;
+        auto dy_of = [&](int j) { return Pk::get(row_word<T, ANY>(rdy + j * qdy)); };
         auto token = [&](int j, F dy) {
-            extend(all, decay_of<LOGIT>(row_value<T, CKPT>(rg + j * kRow, scale)));
+            extend(all, decay_of<LOGIT>(row_value<T, CKPT, ANY>(rg + j * qg, scale)));
             if (!PACKED || !closed) all.B = step(all.A, all.L, dy, all.B);
         };
         if (m.valid == kAll && !m.end) [[likely]] {
 #pragma unroll
-            for (int j = 0; j < kSub; ++j) token(j, Pk::get(rdy[j * 32]));
+            for (int j = 0; j < kSub; ++j) token(j, dy_of(j));
         } else {
 #pragma unroll 1
             for (int j = 0; j < kSub; ++j) {
                 if (!(m.valid >> j & 1)) continue;
-                F dy = Pk::get(rdy[j * 32]);
+                F dy = dy_of(j);
                 const bool ends = PACKED && (m.end >> j & 1);
                 if (ends) {
                     const int s = __shfl_sync(0xffffffffu, m.seq, j);
@@ -401,27 +392,30 @@ cudaError_t dispatch_bwd(const GatedArgs& a, cudaStream_t st) {
     using Y = std::true_type;
     using N = std::false_type;
     TileArgs t = tile_args<T>(a);
-    auto go = [&](auto comp, auto packed, auto ckpt) {
+    auto go = [&](auto comp, auto packed, auto ckpt, auto any) {
         constexpr bool C = decltype(comp)::value, K = decltype(packed)::value, Q = decltype(ckpt)::value;
-        const int bytes = bwd_seg_bytes<T, Q>(t.words);
+        constexpr bool A = decltype(any)::value;
         constexpr int W = kBwdWarps<Q>, V = kChannels<T>;
         const long long units = (long long)t.strips * a.batch;
-        const Chunks ch = chunks_of(Q ? Work::kFromCodes : Work::kPlain, units, t.blocks, W, kBwdBlocks<Q>, t.aligned);
+        const Chunks ch = chunks_of(Q ? Work::kFromCodes : Work::kPlain, units, t.blocks, W, kBwdBlocks<Q>,
+                                    t.aligned);
         t.chunks = ch.count;
         t.chunk_tiles = ch.tiles;
         t.maps = static_cast<float*>(a.workspace);
         if (t.chunks > 1) {
-            const int smem = kMeetingBytes<V, kMapWarps> +
-                             kMapWarps * kBackSlots * back_seg_bytes<T, Q>(t.words);
-            const cudaError_t e = launch_ctas<chunk_back_kernel<T, LOGIT, K, Q>>(
-                units * (t.chunks - 1), kMapWarps, smem, false, st, a, t);
+            constexpr int kSmem = kMeetingBytes<V, kMapWarps> + kMapWarps * kBackSlots<A> * kBackSegBytes<T, Q, A>;
+            const cudaError_t e = launch_ctas<chunk_back_kernel<T, LOGIT, K, Q, A>>(
+                units * (t.chunks - 1), kMapWarps, kSmem, false, st, a, t);
             if (e != cudaSuccess) return e;
         }
-        return launch_ctas<scan_bwd_kernel<T, LOGIT, C, K, Q>>(
-            units * t.chunks, W, kMeetingBytes<V, W> + kFwdMapBytes<V, W> + W * kBwdSlots * bytes,
-            t.chunks > 1, st, a, t);
+        constexpr int kSmem = kMeetingBytes<V, W> + kFwdMapBytes<V, W> + W * kBwdSlots * kBwdSegBytes<T, Q, A>;
+        return launch_ctas<scan_bwd_kernel<T, LOGIT, C, K, Q, A>>(units * t.chunks, W, kSmem, t.chunks > 1,
+                                                                  st, a, t);
     };
-    auto packed = [&](auto comp, auto ckpt) { return a.cu ? go(comp, Y{}, ckpt) : go(comp, N{}, ckpt); };
+    auto rows = [&](auto comp, auto packed, auto ckpt) {
+        return t.aligned ? go(comp, packed, ckpt, N{}) : go(comp, packed, ckpt, Y{});
+    };
+    auto packed = [&](auto comp, auto ckpt) { return a.cu ? rows(comp, Y{}, ckpt) : rows(comp, N{}, ckpt); };
     auto input = [&](auto ckpt) { return a.complement ? packed(Y{}, ckpt) : packed(N{}, ckpt); };
     return a.x_q ? input(Y{}) : input(N{});
 }

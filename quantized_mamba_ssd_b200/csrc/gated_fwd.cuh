@@ -7,8 +7,8 @@
 // element for the loads and conversions, and 16 dependent steps.)
 //
 // What bounds it (one B200, of the measured copy bandwidth 6.47 TB/s): with enough strips HBM - 8 x
-// 4096 x 5120 bf16 175 us, 89 %; 2 x 16384 x 8192 logits with 1 - a weights 300 us, 83 %; 4 x 2048 x
-// 4096 bf16 37 us, 84 %, fp32 77 us, 81 % - else the instructions: 18 per element (ncu), of which
+// 4096 x 5120 bf16 174 us, 90 %; 2 x 16384 x 8192 logits with 1 - a weights 295 us, 85 %; 4 x 2048 x
+// 4096 bf16 37 us, 84 %, fp32 76 us, 82 % - else the instructions: 18 per element (ncu), of which
 // half are the segment's own (copies, maps, meeting), at 2 per SM and cycle.
 #pragma once
 
@@ -20,12 +20,12 @@ namespace ssd {
 namespace gated {
 
 // A warp's staged segment: x and gate.
-__host__ __device__ inline int fwd_seg_bytes(const TileArgs& t) { return 2 * sub_bytes<kRowBytes>(t.words); }
+template <bool ANY> constexpr int kFwdSegBytes = 2 * kSubBytes<kRowBytes, ANY>;
 // Segments in shared memory per warp: the current one and those ahead, as many as leave room for a
 // second CTA (128 strips of 4096 bf16 tokens: 42 us with two ahead, 47 with one).
-inline int fwd_slots(const TileArgs& t) { return t.aligned ? 3 : 2; }
+template <bool ANY> constexpr int kFwdSlots = ANY ? 2 : 3;
 
-template <typename T, bool LOGIT, bool COMP, bool PACKED>
+template <typename T, bool LOGIT, bool COMP, bool PACKED, bool ANY>
 __global__ void __launch_bounds__(32 * kFwdWarps, kFwdBlocks)
 scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
     constexpr int V = kChannels<T>;
@@ -53,19 +53,20 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
 
     float* maps = reinterpret_cast<float*>(staged);
-    const int seg_bytes = fwd_seg_bytes(ta), gate_at = seg_bytes / 2;
-    uint8_t* own = staged + kMeetingBytes<V, W> + warp * ta.slots * seg_bytes;
+    constexpr int kSlots = kFwdSlots<ANY>, kSeg = kFwdSegBytes<ANY>, kGateAt = kSeg / 2;
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kSlots * kSeg;
+    const int qx = staged_pitch<kRowBytes, ANY>(sx), qg = staged_pitch<kRowBytes, ANY>(sg);
     auto start = [&](int k) { return (first + k * W + warp) * kSub; };
     auto stage = [&](int k, int slot) {  // this warp's segment of step k
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
-            uint8_t* to = own + slot * seg_bytes;
-            if (ta.aligned && n == kSub) [[likely]] {
-                stage_rows<kRowBytes>(to, px + t * sx, sx, width);
-                stage_rows<kRowBytes>(to + gate_at, pg + t * sg, sg, width);
+            uint8_t* to = own + slot * kSeg;
+            if (ANY || n == kSub) [[likely]] {
+                stage_rows<kRowBytes, ANY>(to, px + t * sx, sx, n, width);
+                stage_rows<kRowBytes, ANY>(to + kGateAt, pg + t * sg, sg, n, width);
             } else {
-                stage_any<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
-                stage_any<kRowBytes>(to + gate_at, pg + t * sg, sg, n, width, ta.align_gate);
+                stage_tail<kRowBytes>(to, px + t * sx, sx, n, width);
+                stage_tail<kRowBytes>(to + kGateAt, pg + t * sg, sg, n, width);
             }
         }
         copy_commit();
@@ -80,8 +81,8 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
             if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
                 store_floats<V>(a.final_state + (size_t)s * d + c, init_of(s), count);
 #pragma unroll 1
-    for (int k = 0; k < ta.slots - 1; ++k) stage(k, k);
-    int slot = 0, free_slot = ta.slots - 1;
+    for (int k = 0; k < kSlots - 1; ++k) stage(k, k);
+    int slot = 0, free_slot = kSlots - 1;
     if (ta.chunks > 1) {
         wait_for_previous_kernel();
         const float* of_chunks = ta.maps + (size_t)unit * ta.chunks * MapSlots<V>::kFloats;
@@ -94,31 +95,26 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         m.valid = (1u << n) - 1;
         m.begin = m.end = 0;
         if constexpr (PACKED) m = marks_of(a.cu, a.nseq, t0, n, held);
-        if (ta.slots == 3) copy_wait<1>();
-        else copy_wait<0>();
+        copy_wait<kSlots - 2>();
         __syncwarp();  // the segment is here, and every lane is done with the slot filled next
-        stage(k + ta.slots - 1, free_slot);
-        uint8_t* here = own + slot * seg_bytes;
+        stage(k + kSlots - 1, free_slot);
+        uint8_t* here = own + slot * kSeg;
         free_slot = slot;
-        slot = slot + 1 == ta.slots ? 0 : slot + 1;
-        if (!ta.words && n) [[unlikely]] {
-            if (ta.align_x < 4) realign_rows<kRowBytes>(here, px + t0 * sx, sx);
-            if (ta.align_gate < 4) realign_rows<kRowBytes>(here + gate_at, pg + t0 * sg, sg);
-        }
-        uint32_t* rx = reinterpret_cast<uint32_t*>(here) + lane;
-        uint32_t* rg = reinterpret_cast<uint32_t*>(here + gate_at) + lane;
+        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        uint8_t* rx = here + staged_start<ANY>(px + t0 * sx) + lane * 4;
+        uint8_t* rg = here + kGateAt + staged_start<ANY>(pg + t0 * sg) + lane * 4;
         if (m.valid != kAll) [[unlikely]] {
             // tokens of no sequence keep the state: x 0, decay 1 (each lane mends its own words)
             for (int j = 0; j < kSub; ++j)
                 if (!(m.valid >> j & 1)) {
-                    rx[j * 32] = 0;
-                    rg[j * 32] = LOGIT ? Pk::kInf : 0u;
+                    set_row_word<T, ANY>(rx + j * qx, 0u);
+                    set_row_word<T, ANY>(rg + j * qg, LOGIT ? Pk::kInf : 0u);
                 }
         }
         if (a.x_q && n > 0) {
             const size_t at = (row0 + t0) * d + c, be = ((size_t)b * ta.blocks + t0 / kBlock) * d + c;
-            code_rows<T>(rx, m.valid, -INFINITY, INFINITY, a.x_q + at, a.x_e + be, d, whole_codes, count);
-            code_rows<T>(rg, m.valid, -kHeldGate, LOGIT ? kHeldGate : INFINITY, a.gate_q + at,
+            code_rows<T, ANY>(rx, qx, m.valid, -INFINITY, INFINITY, a.x_q + at, a.x_e + be, d, whole_codes, count);
+            code_rows<T, ANY>(rg, qg, m.valid, -kHeldGate, LOGIT ? kHeldGate : INFINITY, a.gate_q + at,
                          a.gate_e + be, d, whole_codes, count);
         }
 
@@ -131,8 +127,8 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
             constexpr bool CHECK = decltype(checks)::value;
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
-                F in = Pk::get(rx[j * 32]);
-                const Decay<V> r = decay_of<LOGIT>(Pk::get(rg[j * 32]));
+                F in = Pk::get(row_word<T, ANY>(rx + j * qx));
+                const Decay<V> r = decay_of<LOGIT>(Pk::get(row_word<T, ANY>(rg + j * qg)));
                 if (CHECK && (m.begin >> j & 1)) seg.B = init_of(__shfl_sync(0xffffffffu, m.seq, j));
                 if constexpr (COMP) in = mul(r.u, in);
                 seg.B = step(r.a, r.lo, seg.B, in);
@@ -189,8 +185,8 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
 }
 
 // The maps of all chunks but the last of every strip: each warp reduces a run of whole segments.
-constexpr int kMapSlots = 3;
-template <typename T, bool LOGIT, bool COMP, bool PACKED>
+template <bool ANY> constexpr int kMapSlots = ANY ? 2 : 3;
+template <typename T, bool LOGIT, bool COMP, bool PACKED, bool ANY>
 __global__ void __launch_bounds__(32 * kMapWarps)
 chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArgs ta) {
     constexpr int V = kChannels<T>, W = kMapWarps;
@@ -210,18 +206,19 @@ chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Ti
     const long long sx = a.x.token_stride * sizeof(T), sg = a.gate.token_stride * sizeof(T);
     const int width = min(kRowBytes, (d - c0) * (int)sizeof(T));
     float* maps = reinterpret_cast<float*>(staged);
-    const int seg_bytes = fwd_seg_bytes(ta), gate_at = seg_bytes / 2;
-    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kMapSlots * seg_bytes;
+    constexpr int kSlots = kMapSlots<ANY>, kSeg = kFwdSegBytes<ANY>, kGateAt = kSeg / 2;
+    uint8_t* own = staged + kMeetingBytes<V, W> + warp * kSlots * kSeg;
+    const int qx = staged_pitch<kRowBytes, ANY>(sx), qg = staged_pitch<kRowBytes, ANY>(sg);
     auto stage = [&](int k) {
         const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
         if (k < run && n > 0) {
-            uint8_t* to = own + k % kMapSlots * seg_bytes;
-            if (ta.aligned && n == kSub) [[likely]] {
-                stage_rows<kRowBytes>(to, px + t * sx, sx, width);
-                stage_rows<kRowBytes>(to + gate_at, pg + t * sg, sg, width);
+            uint8_t* to = own + k % kSlots * kSeg;
+            if (ANY || n == kSub) [[likely]] {
+                stage_rows<kRowBytes, ANY>(to, px + t * sx, sx, n, width);
+                stage_rows<kRowBytes, ANY>(to + kGateAt, pg + t * sg, sg, n, width);
             } else {
-                stage_any<kRowBytes>(to, px + t * sx, sx, n, width, ta.align_x);
-                stage_any<kRowBytes>(to + gate_at, pg + t * sg, sg, n, width, ta.align_gate);
+                stage_tail<kRowBytes>(to, px + t * sx, sx, n, width);
+                stage_tail<kRowBytes>(to + kGateAt, pg + t * sg, sg, n, width);
             }
         }
         copy_commit();
@@ -230,26 +227,22 @@ chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Ti
     bool begins = false;
     Held held;
 #pragma unroll 1
-    for (int k = 0; k < kMapSlots - 1; ++k) stage(k);
+    for (int k = 0; k < kSlots - 1; ++k) stage(k);
     for (int k = 0; k < run; ++k) {
         const int t0 = (first + k) * kSub, n = max(0, min(kSub, a.seqlen - t0));
         Marks m;
         m.valid = (1u << n) - 1;
         m.begin = m.end = 0;
         if constexpr (PACKED) m = marks_of(a.cu, a.nseq, t0, n, held);
-        copy_wait<kMapSlots - 2>();
+        copy_wait<kSlots - 2>();
         __syncwarp();
-        stage(k + kMapSlots - 1);
-        uint8_t* here = own + k % kMapSlots * seg_bytes;
-        if (!ta.words && n) [[unlikely]] {
-            if (ta.align_x < 4) realign_rows<kRowBytes>(here, px + t0 * sx, sx);
-            if (ta.align_gate < 4) realign_rows<kRowBytes>(here + gate_at, pg + t0 * sg, sg);
-        }
-        const uint32_t* rx = reinterpret_cast<const uint32_t*>(here) + lane;
-        const uint32_t* rg = reinterpret_cast<const uint32_t*>(here + gate_at) + lane;
+        stage(k + kSlots - 1);
+        uint8_t* here = own + k % kSlots * kSeg;
+        const uint8_t* rx = here + staged_start<ANY>(px + t0 * sx) + lane * 4;
+        const uint8_t* rg = here + kGateAt + staged_start<ANY>(pg + t0 * sg) + lane * 4;
         auto token = [&](int j) {
-            F in = Pk::get(rx[j * 32]);
-            const Decay<V> r = decay_of<LOGIT>(Pk::get(rg[j * 32]));
+            F in = Pk::get(row_word<T, ANY>(rx + j * qx));
+            const Decay<V> r = decay_of<LOGIT>(Pk::get(row_word<T, ANY>(rg + j * qg)));
             if constexpr (COMP) in = mul(r.u, in);
             all.B = step(r.a, r.lo, all.B, in);
             extend(all, r);
@@ -286,24 +279,28 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
     TileArgs t = tile_args<T>(a);
     const long long units = (long long)t.strips * a.batch;
     const Chunks ch = chunks_of(a.x_q ? Work::kToCodes : Work::kPlain, units, t.blocks, kFwdWarps, kFwdBlocks,
-                                a.x_q ? t.words : t.aligned);
+                                t.aligned);
     t.chunks = ch.count;
     t.chunk_tiles = ch.tiles;
     t.maps = static_cast<float*>(a.workspace);
-    t.slots = fwd_slots(t);
-    auto go = [&](auto logit, auto comp, auto packed) {
+    auto go = [&](auto logit, auto comp, auto packed, auto any) {
         constexpr bool L = decltype(logit)::value, C = decltype(comp)::value, K = decltype(packed)::value;
-        constexpr int V = kChannels<T>;
+        constexpr bool A = decltype(any)::value;
+        constexpr int V = kChannels<T>, kBytes = kFwdSegBytes<A>;
         if (t.chunks > 1) {
-            const int smem = kMeetingBytes<V, kMapWarps> + kMapWarps * kMapSlots * fwd_seg_bytes(t);
-            const cudaError_t e = launch_ctas<chunk_map_kernel<T, L, C, K>>(
-                units * (t.chunks - 1), kMapWarps, smem, false, st, a, t);
+            constexpr int kSmem = kMeetingBytes<V, kMapWarps> + kMapWarps * kMapSlots<A> * kBytes;
+            const cudaError_t e = launch_ctas<chunk_map_kernel<T, L, C, K, A>>(
+                units * (t.chunks - 1), kMapWarps, kSmem, false, st, a, t);
             if (e != cudaSuccess) return e;
         }
-        const int smem = kMeetingBytes<V, kFwdWarps> + kFwdWarps * t.slots * fwd_seg_bytes(t);
-        return launch_ctas<scan_kernel<T, L, C, K>>(units * t.chunks, kFwdWarps, smem, t.chunks > 1, st, a, t);
+        constexpr int kSmem = kMeetingBytes<V, kFwdWarps> + kFwdWarps * kFwdSlots<A> * kBytes;
+        return launch_ctas<scan_kernel<T, L, C, K, A>>(units * t.chunks, kFwdWarps, kSmem, t.chunks > 1,
+                                                       st, a, t);
     };
-    auto packed = [&](auto logit, auto comp) { return a.cu ? go(logit, comp, Y{}) : go(logit, comp, N{}); };
+    auto rows = [&](auto logit, auto comp, auto packed) {
+        return t.aligned ? go(logit, comp, packed, N{}) : go(logit, comp, packed, Y{});
+    };
+    auto packed = [&](auto logit, auto comp) { return a.cu ? rows(logit, comp, Y{}) : rows(logit, comp, N{}); };
     if (a.logit) return a.complement ? packed(Y{}, Y{}) : packed(Y{}, N{});
     return a.complement ? packed(N{}, Y{}) : packed(N{}, N{});
 }

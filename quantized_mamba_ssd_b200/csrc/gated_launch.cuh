@@ -25,13 +25,10 @@ struct TileArgs {
     int spans;        // spans per row
     int chunks;       // CTAs per strip
     int chunk_tiles;  // tiles of a chunk (the last one's may be fewer)
-    int slots;        // forward: segments in shared memory per warp
     float* maps;      // workspace: [strip of all rows][chunk][map of 32 lanes]
-    // what the start of every row is a multiple of (bytes): 16, 4 or less; whether that is 16 for all
-    // inputs, and whether it is at least 4
-    int align_x, align_gate, align_dy, aligned, words;
+    bool aligned;     // every input's rows start at multiples of 16 bytes
     // outputs are written as whole words (codes: pairs of bytes): aligned, and no lane has a part
-    int whole_out, whole_codes;
+    bool whole_out, whole_codes;
 };
 
 // What the start of every row is a multiple of.
@@ -51,19 +48,14 @@ TileArgs tile_args(const GatedArgs& a) {
     t.strips = (a.channels + 32 * V - 1) / (32 * V);
     t.spans = (a.seqlen + kSpan - 1) / kSpan;
     t.blocks = (a.seqlen + kBlock - 1) / kBlock;
-    t.align_x = alignment(a.x, elem);
-    t.align_gate = alignment(a.gate, elem);
-    t.align_dy = alignment(a.dy, elem);  // (16 for an input that the call does not have)
+    // (16 for an input that the call does not have)
+    int least = std::min({alignment(a.x, elem), alignment(a.gate, elem), alignment(a.dy, elem)});
     t.whole_out = a.channels % V == 0 && word_rows(a.y, elem) && word_rows(a.dx, elem) &&
                   word_rows(a.dgate, elem);
     auto all = [](auto... p) { return (reinterpret_cast<uintptr_t>(p) | ...); };
-    if (a.x_q && !a.x.ptr) {  // backward from codes, rows of one byte per channel
-        t.align_x = alignment({a.x_q, 0, a.channels}, 1);
-        t.align_gate = alignment({a.gate_q, 0, a.channels}, 1);
-    }
-    const int least = std::min({t.align_x, t.align_gate, t.align_dy});
+    if (a.x_q && !a.x.ptr)  // backward from codes, rows of one byte per channel
+        least = std::min({least, alignment({a.x_q, 0, a.channels}, 1), alignment({a.gate_q, 0, a.channels}, 1)});
     t.aligned = least == 16;
-    t.words = least >= 4;
     t.whole_codes = (all(a.x_q, a.gate_q, a.x_e, a.gate_e) | a.channels) % 2 == 0;
     return t;
 }
@@ -88,19 +80,19 @@ struct Chunks {
 // CTAs per place (and about 0.4 of the last wave's gaps), and its steps are 1.4 times as long with
 // the SMs full as with them empty; with S > 1 the maps before it take 0.85 of that again, and the
 // second launch and its start about 4 steps (2 of the longer ones of rows that are not aligned).
-// Beside the longer steps of a scan from or to codes both are less.  (`easy`: rows that are copied
-// in 16-byte pieces; of a scan to codes, in words.)  Only the counts that fill one to four waves are
-// looked at.
+// Beside the longer steps of a scan from or to codes both are less.  Only the counts that fill one
+// to four waves are looked at.
 // Measured, whole and in S chunks: forward 16 strips of 512 fp16 tiles 726 us, 133 (S = 18); 40 of
-// 64 tiles 85, 41 (7); 80 of 157 bf16 tiles 200, 186 (3), 182 (8); 128 of 32 tiles 44, 53 (2); 75 of
-// 10 fp32 tiles 19.4, 20.4 (8).  Forward with codes, 48 bf16 strips of 4 tiles 11.6, 8.7 (4); 128 of
-// 32 tiles 77, 82 (2).  Backward from codes 13.2, 9.3 and 103, 98; 75 of 10 fp32 tiles 44, 38 (3).
+// 64 tiles 85, 41 (7); 80 of 157 bf16 tiles 200, 186 (3), 182 (8); 128 of 32 tiles 44, 53 (2), rows of
+// 4090 channels 65, 80 (2); 75 of 10 fp32 tiles 19.0, 19.4 (4).  Forward with codes, 48 bf16 strips
+// of 4 tiles 11.6, 8.7 (4); 128 of 32 tiles 77, 82 (2).  Backward from codes 13.2, 9.3 and 102, 97;
+// 75 of 10 fp32 tiles 37, 32 (4).
 enum class Work { kPlain, kToCodes, kFromCodes };
-inline Chunks chunks_of(Work work, long long strips, int segments, int warps, int per_sm, bool easy) {
+inline Chunks chunks_of(Work work, long long strips, int segments, int warps, int per_sm, bool aligned) {
     const long long room = (long long)sm_count() * per_sm;
     const int tiles = (segments + warps - 1) / warps;
     const double maps = work == Work::kPlain ? 1.85 : work == Work::kToCodes ? 1.6 : 1.4;
-    const double second = work == Work::kPlain ? (easy ? 4 : 2) : (easy ? 1 : 0);
+    const double second = work == Work::kPlain ? (aligned ? 4 : 2) : (aligned ? 1 : 0);
     auto time = [&](int s, int each) {
         const double full = (double)(strips * s) / room;
         const double scan = (full <= 1 ? 1 : full + 0.4) * (each + 1) * (1 + 0.4 * (full < 1 ? full : 1));

@@ -98,134 +98,91 @@ __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int AHEAD> __device__ __forceinline__ void copy_wait() {  // all but the last AHEAD commits
     asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
 }
 
-// Room for kSub rows of W bytes: rows that do not start at multiples of 4 bytes take 16 more each.
-template <int W> __host__ __device__ constexpr int sub_bytes(bool words) {
-    return kSub * (words ? W : W + 16);
+// Rows whose starts are all multiples of 16 bytes (ANY false) are staged at a pitch of W bytes, from
+// the start of their place.  Other rows (ANY) are copied as the aligned 16-byte pieces of memory
+// that hold their bytes, so each stands at its address modulo 16.  With a pitch that is that of
+// memory modulo 16 (and leaves the pieces of two rows apart), they still stand at even distances,
+// and a lane's value of row j is at one offset plus j pitches (of 16-bit rows in two halves).
+// Nothing but pieces that hold bytes of the rows is read.  Kernels of their own keep the others'
+// loop small.  (2 x 4096 bf16 tokens of 4096, 4090 and 4095 channels: forward 40, 60 and 77 us,
+// backward 73, 102 and 119; copied in 4-byte words 72 and 134, moved in shared memory to the start
+// of their place 110 and 169.)
+template <int W, bool ANY> constexpr int kSubBytes = kSub * (ANY ? W + 32 : W);  // room for kSub rows
+
+template <int W, bool ANY> __device__ __forceinline__ int staged_pitch(long long pitch) {
+    return ANY ? W + 16 + static_cast<int>(pitch & 15) : W;
+}
+template <bool ANY> __device__ __forceinline__ int staged_start(const char* src) {
+    return ANY ? static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) : 0;
 }
 
-// Rows at src + j * pitch (bytes); rows from `rows` on and bytes from `width` on become 0.  `align`
-// is what base and pitch are multiples of: with 16 the rows are copied in pieces of 16 bytes, with
-// 4 in words; with less, the 16-byte pieces of memory that hold a row's bytes are copied, and
-// realign_rows, once they are here, moves each row to the start of its place.  Nothing but pieces
-// that hold bytes of the rows is read.  (2 x 4096 bf16 tokens of 4096, 4090 and 4095 channels take
-// 42, 72 and 110 us; 4090 in moved pieces 84, 4095 in moved words 113.)
-//
-// What most calls do not run is out of line: it would push the hot loop out of the instruction
-// cache.
+// The rows' bytes from `width` on, and rows from `rows` on, stay undefined (kernels give no lane
+// and no token a meaning that has none).  What most calls do not run is out of line: it would push
+// the hot loop out of the instruction cache.
 template <int W>
-__device__ __forceinline__ void stage_words(uint32_t to, const char* src, long long pitch, int rows,
-                                         int width) {
-    constexpr int kPer = W / 4, kStep = 32 / kPer;  // words per row, rows per instruction
-    const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 4;
-    const int bytes = max(0, min(4, width - at));
-    const char* p = src + row * pitch + at;
-    to += row * W + at;
-    if (rows == kSub) {
-#pragma unroll
-        for (int i = 0; i < kSub; i += kStep) {
-            copy_async4(to + i * W, p, bytes);
-            p += kStep * pitch;
-        }
-    } else {
-#pragma unroll 4
-        for (int i = 0; i < kSub; i += kStep) {
-            const int n = row + i < rows ? bytes : 0;
-            copy_async4(to + i * W, n ? p : src, n);
-            p += kStep * pitch;
-        }
-    }
-}
-
-template <int W>
-__device__ __forceinline__ void stage_pieces(uint32_t to, const char* src, long long pitch, int rows,
-                                          int width) {
-    constexpr int kPer = W / 16, kStep = 32 / kPer, kPitch = W + 16;
+__device__ __noinline__ void stage_tail(void* dst, const char* src, long long pitch, int rows, int width) {
+    constexpr int kPer = W / 16, kStep = 32 / kPer;  // pieces per row, rows per instruction
     const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
-    const char* none = src - (reinterpret_cast<uintptr_t>(src) & 15);  // an address for copies of nothing
-    to += row * kPitch + at;
-    const char* first = src + row * pitch;
-#pragma unroll
-    for (int i = 0; i < kSub; i += kStep) {
-        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(first) & 15);
-        const int bytes = row + i < rows ? max(0, min(16, shift + width - at)) : 0;
-        copy_async16(to + i * kPitch, bytes ? first - shift + at : none, bytes);
-        first += kStep * pitch;
-    }
-    if (lane < kSub) {  // the last piece of each row
-        first = src + lane * pitch;
-        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(first) & 15);
-        const int bytes = lane < rows ? max(0, min(16, shift + width - W)) : 0;
-        copy_async16(to - (row * kPitch + at) + lane * kPitch + W, bytes ? first - shift + W : none, bytes);
-    }
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + row * W + at;
+    const int bytes = max(0, min(16, width - at));
+    for (int i = 0; row + i < rows; i += kStep)
+        if (bytes) copy_async16(to + i * W, src + (row + i) * pitch + at, bytes);
 }
 
-// The last rows of a tensor whose rows are aligned.
-template <int W>
-__device__ __forceinline__ void stage_tail(uint32_t to, const char* src, long long pitch, int rows,
-                                        int width) {
+// kSub rows at src + j * pitch (bytes); with ANY, the first `rows` of them.
+template <int W, bool ANY>
+__device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int rows, int width) {
     constexpr int kPer = W / 16, kStep = 32 / kPer;
     const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
-    for (int i = 0; i < kSub; i += kStep) {
-        const int bytes = row + i < rows ? max(0, min(16, width - at)) : 0;
-        copy_async16(to + (row + i) * W + at, bytes ? src + (row + i) * pitch + at : src, bytes);
-    }
-}
-
-// kSub whole rows that are aligned to 16 bytes.
-template <int W>
-__device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int width) {
-    constexpr int kPer = W / 16;      // pieces per row
-    constexpr int kStep = 32 / kPer;  // rows per instruction
-    const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
-    const int bytes = max(0, min(16, width - at));
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + row * W + at;
-    const char* p = bytes ? src + row * pitch + at : src;
-    const long long by = bytes ? kStep * pitch : 0;
-#pragma unroll
-    for (int i = 0; i < kSub / kStep; ++i) {
-        copy_async16(d + i * kStep * W, p, bytes);
-        p += by;
-    }
-}
-
-// Any others.
-template <int W>
-__device__ __noinline__ void stage_any(void* dst, const char* src, long long pitch, int rows,
-                                       int width, int align) {
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    if (align == 16) stage_tail<W>(to, src, pitch, rows, width);
-    else if (align == 4) stage_words<W>(to, src, pitch, rows, width);
-    else stage_pieces<W>(to, src, pitch, rows, width);
+    if constexpr (!ANY) {
+        const int bytes = max(0, min(16, width - at));
+        const uint32_t d = to + row * W + at;
+        const char* p = bytes ? src + row * pitch + at : src;
+        const long long by = bytes ? kStep * pitch : 0;
+#pragma unroll
+        for (int i = 0; i < kSub / kStep; ++i) {
+            copy_async16(d + i * kStep * W, p, bytes);
+            p += by;
+        }
+    } else {
+        const int q = staged_pitch<W, true>(pitch), start = staged_start<true>(src);
+        auto piece = [&](int r, const char* first, int at) {  // of row r, which starts at `first`
+            const int place = start + r * q, shift = place & 15;
+            const int bytes = r < rows ? max(0, min(16, shift + width - at)) : 0;
+            if (bytes) copy_async16(to + (place - shift) + at, first - shift + at, bytes);
+        };
+        const char* first = src + row * pitch;
+#pragma unroll
+        for (int i = 0; i < kSub; i += kStep) {
+            piece(row + i, first, at);
+            first += kStep * pitch;
+        }
+        if (lane < kSub) piece(lane, src + lane * pitch, W);  // the last piece of each row
+    }
 }
 
-// After the copies of rows that are not aligned to words: the same rows, each at the start of its
-// place.
-template <int W>
-__device__ __noinline__ void realign_rows(void* dst, const char* src, long long pitch) {
-    constexpr int kPer = W / 4, kStep = 32 / kPer, kPitch = kPer + 4;
-    const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer;
-    uint32_t* w = static_cast<uint32_t*>(dst);
-    uint32_t start = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src)) + row * static_cast<uint32_t>(pitch);
-    uint32_t v[kSub / kStep];
-#pragma unroll
-    for (int i = 0; i < kSub / kStep; ++i) {
-        const uint32_t* first = w + (row + i * kStep) * kPitch + at + (start >> 2 & 3);
-        v[i] = __funnelshift_r(first[0], first[1], 8 * (start & 3));
-        start += kStep * static_cast<uint32_t>(pitch);
+// The lane's word of a staged row.
+template <typename T, bool ANY> __device__ __forceinline__ uint32_t row_word(const uint8_t* r) {
+    if constexpr (ANY && sizeof(T) == 2) {
+        const uint32_t low = *reinterpret_cast<const uint16_t*>(r);
+        return low | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(r + 2)) << 16;
+    } else {
+        return *reinterpret_cast<const uint32_t*>(r);
     }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kSub / kStep; ++i) w[i * 32 + lane] = v[i];
-    __syncwarp();
+}
+template <typename T, bool ANY> __device__ __forceinline__ void set_row_word(uint8_t* r, uint32_t w) {
+    if constexpr (ANY && sizeof(T) == 2) {
+        *reinterpret_cast<uint16_t*>(r) = static_cast<uint16_t>(w);
+        *reinterpret_cast<uint16_t*>(r + 2) = static_cast<uint16_t>(w >> 16);
+    } else {
+        *reinterpret_cast<uint32_t*>(r) = w;
+    }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -259,14 +216,15 @@ __device__ __forceinline__ uint32_t block_codes(H2 v, H2 most, Vec<2> inv) {
 
 // `floor` and `ceil` limit the values first (a gate's; infinities limit nothing, NaN stays).  Out of
 // line: x and gate share the code, and scans without checkpoints do without it in their loop.
-template <typename T>
-__device__ __noinline__ void code_rows(const uint32_t* r, uint32_t valid, float floor, float ceil,
+template <typename T, bool ANY>
+__device__ __noinline__ void code_rows(const uint8_t* r, int pitch, uint32_t valid, float floor, float ceil,
                                        int8_t* q, uint8_t* e, int d, bool whole, int count) {
     constexpr int V = kChannels<T>;
     uint8_t* out = reinterpret_cast<uint8_t*>(q);
+    auto word = [&](int j) { return row_word<T, ANY>(r + j * (ANY ? pitch : kRowBytes)); };
     if constexpr (V == 1) {
         auto held = [&](int j) {
-            float v = __uint_as_float(r[j * 32]);
+            float v = __uint_as_float(word(j));
             if (v < floor) v = floor;
             if (v > ceil) v = ceil;
             return v;
@@ -297,13 +255,13 @@ __device__ __noinline__ void code_rows(const uint32_t* r, uint32_t valid, float 
         using H2 = decltype(both<T>(0.f, 0.f));
         const H2 lowest = both<T>(floor, floor), highest = both<T>(ceil, ceil);
         auto held = [&](int j) {
-            const uint32_t w = r[j * 32];
+            const uint32_t w = word(j);
             return __hmin2_nan(__hmax2_nan(*reinterpret_cast<const H2*>(&w), lowest), highest);
         };
         H2 top = both<T>(0.f, 0.f), most;
         uint32_t e0, e1;
         Vec<2> inv;
-        if (valid == kAll && whole) {
+        if (valid == kAll && (ANY || whole)) {
             H2 v[kSub];
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
@@ -311,10 +269,18 @@ __device__ __noinline__ void code_rows(const uint32_t* r, uint32_t valid, float 
                 top = __hmax2_nan(top, __habs2(v[j]));
             }
             block_scales<T>(top, e0, e1, most, inv);
-            if (count)
+            if (whole && count) {
 #pragma unroll
                 for (int j = 0; j < kSub; ++j, out += d)
                     *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(block_codes<T>(v[j], most, inv));
+            } else if (ANY) {
+#pragma unroll
+                for (int j = 0; j < kSub; ++j, out += d) {
+                    const uint32_t w = block_codes<T>(v[j], most, inv);
+                    if (count > 0) out[0] = static_cast<uint8_t>(w);
+                    if (count > 1) out[1] = static_cast<uint8_t>(w >> 8);
+                }
+            }
         } else {
 #pragma unroll 1
             for (int j = 0; j < kSub; ++j)
