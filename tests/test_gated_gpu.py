@@ -332,6 +332,47 @@ def test_strides(layout, dtype):
     assert torch.equal(q, q2) and torch.equal(e, e2)
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [1, 66, 71, 129])
+def test_rows_at_every_place(d, dtype, packed):
+    # every tensor with a first element and a row pitch of its own modulo 16 bytes, codes at odd
+    # addresses: the same bits as through contiguous tensors
+    l, form = 150, dict(gate_form="logit", input_form="complement")
+    rng = np.random.default_rng(d)
+    x, g = draw(rng, (l, d), "logit", dtype)
+    dy = tensor(rng.normal(size=(l, d)), dtype)
+    cu = torch.tensor([3, 3, 40, 41, 130, 149], dtype=torch.int32, device=DEV) if packed else None
+    lead = (lambda t: t) if packed else (lambda t: t[None])
+    zeros = lambda: lead(torch.zeros_like(x))
+
+    def run(x, g, dy, ck, y, dxs):
+        spans = lead(torch.zeros(-(-l // 64), d, device=DEV))
+        for t in ck:
+            t.zero_()
+        ssd_i8.ssd_i8_gated_scan(lead(x), lead(g), cu, y=y, span_states=spans, ckpt=ck, **form)
+        ssd_i8.ssd_i8_gated_scan_bwd(lead(dy), lead(x), lead(g), spans, cu, dx=dxs[0], dgate=dxs[1], **form)
+        ssd_i8.ssd_i8_gated_scan_bwd_ckpt(lead(dy), ck, spans, cu, dx=dxs[2], dgate=dxs[3], **form)
+        return [y, spans, *ck, *dxs]
+
+    want = run(x, g, dy, ssd_i8.ssd_i8_gated_ckpt_empty(lead(x)), zeros(), [zeros() for _ in range(4)])
+    for k in range(8):
+        def place(n, t=None):  # a view of zeros, or of t's values, at place k + n
+            first, pitch = (3 * k + 5 * n) % 16, d + (k + 3 * n) % 16
+            flat = torch.zeros(first + l * pitch + 16, dtype=x.dtype, device=DEV)
+            v = flat[first:first + l * pitch].view(l, pitch)[:, :d]
+            return v if t is None else v.copy_(t)
+
+        def codes(t, n):
+            first = (k + n) % 5
+            return torch.zeros(first + t.numel(), dtype=t.dtype, device=DEV)[first:].view(t.shape)
+
+        ck = ssd_i8.GatedCkpt(*(codes(t, n) for n, t in enumerate(ssd_i8.ssd_i8_gated_ckpt_empty(lead(x)))))
+        got = run(place(0, x), place(1, g), place(2, dy), ck, lead(place(3)),
+                  [lead(place(n)) for n in (4, 5, 6, 7)])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+
+
 def test_broadcast_gradient():
     # the gradient of y.sum() is one element with stride 0; channels must be contiguous, so rows
     # of ones are given once for all tokens
