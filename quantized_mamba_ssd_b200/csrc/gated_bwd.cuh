@@ -102,14 +102,14 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
             uint8_t* to = own + k % kBwdSlots * kSeg;
-            if (ANY || n == kSub) [[likely]] {
-                stage_rows<kRow, ANY>(to, px + t * sx, sx, n, in_width);
-                stage_rows<kRow, ANY>(to + kIn, pg + t * sg, sg, n, in_width);
-                stage_rows<kRowBytes, ANY>(to + 2 * kIn, pdy + t * sdy, sdy, n, width);
+            if (n == kSub) [[likely]] {
+                stage_rows<kRow, ANY>(to, px + t * sx, sx, in_width);
+                stage_rows<kRow, ANY>(to + kIn, pg + t * sg, sg, in_width);
+                stage_rows<kRowBytes, ANY>(to + 2 * kIn, pdy + t * sdy, sdy, width);
             } else {
-                stage_tail<kRow>(to, px + t * sx, sx, n, in_width);
-                stage_tail<kRow>(to + kIn, pg + t * sg, sg, n, in_width);
-                stage_tail<kRowBytes>(to + 2 * kIn, pdy + t * sdy, sdy, n, width);
+                stage_part<kRow, ANY>(to, px + t * sx, sx, n, in_width);
+                stage_part<kRow, ANY>(to + kIn, pg + t * sg, sg, n, in_width);
+                stage_part<kRowBytes, ANY>(to + 2 * kIn, pdy + t * sdy, sdy, n, width);
             }
         }
         copy_commit();
@@ -232,8 +232,8 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
 
         char* qdx = pdx + (t0 + kSub - 1) * sdx + lane * 4;
         char* qdg = pdg + (t0 + kSub - 1) * sdg + lane * 4;
-        auto gradients = [&](auto checks) {
-            constexpr bool CHECK = decltype(checks)::value;
+        auto gradients = [&](auto checks, auto wholes) {
+            constexpr bool CHECK = decltype(checks)::value, WHOLE = decltype(wholes)::value;
             // what the gradient of token j's decay multiplies: h_{j-1}, or h_{j-1} - x_j
             F past[kSub];
 #pragma unroll
@@ -268,15 +268,17 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                     if (a.dinit_state) store_floats<V>(a.dinit_state + (size_t)s * d + c, e, count);
                 }
                 if (!CHECK || (m.valid >> j & 1)) {
-                    store_row<T>(qdx, dx, !CHECK || whole, count);
-                    store_row<T>(qdg, dg, !CHECK || whole, count);
+                    store_row<T>(qdx, dx, WHOLE || (CHECK && whole), count);
+                    store_row<T>(qdg, dg, WHOLE || (CHECK && whole), count);
                 }
                 qdx -= sdx;
                 qdg -= sdg;
             }
         };
-        if (inside && whole && m.valid == kAll) [[likely]] gradients(std::false_type{});
-        else gradients(std::true_type{});
+        const bool plain = inside && m.valid == kAll;
+        if (plain && whole) [[likely]] gradients(std::false_type{}, std::true_type{});
+        else if (ANY && plain) gradients(std::false_type{}, std::false_type{});
+        else gradients(std::true_type{}, std::false_type{});
     }
     // the carry behind the first tile is the initial state's gradient, in every thread of its CTA
     if (!PACKED && a.dinit_state && chunk == 0 && warp == 0)
@@ -319,12 +321,12 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
         const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
         if (k < run && n > 0) {
             uint8_t* to = own + k % kSlots * kSeg;
-            if (ANY || n == kSub) [[likely]] {
-                stage_rows<kRow, ANY>(to, pg + t * sg, sg, n, CKPT ? min(kRow, d - c0) : width);
-                stage_rows<kRowBytes, ANY>(to + kIn, pdy + t * sdy, sdy, n, width);
+            if (n == kSub) [[likely]] {
+                stage_rows<kRow, ANY>(to, pg + t * sg, sg, CKPT ? min(kRow, d - c0) : width);
+                stage_rows<kRowBytes, ANY>(to + kIn, pdy + t * sdy, sdy, width);
             } else {
-                stage_tail<kRow>(to, pg + t * sg, sg, n, CKPT ? min(kRow, d - c0) : width);
-                stage_tail<kRowBytes>(to + kIn, pdy + t * sdy, sdy, n, width);
+                stage_part<kRow, ANY>(to, pg + t * sg, sg, n, CKPT ? min(kRow, d - c0) : width);
+                stage_part<kRowBytes, ANY>(to + kIn, pdy + t * sdy, sdy, n, width);
             }
         }
         copy_commit();

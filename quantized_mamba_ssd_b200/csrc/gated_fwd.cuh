@@ -61,12 +61,12 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         const int t = start(k), n = max(0, min(kSub, a.seqlen - t));
         if (k < steps && n > 0) {
             uint8_t* to = own + slot * kSeg;
-            if (ANY || n == kSub) [[likely]] {
-                stage_rows<kRowBytes, ANY>(to, px + t * sx, sx, n, width);
-                stage_rows<kRowBytes, ANY>(to + kGateAt, pg + t * sg, sg, n, width);
+            if (n == kSub) [[likely]] {
+                stage_rows<kRowBytes, ANY>(to, px + t * sx, sx, width);
+                stage_rows<kRowBytes, ANY>(to + kGateAt, pg + t * sg, sg, width);
             } else {
-                stage_tail<kRowBytes>(to, px + t * sx, sx, n, width);
-                stage_tail<kRowBytes>(to + kGateAt, pg + t * sg, sg, n, width);
+                stage_part<kRowBytes, ANY>(to, px + t * sx, sx, n, width);
+                stage_part<kRowBytes, ANY>(to + kGateAt, pg + t * sg, sg, n, width);
             }
         }
         copy_commit();
@@ -170,6 +170,12 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
                 store_row<T>(qy, step(P[j], Q[V == 1 ? j : 0], h, B[j]), true, count);
                 qy += sy;
             }
+        } else if (ANY && m.valid == kAll) {
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+                store_row<T>(qy, step(P[j], Q[V == 1 ? j : 0], h, B[j]), false, count);
+                qy += sy;
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
@@ -213,12 +219,12 @@ chunk_map_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Ti
         const int t = (first + k) * kSub, n = min(kSub, a.seqlen - t);
         if (k < run && n > 0) {
             uint8_t* to = own + k % kSlots * kSeg;
-            if (ANY || n == kSub) [[likely]] {
-                stage_rows<kRowBytes, ANY>(to, px + t * sx, sx, n, width);
-                stage_rows<kRowBytes, ANY>(to + kGateAt, pg + t * sg, sg, n, width);
+            if (n == kSub) [[likely]] {
+                stage_rows<kRowBytes, ANY>(to, px + t * sx, sx, width);
+                stage_rows<kRowBytes, ANY>(to + kGateAt, pg + t * sg, sg, width);
             } else {
-                stage_tail<kRowBytes>(to, px + t * sx, sx, n, width);
-                stage_tail<kRowBytes>(to + kGateAt, pg + t * sg, sg, n, width);
+                stage_part<kRowBytes, ANY>(to, px + t * sx, sx, n, width);
+                stage_part<kRowBytes, ANY>(to + kGateAt, pg + t * sg, sg, n, width);
             }
         }
         copy_commit();

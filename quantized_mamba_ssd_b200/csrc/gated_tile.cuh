@@ -109,8 +109,8 @@ template <int AHEAD> __device__ __forceinline__ void copy_wait() {  // all but t
 // memory modulo 16 (and leaves the pieces of two rows apart), they still stand at even distances,
 // and a lane's value of row j is at one offset plus j pitches (of 16-bit rows in two halves).
 // Nothing but pieces that hold bytes of the rows is read.  Kernels of their own keep the others'
-// loop small.  (2 x 4096 bf16 tokens of 4096, 4090 and 4095 channels: forward 40, 60 and 77 us,
-// backward 73, 102 and 119; copied in 4-byte words 72 and 134, moved in shared memory to the start
+// loop small.  (2 x 4096 bf16 tokens of 4096, 4090 and 4095 channels: forward 40, 56 and 70 us,
+// backward 73, 97 and 112; copied in 4-byte words 72 and 134, moved in shared memory to the start
 // of their place 110 and 169.)
 template <int W, bool ANY> constexpr int kSubBytes = kSub * (ANY ? W + 32 : W);  // room for kSub rows
 
@@ -124,20 +124,24 @@ template <bool ANY> __device__ __forceinline__ int staged_start(const char* src)
 // The rows' bytes from `width` on, and rows from `rows` on, stay undefined (kernels give no lane
 // and no token a meaning that has none).  What most calls do not run is out of line: it would push
 // the hot loop out of the instruction cache.
-template <int W>
-__device__ __noinline__ void stage_tail(void* dst, const char* src, long long pitch, int rows, int width) {
-    constexpr int kPer = W / 16, kStep = 32 / kPer;  // pieces per row, rows per instruction
-    const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + row * W + at;
-    const int bytes = max(0, min(16, width - at));
-    for (int i = 0; row + i < rows; i += kStep)
-        if (bytes) copy_async16(to + i * W, src + (row + i) * pitch + at, bytes);
+template <int W, bool ANY>
+__device__ __noinline__ void stage_part(void* dst, const char* src, long long pitch, int rows, int width) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int q = staged_pitch<W, ANY>(pitch), start = staged_start<ANY>(src);
+    constexpr int kPer = W / 16 + ANY;  // pieces of a row
+    for (int i = lane; i < rows * kPer; i += 32) {
+        const int row = i / kPer, at = i % kPer * 16;
+        const int place = start + row * q, shift = place & 15;
+        const int bytes = min(16, shift + width - at);
+        if (bytes > 0) copy_async16(to + (place - shift) + at, src + row * pitch - shift + at, bytes);
+    }
 }
 
-// kSub rows at src + j * pitch (bytes); with ANY, the first `rows` of them.
+// kSub whole rows at src + j * pitch (bytes).
 template <int W, bool ANY>
-__device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int rows, int width) {
-    constexpr int kPer = W / 16, kStep = 32 / kPer;
+__device__ __forceinline__ void stage_rows(void* dst, const char* src, long long pitch, int width) {
+    constexpr int kPer = W / 16, kStep = 32 / kPer;  // pieces per row, rows per instruction
     const int lane = threadIdx.x & 31, row = lane / kPer, at = lane % kPer * 16;
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
     if constexpr (!ANY) {
@@ -152,18 +156,21 @@ __device__ __forceinline__ void stage_rows(void* dst, const char* src, long long
         }
     } else {
         const int q = staged_pitch<W, true>(pitch), start = staged_start<true>(src);
-        auto piece = [&](int r, const char* first, int at) {  // of row r, which starts at `first`
-            const int place = start + r * q, shift = place & 15;
-            const int bytes = r < rows ? max(0, min(16, shift + width - at)) : 0;
-            if (bytes) copy_async16(to + (place - shift) + at, first - shift + at, bytes);
+        int place = start + row * q;
+        unsigned long long from = reinterpret_cast<unsigned long long>(src + row * pitch);
+        auto piece = [&](int place, unsigned long long from, int at) {
+            const int bytes = max(0, min(16, (place & 15) + width - at));
+            copy_async16(to + (place & ~15) + at,
+                         reinterpret_cast<const char*>(from & ~15ull) + (bytes ? at : 0), bytes);
         };
-        const char* first = src + row * pitch;
 #pragma unroll
-        for (int i = 0; i < kSub; i += kStep) {
-            piece(row + i, first, at);
-            first += kStep * pitch;
+        for (int i = 0; i < kSub / kStep; ++i) {
+            piece(place, from, at);
+            place += kStep * q;
+            from += kStep * pitch;
         }
-        if (lane < kSub) piece(lane, src + lane * pitch, W);  // the last piece of each row
+        if (lane < kSub)  // the last piece of each row
+            piece(start + lane * q, reinterpret_cast<unsigned long long>(src + lane * pitch), W);
     }
 }
 
