@@ -221,10 +221,10 @@ __device__ __forceinline__ uint32_t block_codes(H2 v, H2 most, Vec<2> inv) {
     return __byte_perm(__float_as_uint(f.x.x), __float_as_uint(f.x.y), 0x0040);
 }
 
-// `floor` and `ceil` limit the values first (a gate's; infinities limit nothing, NaN stays).  Out of
-// line: x and gate share the code, and scans without checkpoints do without it in their loop.
-template <typename T, bool ANY>
-__device__ __noinline__ void code_rows(const uint8_t* r, int pitch, uint32_t valid, float floor, float ceil,
+// A gate's values are first held to >= -kHeldGate (FLOOR) and <= kHeldGate (CEIL; NaN stays).  Out
+// of line: scans without checkpoints do without it in their loop.
+template <typename T, bool ANY, bool FLOOR, bool CEIL>
+__device__ __noinline__ void code_rows(const uint8_t* r, int pitch, uint32_t valid,
                                        int8_t* q, uint8_t* e, int d, bool whole, int count) {
     constexpr int V = kChannels<T>;
     uint8_t* out = reinterpret_cast<uint8_t*>(q);
@@ -232,8 +232,8 @@ __device__ __noinline__ void code_rows(const uint8_t* r, int pitch, uint32_t val
     if constexpr (V == 1) {
         auto held = [&](int j) {
             float v = __uint_as_float(word(j));
-            if (v < floor) v = floor;
-            if (v > ceil) v = ceil;
+            if (FLOOR && v < -kHeldGate) v = -kHeldGate;
+            if (CEIL && v > kHeldGate) v = kHeldGate;
             return v;
         };
         uint32_t top = 0;  // bits of the magnitudes: their order, NaN on top
@@ -260,10 +260,13 @@ __device__ __noinline__ void code_rows(const uint8_t* r, int pitch, uint32_t val
         if (count) *e = static_cast<uint8_t>(scale_exp(top));
     } else {
         using H2 = decltype(both<T>(0.f, 0.f));
-        const H2 lowest = both<T>(floor, floor), highest = both<T>(ceil, ceil);
+        const H2 lowest = both<T>(-kHeldGate, -kHeldGate), highest = both<T>(kHeldGate, kHeldGate);
         auto held = [&](int j) {
             const uint32_t w = word(j);
-            return __hmin2_nan(__hmax2_nan(*reinterpret_cast<const H2*>(&w), lowest), highest);
+            H2 v = *reinterpret_cast<const H2*>(&w);
+            if constexpr (FLOOR) v = __hmax2_nan(v, lowest);
+            if constexpr (CEIL) v = __hmin2_nan(v, highest);
+            return v;
         };
         H2 top = both<T>(0.f, 0.f), most;
         uint32_t e0, e1;
