@@ -92,7 +92,7 @@ inline Chunks chunks_of(Work work, long long strips, int segments, int warps, in
     const long long room = (long long)sm_count() * per_sm;
     const int tiles = (segments + warps - 1) / warps;
     const double maps = work == Work::kPlain ? 1.85 : work == Work::kToCodes ? 1.6 : 1.4;
-    const double second = work == Work::kPlain ? (aligned ? 4 : 2) : (aligned ? 1 : 0);
+    const double second = work == Work::kPlain ? (aligned ? 4 : 2) : work == Work::kToCodes && !aligned ? 0 : 1;
     auto time = [&](int s, int each) {
         const double full = (double)(strips * s) / room;
         const double scan = (full <= 1 ? 1 : full + 0.4) * (each + 1) * (1 + 0.4 * (full < 1 ? full : 1));

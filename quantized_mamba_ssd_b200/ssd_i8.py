@@ -632,8 +632,10 @@ def _per(n: int, shape: tuple) -> tuple:
     return (*shape[:-2], -(-shape[-2] // n), shape[-1])
 
 
-def _like(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+def _like(x: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """A contiguous tensor of x's shape."""
+    return (torch.empty_like(x, dtype=dtype) if x.is_contiguous()
+            else x.new_empty(x.shape, dtype=dtype))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -674,9 +676,9 @@ def ssd_i8_gated_ckpt_empty(x: torch.Tensor) -> GatedCkpt:
     """Uninitialised 8-bit checkpoints for a gated scan of ``x`` ([b,l,d] or [T,d])."""
     if x.dim() not in (2, 3):
         raise ValueError("x must be [b,l,d] or [T,d]")
-    e = _per(CKPT_BLOCK, x.shape)
-    return GatedCkpt(x.new_empty(x.shape, dtype=torch.int8), x.new_empty(e, dtype=torch.uint8),
-                     x.new_empty(x.shape, dtype=torch.int8), x.new_empty(e, dtype=torch.uint8))
+    q = _like(x, torch.int8)
+    e = x.new_empty(_per(CKPT_BLOCK, x.shape), dtype=torch.uint8)
+    return GatedCkpt(q, e, torch.empty_like(q), torch.empty_like(e))
 
 
 def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
@@ -831,7 +833,7 @@ def ssd_i8_ckpt_pack(x: torch.Tensor, *, q: Optional[torch.Tensor] = None,
     code, shape = _io_code(x, "x"), x.shape
     rows, se = _rows(x, "x", x.dtype, shape, dev), _per(CKPT_BLOCK, shape)
     if q is None:
-        q = x.new_empty(shape, dtype=torch.int8)
+        q = _like(x, torch.int8)
     if e is None:
         e = x.new_empty(se, dtype=torch.uint8)
     _check("ssd_i8_ckpt_pack", library().ssd_i8_ckpt_pack(
@@ -856,7 +858,7 @@ def ssd_i8_ckpt_unpack(q: torch.Tensor, e: torch.Tensor, *, dtype: str = "bf16",
     pq = _flat(q, "q", torch.int8, shape, dev)
     pe = _flat(e, "e", torch.uint8, _per(CKPT_BLOCK, shape), dev)
     if x is None:
-        x = q.new_empty(shape, dtype=dt)
+        x = _like(q, dt)
     _check("ssd_i8_ckpt_unpack", library().ssd_i8_ckpt_unpack(
         pq, pe, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], code,
         _flat(x, "x", dt, shape, dev), _raw_stream(dev)))
