@@ -119,10 +119,10 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
     };
 
     F carry = PACKED ? splat<V>(0.f) : state_of(a.dfinal_state, b);
-    if (PACKED && a.dinit_state && chunk == 0)  // sequences without a token
-        for (int s = warp; s < a.nseq; s += W)
-            if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
-                store_floats<V>(a.dinit_state + (size_t)s * d + c, state_of(a.dfinal_state, s), count);
+    if (PACKED && a.dinit_state)
+        for_empty_sequences(a.cu, a.nseq, chunk * W + warp, ta.chunks * W, [&](int s) {
+            store_floats<V>(a.dinit_state + (size_t)s * d + c, state_of(a.dfinal_state, s), count);
+        });
 #pragma unroll 1
     for (int k = 0; k < kBwdSlots - 1; ++k) stage(k);
     if (ta.chunks > 1) {

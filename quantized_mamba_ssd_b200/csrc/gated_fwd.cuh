@@ -76,10 +76,10 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
     };
 
     F carry = PACKED ? splat<V>(0.f) : init_of(b);
-    if (PACKED && a.final_state && chunk == 0)  // sequences without a token
-        for (int s = warp; s < a.nseq; s += W)
-            if (__ldg(a.cu + s + 1) <= __ldg(a.cu + s))
-                store_floats<V>(a.final_state + (size_t)s * d + c, init_of(s), count);
+    if (PACKED && a.final_state)
+        for_empty_sequences(a.cu, a.nseq, chunk * W + warp, ta.chunks * W, [&](int s) {
+            store_floats<V>(a.final_state + (size_t)s * d + c, init_of(s), count);
+        });
 #pragma unroll 1
     for (int k = 0; k < kSlots - 1; ++k) stage(k, k);
     int slot = 0, free_slot = kSlots - 1;

@@ -248,6 +248,35 @@ def test_packed_in_chunks(gate, inp, dtype, d, kind, ckpt):
         assert (t[outside] == 7.0).all()
 
 
+@pytest.mark.parametrize("d", [72, 2000])
+def test_many_short_and_empty_sequences(d):
+    # thousands of sequences of 0 to 9 tokens, in chunks of strips too
+    rng = np.random.default_rng(d)
+    lens = rng.integers(0, 10, 3001) * (rng.random(3001) < 0.6)
+    lens[-40:] = 0
+    off = np.concatenate([[0], np.cumsum(lens)])
+    n, T = len(lens), int(off[-1])
+    x, g = draw(rng, (T, d), "log", "f32")
+    init, dfin, dy = (tensor(rng.normal(size=s)) for s in ((n, d), (n, d), (T, d)))
+    cu = torch.tensor(off, dtype=torch.int32, device=DEV)
+    nan = lambda *s: torch.full(s, float("nan"), device=DEV)
+    final, dinit, spans = nan(n, d), nan(n, d), nan(-(-T // 64), d)
+    y = ssd_i8.ssd_i8_gated_scan(x, g, cu, init_state=init, final_state=final, span_states=spans)
+    dx, dg = ssd_i8.ssd_i8_gated_scan_bwd(dy, x, g, spans, cu, init_state=init, dfinal_state=dfin,
+                                          dinit_state=dinit)
+    pick = [0, 33, d - 1]
+    c = ref.Case(f64(x[:, pick]), f64(g[:, pick]), "log", "plain", off, f64(init[:, pick]), "f32").forward()
+    within(y[:, pick], c.y, c.ey, "y")
+    within(final[:, pick], c.final, c.efinal, "final_state")
+    within(spans[:, pick], *c.span_states(), "span_states")
+    c.backward(f64(dy[:, pick]), f64(dfin[:, pick]))
+    within(dx[:, pick], c.dx, c.edx, "dx")
+    within(dg[:, pick], c.dgate, c.edgate, "dgate")
+    within(dinit[:, pick], c.dinit, c.edinit, "dinit_state")
+    empty = torch.from_numpy(lens == 0).to(DEV)
+    assert torch.equal(final[empty], init[empty]) and torch.equal(dinit[empty], dfin[empty])
+
+
 def test_infinite_states_do_not_cross_into_another_sequence():
     # the first sequence's state and gradient overflow; whole chunks follow them
     T, d = 9000, 64
