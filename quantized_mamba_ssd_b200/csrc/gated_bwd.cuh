@@ -33,13 +33,13 @@ template <typename T, bool CKPT, bool ANY>
 __device__ __forceinline__ Vec<kChannels<T>> row_value(const uint8_t* r, Vec<kChannels<T>> scale) {
     constexpr int V = kChannels<T>;
     if constexpr (CKPT && V == 2) {
-        // code + 128 in the low byte of 2^23 is that number as a float; times a power of two, and
-        // less (2^23 + 128) of it, the value, all exact
+        // code + 128 in the low byte of 2^23 is that number as a float, less 2^23 + 128 the code (in
+        // one instruction with the scale, 2^23 of the largest ones would not be a number)
         const uint32_t q = (ANY ? r[0] | r[1] << 8 : *reinterpret_cast<const uint16_t*>(r)) ^ 0x8080u;
         Vec<2> f;
         f.x = make_float2(__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7440)),
                           __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7441)));
-        return fma(f, scale, mul(scale, splat<V>(-8388736.f)));
+        return mul(add(f, splat<V>(-8388736.f)), scale);
     } else if constexpr (CKPT) {
         return mul(Vec<1>{static_cast<float>(*reinterpret_cast<const int8_t*>(r))}, scale);
     } else {

@@ -446,6 +446,32 @@ def test_extreme_gates(gate, inp, dtype):
     within(dg[0], c.dgate, c.edgate, "dgate on checkpoints")
 
 
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("d", [33, 64])
+@pytest.mark.parametrize("dtype,size", [("f32", 1e36), ("bf16", 1e35), ("f16", 6e3), ("bf16", 1e-36), ("f16", 1e-6)])
+def test_largest_and_smallest_values(dtype, size, d, ckpt):
+    # x near the ends of its type, gradients that keep the products inside it
+    l, form = 70, dict(gate_form="log", input_form="complement")
+    rng = np.random.default_rng(int(d))
+    x = tensor(rng.normal(size=(1, l, d)) * size, dtype)
+    _, g = draw(rng, (1, l, d), "log", dtype)
+    dy = tensor(rng.normal(size=(1, l, d)) * min(1e3 / size, 1e30 if dtype != "f16" else 1e3), dtype)
+    spans, dinit = torch.empty(1, 2, d, device=DEV), torch.empty(1, d, device=DEV)
+    ck = ssd_i8.ssd_i8_gated_ckpt_empty(x) if ckpt else None
+    y = ssd_i8.ssd_i8_gated_scan(x, g, span_states=spans, ckpt=ck, **form)
+    c = ref.Case(f64(x[0]), f64(g[0]), "log", "complement", None, None, dtype).forward()
+    within(y[0], c.y, c.ey, "y")
+    if ckpt:
+        dx, dg = ssd_i8.ssd_i8_gated_scan_bwd_ckpt(dy, ck, spans, dinit_state=dinit, **form)
+        c = c.rebuilt()
+    else:
+        dx, dg = ssd_i8.ssd_i8_gated_scan_bwd(dy, x, g, spans, dinit_state=dinit, **form)
+    c.backward(f64(dy[0]), None)
+    within(dx[0], c.dx, c.edx, "dx")
+    within(dg[0], c.dgate, c.edgate, "dgate")
+    within(dinit, c.dinit, c.edinit, "dinit_state")
+
+
 def test_nan_stays_in_its_channel_and_sequence():
     x, g = draw(np.random.default_rng(8), (200, 40), "log", "bf16")
     x[30, 3], g[150, 7] = float("nan"), float("nan")
