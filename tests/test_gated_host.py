@@ -162,3 +162,10 @@ def test_binding_refuses_cpu_tensors(lib):
         with pytest.raises(ValueError):
             call()
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_workspace_size_of_the_binding(lib):
+    assert ssd_i8.ssd_i8_gated_scan_workspace_size(1, 20000, 4, "f32") > 0
+    assert ssd_i8.ssd_i8_gated_scan_workspace_size(64, 20000, 4096, "bf16") == 0  # strips enough
+    with pytest.raises(ValueError):
+        ssd_i8.ssd_i8_gated_scan_workspace_size(1, 20000, 4, "i8")
