@@ -594,6 +594,15 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int
     _refuse(t, name, dtype, shape, dev, ": the channels (last dim) must be contiguous")
 
 
+def _out_rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dev: int) -> tuple:
+    """An output of the shape and dtype of ``like``, allocated where the caller gave none, and its
+    pointer and strides."""
+    if t is not None:
+        return (t, *_rows(t, name, like.dtype, like.shape, dev))
+    t, shape = _like(like), like.shape
+    return t, t.data_ptr(), (shape[1] * shape[2] if len(shape) == 3 else 0), shape[-1]
+
+
 def _gated_shape(t: torch.Tensor, name: str, cu_seqlens, dev: int) -> tuple:
     """(batch, tokens, channels, sequences, pointer of cu_seqlens, their count or 0) of a call on
     [b, l, d] rows, or on packed [T, d] rows with ``cu_seqlens``."""
@@ -652,6 +661,7 @@ def _gated_workspace(workspace, like: torch.Tensor, b: int, l: int, d: int, code
         if not need:
             return None, None, 0
         workspace = like.new_empty(need, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need
     n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
     return workspace, _flat(workspace, "workspace", torch.uint8, (n,), dev), n
 
@@ -714,11 +724,10 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
     code, dt, shape = _io_code(x, "x"), x.dtype, x.shape
     form = _form(gate_form, input_form)
     rows = (*_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev))
-    if y is None:
-        y = _like(x)
+    y, *y_rows = _out_rows(y, "y", x, dev)
     ws, pws, nws = _gated_workspace(workspace, x, b, l, d, code, dev)
     _check("ssd_i8_gated_scan", library().ssd_i8_gated_scan(
-        *rows, *_rows(y, "y", dt, shape, dev), b, l, d, cu, nseq, form, code,
+        *rows, *y_rows, b, l, d, cu, nseq, form, code,
         _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
         _flat(final_state, "final_state", torch.float32, (seqs, d), dev),
         None if span_states is None else
@@ -741,14 +750,11 @@ def _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form,
     if span_states is None:
         raise TypeError("span_states must be the tensor that the forward call wrote")
     rows = (*_rows(dy, "dy", dt, shape, dev), *inputs(dt, shape, dev))
-    if dx is None:
-        dx = _like(dy)
-    if dgate is None:
-        dgate = _like(dy)
+    dx, *dx_rows = _out_rows(dx, "dx", dy, dev)
+    dgate, *dgate_rows = _out_rows(dgate, "dgate", dy, dev)
     ws, pws, nws = _gated_workspace(workspace, dy, b, l, d, code, dev)
     _check(name, getattr(library(), name)(
-        *rows, *_rows(dx, "dx", dt, shape, dev), *_rows(dgate, "dgate", dt, shape, dev),
-        b, l, d, cu, nseq, form, code,
+        *rows, *dx_rows, *dgate_rows, b, l, d, cu, nseq, form, code,
         _flat(init_state, "init_state", torch.float32, (seqs, d), dev),
         _flat(span_states, "span_states", torch.float32, _per(GATED_SPAN, shape), dev),
         _flat(dfinal_state, "dfinal_state", torch.float32, (seqs, d), dev),
@@ -815,9 +821,11 @@ def ssd_i8_gated_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, 
     px, pg = _flat(x, "x", dt, shape, dev), _flat(gate, "gate", dt, shape, dev)
     if y is None:
         y = torch.empty_like(x)
+        py = y.data_ptr()
+    else:
+        py = _flat(y, "y", dt, shape, dev)
     _check("ssd_i8_gated_step", library().ssd_i8_gated_step(
-        ps, px, pg, _flat(y, "y", dt, shape, dev), shape[0], shape[1], form, code,
-        _raw_stream(dev)))
+        ps, px, pg, py, shape[0], shape[1], form, code, _raw_stream(dev)))
     return y
 
 
