@@ -361,6 +361,10 @@ SSD_API size_t ssd_i8_gated_scan_workspace_size(int batch, int seqlen, int chann
  *              checkpoints of x and gate in the format of ssd_i8_ckpt_pack, for
  *              ssd_i8_gated_scan_bwd_ckpt.  The gate is limited to >= -16 (SSD_GATE_LOGIT: to
  *              [-16, 16]) first.  Tokens outside every sequence count as zero in their blocks.
+ *              Blocks begin at tokens 0, 16, 32, .. of a row whatever sequences they hold, so packed
+ *              sequences that meet inside a block share its scales: a large value of one makes the
+ *              codes of both coarse.  A value that is not finite there gets the code -128, which
+ *              stands for NaN, and no part in the scale: it does not reach the other sequences.
  */
 SSD_API ssd_status ssd_i8_gated_scan(const void *x, long long x_batch_stride,
                                      long long x_token_stride, const void *gate,
@@ -439,7 +443,8 @@ SSD_API ssd_status ssd_i8_ckpt_pack(const void *x, long long x_batch_stride,
                                     int io_dtype, int8_t *q, uint8_t *e, void *stream);
 
 /* The values of a checkpoint, x [batch, seqlen, channels] of io_dtype, contiguous (rounded to it;
- * exact when the packed tensor had that type). */
+ * exact when the packed tensor had that type).  The code -128, which only ssd_i8_gated_scan writes, is
+ * NaN. */
 SSD_API ssd_status ssd_i8_ckpt_unpack(const int8_t *q, const uint8_t *e, int batch, int seqlen,
                                       int channels, int io_dtype, void *x, void *stream);
 

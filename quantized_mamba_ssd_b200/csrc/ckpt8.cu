@@ -7,8 +7,8 @@
 // rows' starts and the codes' allow words of them.
 //
 // What bounds it (one B200, of the measured copy bandwidth 6.47 TB/s): HBM where the words are whole -
-// 4 x 4096 x 4096 bf16 34 us to pack, 95 %, and 36 us to unpack, 89 %; fp32 52 and 64 us, 102 and 82 %.
-// 4090 bf16 channels, in pairs, take 38 and 54 us, 4095 52 and 56 (one channel a thread packs either
+// 4 x 4096 x 4096 bf16 34 us to pack, 95 %, and 36 us to unpack, 89 %; fp32 52 and 55 us, 102 and 95 %.
+// 4090 bf16 channels, in pairs, take 38 and 47 us, 4095 52 and 59 (one channel a thread packs either
 // in 76): stores across the 128-byte lines.
 #include "gated_tile.cuh"
 
@@ -164,14 +164,35 @@ unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, int b
         float scale[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) scale[i] = scale_of(ex.v[i]);
+        // Whether a code is kCodeNaN (rare: see mark_rows) is asked of words of codes, w: a zero byte of it.
+        // w - 0x01010101 borrows at the lowest zero byte, and only there is a byte's top bit set in that and
+        // not in w.  Single codes are asked one by one as they leave (4095 bf16 channels 59 us; all of them
+        // before the first store 68, without the question 55).
+        uint32_t zeros = 0;
+        if constexpr (N > 1) {
 #pragma unroll
-        for (int j = 0; j < kBlock; ++j) {
-            if (j >= n) break;
-            Values<T, N> out;
-#pragma unroll
-            for (int i = 0; i < N; ++i) out.v[i] = static_cast<T>(scale[i] * in[j].v[i]);
-            *reinterpret_cast<decltype(out.word)*>(x + at + (size_t)j * d) = out.word;
+            for (int j = 0; j < kBlock; ++j) {
+                if (j >= n) break;
+                const uint32_t w = (N == 2 ? in[j].word | 0xffff0000u : in[j].word) ^ 0x01010101u * kCodeNaN;
+                zeros |= (w - 0x01010101u) & ~w;
+            }
         }
+        auto store = [&](auto marks) {
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j) {
+                if (j >= n) break;
+                Values<T, N> out;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    float v = scale[i] * in[j].v[i];
+                    if (decltype(marks)::value && static_cast<uint8_t>(in[j].v[i]) == kCodeNaN) v = NAN;
+                    out.v[i] = static_cast<T>(v);
+                }
+                *reinterpret_cast<decltype(out.word)*>(x + at + (size_t)j * d) = out.word;
+            }
+        };
+        if (N > 1 && !(zeros & 0x80808080u)) [[likely]] store(std::false_type{});
+        else store(std::true_type{});
     }
 }
 

@@ -172,6 +172,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ cu, int n
 // 8-bit checkpoints: int8 codes of kBlock tokens of one channel with one scale 2^(e - 127)
 // ---------------------------------------------------------------------------------------
 constexpr uint32_t kExpNaN = 255;  // the block holds a value that is not finite
+constexpr uint32_t kCodeNaN = 0x80;  // the code -128, which no value has: one that is not finite
 
 // Scale exponent for a block whose largest magnitude has the bit pattern `top`: top = m 2^E with
 // 1 <= m < 2 gets the scale 2^(E - 6), so that its codes use 64 to 127; scales stop at 2^-126.

@@ -28,8 +28,9 @@ constexpr int kSpanSegs = kSpan / kSub;
 constexpr int kBwdSlots = 2;
 template <int V, int W> constexpr int kFwdMapBytes = 2 * W * MapSlots<V>::kFloats * 4;
 
-// The lane's channels of one staged row: values, or codes times their scales.
-template <typename T, bool CKPT, bool ANY>
+// The lane's channels of one staged row: values, or codes times their scales.  MARKS: the code kCodeNaN
+// is NaN (it only stands in segments with a sequence border, and those have loops of their own).
+template <typename T, bool CKPT, bool ANY, bool MARKS>
 __device__ __forceinline__ Vec<kChannels<T>> row_value(const uint8_t* r, Vec<kChannels<T>> scale) {
     constexpr int V = kChannels<T>;
     if constexpr (CKPT && V == 2) {
@@ -39,8 +40,14 @@ __device__ __forceinline__ Vec<kChannels<T>> row_value(const uint8_t* r, Vec<kCh
         Vec<2> f;
         f.x = make_float2(__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7440)),
                           __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7441)));
-        return mul(add(f, splat<V>(-8388736.f)), scale);
+        f = mul(add(f, splat<V>(-8388736.f)), scale);
+        if constexpr (MARKS) {
+            if (!(q & 0x00ffu)) f.x.x = NAN;
+            if (!(q & 0xff00u)) f.x.y = NAN;
+        }
+        return f;
     } else if constexpr (CKPT) {
+        if (MARKS && *r == kCodeNaN) return {NAN};
         return mul(Vec<1>{static_cast<float>(*reinterpret_cast<const int8_t*>(r))}, scale);
     } else {
         return Pack<T>::get(row_word<T, ANY>(r));
@@ -172,9 +179,11 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
                 }
         }
         auto dy_of = [&](int j) { return Pk::get(row_word<T, ANY>(rdy + j * qdy)); };
-        auto x_of = [&](int j) { return row_value<T, CKPT, ANY>(rx + j * qx, scale_x); };
-        auto gate_of = [&](int j) {
-            F g = row_value<T, CKPT, ANY>(rg + j * qg, scale_g);
+        auto x_of = [&](auto checks, int j) {
+            return row_value<T, CKPT, ANY, PACKED && decltype(checks)::value>(rx + j * qx, scale_x);
+        };
+        auto gate_of = [&](auto checks, int j) {
+            F g = row_value<T, CKPT, ANY, PACKED && decltype(checks)::value>(rg + j * qg, scale_g);
             // no code stands for the logit of a decay of 1
             if (CKPT && LOGIT && !(m.valid >> j & 1)) g = splat<V>(INFINITY);
             return g;
@@ -194,8 +203,8 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
             constexpr bool CHECK = decltype(checks)::value;
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
-                F in = x_of(j), dy = dy_of(j);
-                const Decay<V> r = decay_of<LOGIT>(gate_of(j));
+                F in = x_of(checks, j), dy = dy_of(j);
+                const Decay<V> r = decay_of<LOGIT>(gate_of(checks, j));
                 if (CHECK && (m.begin >> j & 1))
                     fwd.B = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
                 if (CHECK && (m.end >> j & 1))
@@ -240,7 +249,7 @@ scan_bwd_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ Til
             for (int j = 0; j < kSub; ++j) {
                 const bool begins = CHECK && (m.begin >> j & 1);
                 if constexpr (!kStates) {
-                    F in = x_of(j);
+                    F in = x_of(checks, j);
                     if (begins) before = state_of(a.init_state, __shfl_sync(0xffffffffu, m.seq, j));
                     past[j] = COMP ? sub(before, in) : before;
                     if constexpr (COMP) in = mul(u[kUsesU ? j : 0], in);
@@ -357,13 +366,14 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
         const uint8_t* rg = here + staged_start<ANY>(pg + t0 * sg) + lane * (kRow / 32);
         const uint8_t* rdy = here + kIn + staged_start<ANY>(pdy + t0 * sdy) + lane * 4;
         auto dy_of = [&](int j) { return Pk::get(row_word<T, ANY>(rdy + j * qdy)); };
-        auto token = [&](int j, F dy) {
-            extend(all, decay_of<LOGIT>(row_value<T, CKPT, ANY>(rg + j * qg, scale)));
+        auto token = [&](auto checks, int j, F dy) {
+            constexpr bool MARKS = PACKED && decltype(checks)::value;
+            extend(all, decay_of<LOGIT>(row_value<T, CKPT, ANY, MARKS>(rg + j * qg, scale)));
             if (!PACKED || !closed) all.B = step(all.A, all.L, dy, all.B);
         };
         if (m.valid == kAll && !m.end) [[likely]] {
 #pragma unroll
-            for (int j = 0; j < kSub; ++j) token(j, dy_of(j));
+            for (int j = 0; j < kSub; ++j) token(std::false_type{}, j, dy_of(j));
         } else {
 #pragma unroll 1
             for (int j = 0; j < kSub; ++j) {
@@ -375,7 +385,7 @@ chunk_back_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ T
                     dy = add(dy, load_floats<V>(
                                      a.dfinal_state ? a.dfinal_state + (size_t)s * d + c : nullptr, count));
                 }
-                token(j, dy);
+                token(std::true_type{}, j, dy);
                 closed |= ends;
             }
         }

@@ -113,8 +113,14 @@ scan_kernel(const __grid_constant__ GatedArgs a, const __grid_constant__ TileArg
         }
         if (a.x_q && n > 0) {
             const size_t at = (row0 + t0) * d + c, be = ((size_t)b * ta.blocks + t0 / kBlock) * d + c;
-            code_rows<T, ANY, false, false>(rx, qx, m.valid, a.x_q + at, a.x_e + be, d, whole_codes, count);
-            code_rows<T, ANY, true, LOGIT>(rg, qg, m.valid, a.gate_q + at, a.gate_e + be, d, whole_codes, count);
+            const bool odd_x = code_rows<T, ANY, false, false>(rx, qx, m.valid, a.x_q + at, a.x_e + be, d,
+                                                               whole_codes, count);
+            const bool odd_gate = code_rows<T, ANY, true, LOGIT>(rg, qg, m.valid, a.gate_q + at, a.gate_e + be, d,
+                                                                 whole_codes, count);
+            if (PACKED && (odd_x || odd_gate) && mixed_block(m)) [[unlikely]] {
+                mark_rows<T, ANY, false, false>(rx, qx, m.valid, a.x_q + at, a.x_e + be, d, count);
+                mark_rows<T, ANY, true, LOGIT>(rg, qg, m.valid, a.gate_q + at, a.gate_e + be, d, count);
+            }
         }
 
         // The state behind token j is P[j] carry + B[j] (P with its low part Q in fp32): from the

@@ -1,0 +1,115 @@
+"""The gated recurrence on the GPU at its edges: sequences that share checkpoint blocks."""
+import numpy as np
+import pytest
+import torch
+
+from quantized_mamba_ssd_b200 import build as qbuild
+from quantized_mamba_ssd_b200 import ssd_i8
+from test_gated_gpu import DEV, FORMS, draw, tensor
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    qbuild.build()
+    ssd_i8.library()
+
+
+# offsets, rows behind them, channels, and (tensor, token, value) of what is not finite
+NAN, INF = float("nan"), float("inf")
+SHARED = [
+    # borders inside blocks (20, 40, 43, 100, 150) and on a block's edge (96)
+    ([0, 20, 40, 43, 96, 100, 150], 20, 70,
+     [("x", 18, INF), ("x", 41, NAN), ("x", 97, -INF), ("x", 99, NAN), ("x", 149, NAN), ("x", 10, NAN),
+      ("gate", 20, NAN), ("gate", 19, NAN), ("gate", 42, NAN), ("gate", 100, NAN), ("gate", 120, NAN)]),
+    # a gap and empty sequences before the border
+    ([5, 9, 9, 60, 60, 61, 64, 90], 7, 33,
+     [("x", 8, NAN), ("x", 60, INF), ("x", 61, NAN), ("x", 64, NAN), ("gate", 9, NAN), ("gate", 8, NAN),
+      ("gate", 60, NAN)]),
+    # strips in chunks
+    ([0, 4005, 6011, 9000], 100, 40,
+     [("x", 4004, NAN), ("x", 6011, INF), ("gate", 4005, NAN), ("gate", 6010, NAN), ("gate", 3000, NAN)]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SHARED)))
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("gate,inp", FORMS)
+def test_not_finite_values_stay_in_their_sequence_on_checkpoints(gate, inp, dtype, case):
+    # Sequences that share a block with a value that is not finite get the bits that they get when a
+    # zero stands there: the value has no part in the block's scale.
+    off, behind, d, bad = SHARED[case]
+    T, n = off[-1] + behind, len(off) - 1
+    rng = np.random.default_rng(case)
+    x, g = draw(rng, (T, d), gate, dtype)
+    init, dfin, dy = tensor(rng.normal(size=(n, d))), tensor(rng.normal(size=(n, d))), tensor(
+        rng.normal(size=(T, d)), dtype)
+    cu = torch.tensor(off, dtype=torch.int32, device=DEV)
+    form = dict(gate_form=gate, input_form=inp)
+
+    def run(x, g):
+        spans = torch.zeros(-(-T // 64), d, device=DEV)
+        final, dinit = (torch.zeros(n, d, device=DEV) for _ in range(2))
+        y, dx, dg = (torch.zeros_like(x) for _ in range(3))
+        ck = ssd_i8.ssd_i8_gated_ckpt_empty(x)
+        for t in ck:
+            t.zero_()
+        ssd_i8.ssd_i8_gated_scan(x, g, cu, init_state=init, final_state=final, y=y, span_states=spans,
+                                 ckpt=ck, **form)
+        ssd_i8.ssd_i8_gated_scan_bwd_ckpt(dy, ck, spans, cu, init_state=init, dfinal_state=dfin,
+                                          dinit_state=dinit, dx=dx, dgate=dg, **form)
+        return ck, (y, dx, dg), (final, dinit)
+
+    for part in range(2):  # every second value: two of one block are then also tried apart
+        put = [(which, t, v, (5 * i + 3) % d) for i, (which, t, v) in enumerate(bad)][part::2]
+        bx, bg, cx, cg = x.clone(), g.clone(), x.clone(), g.clone()
+        row_hit = torch.zeros(T, d, dtype=torch.bool, device=DEV)
+        seq_hit = torch.zeros(n, d, dtype=torch.bool, device=DEV)
+        for which, t, v, c in put:
+            (bx if which == "x" else bg)[t, c] = v
+            (cx if which == "x" else cg)[t, c] = 0.0
+            s = next(s for s in range(n) if off[s] <= t < off[s + 1])
+            row_hit[off[s]:off[s + 1], c] = seq_hit[s, c] = True
+        ck, rows, states = run(bx, bg)
+        clean_ck, clean_rows, clean_states = run(cx, cg)
+        for a, b in zip(rows, clean_rows):
+            assert torch.equal(a[~row_hit], b[~row_hit])
+        for a, b in zip(states, clean_states):
+            assert torch.equal(a[~seq_hit], b[~seq_hit])
+        for which, t, _, c in put:
+            s = next(s for s in range(n) if off[s] <= t < off[s + 1])
+            if which == "x":  # the state behind it, and with it the later tokens' gate gradients
+                assert not torch.isfinite(rows[2][t + 1:off[s + 1], c]).any()
+            else:             # the gradients of all tokens before it
+                assert not torch.isfinite(rows[1][off[s]:t, c]).any()
+            # a block of several sequences marks the token, one of a single sequence the block
+            at = 0 if which == "x" else 2
+            blk = t // 16
+            mixed = sum(min(off[i + 1], 16 * blk + 16) > max(off[i], 16 * blk) for i in range(n)) > 1
+            values = ssd_i8.ssd_i8_ckpt_unpack(ck[at], ck[at + 1], dtype=dtype)
+            want = ssd_i8.ssd_i8_ckpt_unpack(clean_ck[at], clean_ck[at + 1], dtype=dtype)
+            inside = slice(16 * blk, min(16 * blk + 16, T))
+            others = [u for u in range(*inside.indices(T)) if u not in [p[1] for p in put
+                                                                        if p[0] == which and p[3] == c]]
+            assert torch.isnan(values[t, c])
+            if mixed:
+                assert ck[at][t, c] == -128 and ck[at + 1][blk, c] == clean_ck[at + 1][blk, c]
+                assert torch.equal(values[others, c], want[others, c])
+            else:
+                assert ck[at + 1][blk, c] == 255 and (ck[at][inside, c] == 0).all()
+                assert torch.isnan(values[inside, c]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [1, 2, 6, 8, 33])
+def test_unpack_reads_the_code_of_no_value(d, dtype):
+    # every code at every place: -128 is NaN, the others times the scale (a power of two: exact)
+    codes = torch.arange(-128, 128, device=DEV, dtype=torch.int16).to(torch.int8)
+    q = torch.stack([codes.roll(7 * c) for c in range(d)], 1).contiguous()
+    e = torch.full((16, d), 127 - 7, dtype=torch.uint8, device=DEV)
+    got = ssd_i8.ssd_i8_ckpt_unpack(q, e, dtype=dtype).float()
+    want = q.float() / 128
+    want[q == -128] = NAN
+    assert torch.equal(torch.isnan(got), q == -128)
+    assert torch.equal(got[q != -128], want[q != -128])
