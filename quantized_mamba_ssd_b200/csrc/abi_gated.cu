@@ -200,7 +200,8 @@ ssd_status ssd_i8_gated_scan(const void* x, long long x_batch_stride, long long 
     Regions r;
     r.flat(init_state, seqs * d * 4, false);
     r.flat(final_state, seqs * d * 4, true);
-    if (batch == 0 || (cu_seqlens && nseq == 0)) return SSD_OK;
+    // (without a sequence there still are span states and checkpoint scales, those of no token)
+    if (batch == 0 || (cu_seqlens && nseq == 0 && !span_states && !ckpt)) return SSD_OK;
     if (seqlen == 0) {
         if (r.clash()) return SSD_ERR_INVALID_ARG;
         return pass_states(init_state, final_state, seqs * d, st);

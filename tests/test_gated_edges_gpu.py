@@ -113,3 +113,28 @@ def test_unpack_reads_the_code_of_no_value(d, dtype):
     want[q == -128] = NAN
     assert torch.equal(torch.isnan(got), q == -128)
     assert torch.equal(got[q != -128], want[q != -128])
+
+
+@pytest.mark.parametrize("T", [5, 16, 200, 9000])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_without_a_sequence(dtype, T):
+    # offsets of no sequence: the span states and the scales of blocks without a token are written, no
+    # row is
+    d = 33
+    x = torch.full((T, d), NAN, device=DEV, dtype=torch.float32 if dtype == "f32" else torch.bfloat16)
+    cu = torch.zeros(1, dtype=torch.int32, device=DEV)
+    spans = torch.full((-(-T // 64), d), 7.0, device=DEV)
+    y = torch.full_like(x, 7.0)
+    ck = ssd_i8.ssd_i8_gated_ckpt_empty(x)
+    for t in ck:
+        t.fill_(9)
+    ssd_i8.ssd_i8_gated_scan(x, x, cu, y=y, span_states=spans, ckpt=ck)
+    assert (y == 7).all() and not spans.any()
+    assert (ck.x_q == 9).all() and (ck.gate_q == 9).all()
+    assert (ck.x_e == 1).all() and (ck.gate_e == 1).all()
+    empty = torch.empty(0, d, device=DEV)
+    for call in (lambda **k: ssd_i8.ssd_i8_gated_scan_bwd(x, x, x, spans, cu, **k),
+                 lambda **k: ssd_i8.ssd_i8_gated_scan_bwd_ckpt(x, ck, spans, cu, **k)):
+        dx, dg = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+        call(dx=dx, dgate=dg, init_state=empty, dfinal_state=empty)
+        assert (dx == 7).all() and (dg == 7).all()
