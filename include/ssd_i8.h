@@ -330,7 +330,9 @@ SSD_API ssd_status ssd_i8_chunk_cb(const int8_t *C, const int8_t *B, int batch, 
  *   - Per-sequence states are float [batch, channels], or [nseq, channels] with cu_seqlens;
  *     optional ones are NULL (zero when read, not written).
  *   - No output may overlap an input or another output (SSD_ERR_INVALID_ARG where it does); the
- *     `state` of the step is both.
+ *     `state` of the step is both.  Parts of one buffer are told apart where their rows have the
+ *     same strides (column slices, stacked tensors, ranges of tokens); rows of different strides
+ *     that interleave count as overlapping.
  *   - The scans take ssd_i8_gated_scan_workspace_size(...) bytes of workspace, 256-byte aligned (0
  *     bytes, and NULL, where there are enough channels to fill the machine).  Its contents need no
  *     initialisation and mean nothing afterwards.  One workspace per concurrently running call.

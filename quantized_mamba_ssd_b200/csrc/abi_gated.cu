@@ -34,29 +34,55 @@ struct Region {
     }
 };
 
-// Whether two regions can share a byte.  Rows whose starts all lie on one grid (column slices of
-// one wider buffer) are told apart by their place inside the grid's cell.
+using Wide = __int128;  // addresses and strides of any size, their products and differences
+
+Wide floor_div(Wide a, Wide b) { return a / b - (a % b < 0); }  // b > 0
+
+// One dimension of a pair of regions: the stride they have in common and the last index of either.
+// False where their strides differ.  (An index that no stride follows counts once.)
+struct Dim {
+    Wide stride = 1, last_a = 0, last_b = 0;
+    bool set(unsigned long long stride_a, unsigned long long count_a, unsigned long long stride_b,
+             unsigned long long count_b) {
+        if (count_a > 1 && stride_a) last_a = count_a - 1;
+        if (count_b > 1 && stride_b) last_b = count_b - 1;
+        if (last_a) stride = stride_a;
+        else if (last_b) stride = stride_b;
+        return !last_a || !last_b || stride_a == stride_b;
+    }
+};
+
+// Whether two regions share a byte; also said of regions whose extents interleave at different strides.
+// A row of b stands delta + i outer + j inner behind a row of a, with i and j from -last_a to last_b; the
+// two share a byte where that lies between -b.width and a.width.
 bool overlap(const Region& a, const Region& b) {
     if (!a.at || !b.at || !a.batch || !b.batch || !a.tokens || !b.tokens) return false;
     if (a.at + a.extent() <= b.at || b.at + b.extent() <= a.at) return false;
-    if (a.batch != b.batch || a.tokens != b.tokens) return true;
-    unsigned long long m = 0;  // the grid: every used stride is a multiple of it
-    if (a.tokens > 1) {
-        if (a.ts != b.ts) return true;
-        m = a.ts;
+    Dim outer, inner;
+    if (!outer.set(a.bs, a.batch, b.bs, b.batch) || !inner.set(a.ts, a.tokens, b.ts, b.tokens)) return true;
+    if (outer.stride < inner.stride) {
+        const Dim d = outer;
+        outer = inner;
+        inner = d;
     }
-    if (a.batch > 1) {
-        if (a.bs != b.bs) return true;
-        if (m == 0 || (a.bs && a.bs < m)) {
-            if (m && m % a.bs) return true;
-            m = a.bs;
-        } else if (a.bs % m) {
-            return true;
-        }
+    const Wide delta = (Wide)b.at - (Wide)a.at, wa = a.width, wb = b.width;
+    // the integers k with low < k stride < high, between -last_a and last_b
+    auto from = [](Wide low, const Dim& d) {
+        const Wide k = floor_div(low, d.stride) + 1;
+        return k < -d.last_a ? -d.last_a : k;
+    };
+    auto to = [](Wide high, const Dim& d) {
+        const Wide k = -floor_div(-high, d.stride) - 1;
+        return k > d.last_b ? d.last_b : k;
+    };
+    const Wide i0 = from(-wb - inner.last_b * inner.stride - delta, outer);
+    const Wide i1 = to(wa + inner.last_a * inner.stride - delta, outer);
+    if (i1 - i0 > 7) return true;  // rows wider than their own pitch; two at most of any others
+    for (Wide i = i0; i <= i1; ++i) {
+        const Wide at = delta + i * outer.stride;
+        if (from(-wb - at, inner) <= to(wa - at, inner)) return true;
     }
-    if (m == 0) return true;
-    const unsigned long long delta = b.at >= a.at ? (b.at - a.at) % m : (m - (a.at - b.at) % m) % m;
-    return delta < a.width || delta + b.width > m;
+    return false;
 }
 
 // Collects the arguments' memory and refuses an output that shares bytes with another argument.

@@ -138,3 +138,46 @@ def test_rows_without_a_sequence(dtype, T):
         dx, dg = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
         call(dx=dx, dgate=dg, init_state=empty, dfinal_state=empty)
         assert (dx == 7).all() and (dg == 7).all()
+
+
+@pytest.mark.parametrize("layout", ["stack", "token halves", "time-major stack", "columns at a pitch of their own"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_halves_of_one_buffer(dtype, layout):
+    # x and gate, y and a copy of it, dx and dgate as the two halves of one buffer: the same bits as from
+    # tensors of their own, and a half moved onto the other one is refused
+    b, l, d = 2, 100, 64
+    x, g = draw(np.random.default_rng(17), (b, l, d), "log", dtype)
+    dy = torch.randn_like(x)
+
+    def halves(n=2):
+        t = dict(device=DEV, dtype=x.dtype)
+        if layout == "stack":
+            buf = torch.zeros(b, n, l, d, **t)
+            return [buf[:, i] for i in range(n)]
+        if layout == "token halves":
+            buf = torch.zeros(b, n * l, d, **t)
+            return [buf[:, i * l:(i + 1) * l] for i in range(n)]
+        if layout == "time-major stack":
+            buf = torch.zeros(l, n, b, d, **t)
+            return [buf[:, i].transpose(0, 1) for i in range(n)]
+        buf = torch.zeros(b, l * n * d + 24, **t)[:, :l * n * d].unflatten(1, (l, n * d))
+        return [buf[..., i * d:(i + 1) * d] for i in range(n)]
+
+    spans = torch.empty(b, 2, d, device=DEV)
+    want = ssd_i8.ssd_i8_gated_scan(x, g, span_states=spans)
+    want_bwd = ssd_i8.ssd_i8_gated_scan_bwd(dy, x, g, spans)
+    vx, vy, vg = halves(3)
+    vx.copy_(x), vg.copy_(g)
+    ssd_i8.ssd_i8_gated_scan(vx, vg, y=vy)
+    assert torch.equal(vy, want)
+    assert torch.equal(vx, x) and torch.equal(vg, g)
+    dx, dg = halves()
+    ssd_i8.ssd_i8_gated_scan_bwd(dy, vx, vg, spans, dx=dx, dgate=dg)
+    assert torch.equal(dx, want_bwd[0]) and torch.equal(dg, want_bwd[1])
+    for off in (1, d // 2):  # one element, half a row
+        st, at = dx.stride(), dg.storage_offset()
+        near = torch.as_strided(dg, dg.shape, st, at - off)
+        with pytest.raises(ssd_i8.SSDError):
+            ssd_i8.ssd_i8_gated_scan_bwd(dy, vx, vg, spans, dx=dx, dgate=near)
+    with pytest.raises(ssd_i8.SSDError):
+        ssd_i8.ssd_i8_gated_scan(vx, vg, y=vx)
