@@ -137,10 +137,12 @@ __device__ __forceinline__ Decay<2> decay_of(Vec<2> g) {
         d.u.x = make_float2(d.a.x.x < 0.5f ? far.x.x : near.x.x, d.a.x.y < 0.5f ? far.x.y : near.x.y);
     } else {
         d.a = t;
-        // 1 - exp(g) = -g (1 + g/2 + g^2/6 + ..): the three terms are 2^-16 accurate below 1/16,
-        // above it the difference is
-        const Vec<2> p = fma(g, fma(g, splat<2>(1.f / 6.f), splat<2>(0.5f)), one);
-        const Vec<2> near = mul(mul(g, splat<2>(-1.f)), p), far = sub(one, d.a);
+        // 1 - exp(g) = g (-1 - g/2 - g^2/6 - g^3/24 - ..): below 1/16 the next term is 2^-22.9, and the
+        // four are 2^-21 accurate with their roundings; above, the difference is 2^-18 (half a step of
+        // either 16-bit type is far more, but the fp32 states show it: with three terms, 2^-16 too large)
+        const Vec<2> p = fma(g, fma(g, fma(g, splat<2>(-1.f / 24.f), splat<2>(-1.f / 6.f)), splat<2>(-0.5f)),
+                             splat<2>(-1.f));
+        const Vec<2> near = mul(g, p), far = sub(one, d.a);
         d.u.x = make_float2(fabsf(g.x.x) < 0.0625f ? near.x.x : far.x.x,
                             fabsf(g.x.y) < 0.0625f ? near.x.y : far.x.y);
     }

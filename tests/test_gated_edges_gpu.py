@@ -1,11 +1,13 @@
-"""The gated recurrence on the GPU at its edges: sequences that share checkpoint blocks."""
+"""The gated recurrence on the GPU at its edges: sequences that share checkpoint blocks, rows without a
+sequence, parts of one buffer, and how exact the decays and weights of 16-bit gates are."""
 import numpy as np
 import pytest
 import torch
 
+import gated_ref as ref
 from quantized_mamba_ssd_b200 import build as qbuild
 from quantized_mamba_ssd_b200 import ssd_i8
-from test_gated_gpu import DEV, FORMS, draw, tensor
+from test_gated_gpu import DEV, FORMS, draw, f64, tensor, within
 
 pytestmark = pytest.mark.gpu
 
@@ -181,3 +183,26 @@ def test_two_halves_of_one_buffer(dtype, layout):
             ssd_i8.ssd_i8_gated_scan_bwd(dy, vx, vg, spans, dx=dx, dgate=near)
     with pytest.raises(ssd_i8.SSDError):
         ssd_i8.ssd_i8_gated_scan(vx, vg, y=vx)
+
+
+def every_gate(dtype, gate):
+    """All finite gates of a 16-bit type (log: up to 0), [n], and their values in 64 bits."""
+    g = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32).to(torch.int16).view(ref.TYPES[dtype])
+    g = g[torch.isfinite(g)]
+    if gate == "log":
+        g = g[g <= 0]
+    return g.to(DEV), g.double().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_weights_of_every_log_gate(dtype):
+    # One step from 0 with x = 1 leaves 1 - a as the fp32 state.  Below 1/16 the series: the term it
+    # leaves out, g^4 / 120 < 2^-22.9, and six roundings of at most 2^-24, of which those of the inner
+    # terms shrink with g.  Above, a's error over 1 - a: the exponential's instruction 2^-22, its
+    # argument's rounding and that of log2(e) 1.5 |g| 2^-24.  Below 2^-126 the product may be 0.
+    g, v = every_gate(dtype, "log")
+    st = torch.zeros(1, g.numel(), device=DEV)
+    ssd_i8.ssd_i8_gated_step(st, torch.ones_like(g)[None], g[None], input_form="complement")
+    a, u = np.exp(v), -np.expm1(v)
+    far = a * (2.0 ** -22 + 1.5 * np.abs(v) * 2.0 ** -24) + 2.0 ** -24 * u
+    within(st[0], u, np.where(np.abs(v) < 0.0625, 2.0 ** -21 * u, far) + 2.0 ** -126, "1 - a")
