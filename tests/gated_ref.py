@@ -13,9 +13,9 @@ cover the step itself (2), the input product (1) and, in a scan that joins parts
 decays and the joins (a few per part of at least 16 tokens).  The gradient that runs backward obeys
 the same recursion.  A result rounded to its type adds half a step of it.
 
-    decay      16-bit: __expf and the fast division, relative error below 2^-21
+    decay      16-bit: the approximate exponential and reciprocal, relative error below 2^-21
                fp32: two floats; expf / expm1f of 2 ulp leave 2^-22 min(a, 1 - a), doubled
-    weight     16-bit: 2^-16 (three terms of the series below 1/16; above, 2^-24 / u < 2^-20),
+    weight     16-bit: 2^-16 (the series below 1/16 and the difference above it are below 2^-18),
                logit 2^-20;  fp32: 2^-21
 
 A relative bound ends at fp32's smallest normal number: below it numbers are 2^-149 apart (exp(-100)

@@ -206,3 +206,46 @@ def test_weights_of_every_log_gate(dtype):
     a, u = np.exp(v), -np.expm1(v)
     far = a * (2.0 ** -22 + 1.5 * np.abs(v) * 2.0 ** -24) + 2.0 ** -24 * u
     within(st[0], u, np.where(np.abs(v) < 0.0625, 2.0 ** -21 * u, far) + 2.0 ** -126, "1 - a")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("gate", ["log", "logit"])
+def test_decays_of_every_gate(gate, dtype):
+    # One step from 1 with x = 0 leaves the decay as the fp32 state.  From 1/2 on it is as exact as the
+    # header says: an error of 1.9 x 2^-24, relative to 1 (the decay of a long memory).  Below, the instructions' errors: 2^-22 of the exponential with 1.5
+    # |gate| 2^-24 of its argument, for logits also 2^-23 of the reciprocal and 2^-24 of its sum.  Below
+    # 2^-126 it may be 0.
+    g, v = every_gate(dtype, gate)
+    st = torch.ones(1, g.numel(), device=DEV)
+    ssd_i8.ssd_i8_gated_step(st, torch.zeros_like(g)[None], g[None], gate_form=gate)
+    a = ref.decay(v, gate)[0]
+    small = 2.0 ** -22 + 1.5 * np.abs(v) * 2.0 ** -24 + (2.0 ** -23 + 2.0 ** -24 if gate == "logit" else 0)
+    small = np.minimum(small, 1.0)
+    within(st[0], a, np.where(a >= 0.5, 1.9 * 2.0 ** -24, small * a) + 2.0 ** -126, "decay")
+
+
+@pytest.mark.parametrize("parts", ["chunks", "whole"])
+@pytest.mark.parametrize("dtype,memory", [("f16", 4400), ("bf16", 34000)])
+def test_long_memory_in_16_bits(dtype, memory, parts):
+    # Steady gates with the memories, in tokens, at which the decay's error reaches half a step of y.  Per
+    # token and 2^-24 of the state: 1.9 of the decay, 0.5 of the step and 0.5 of the decays' product, and
+    # for the joins of 16 tokens' maps less than 0.3.  Positive x: the state bounds every partial sum.
+    l = 2 * memory
+    d = 24 if parts == "chunks" else 64 * 200  # strips for every SM are not cut
+    some = [0, 1, d // 2, d - 1]
+    rng = np.random.default_rng(memory)
+    gen = torch.Generator(device=DEV).manual_seed(memory)
+    x = torch.rand(1, l, d, device=DEV, generator=gen).add_(0.5).div_(memory).to(ref.TYPES[dtype])
+    g = torch.from_numpy(-rng.uniform(0.9, 1.1, d) / memory).to(ref.TYPES[dtype]).to(DEV).expand(1, l, d)
+    assert (ssd_i8.ssd_i8_gated_scan_workspace_size(1, l, d, dtype) > 0) == (parts == "chunks")
+    final = torch.empty(1, d, device=DEV)
+    y = ssd_i8.ssd_i8_gated_scan(x, g, final_state=final)
+    a = np.exp(f64(g[0, 0, some]))
+    h = e = np.zeros(len(some))
+    want, err = np.empty((2, l, len(some)))
+    for t, row in enumerate(f64(x[0][:, some])):
+        h = a * h + row
+        e = a * e + 3.2 * 2.0 ** -24 * h
+        want[t], err[t] = h, e
+    within(y[0][:, some], want, err + ref.rounded(want, dtype), "y")
+    within(final[0, some], h, e, "final_state")

@@ -108,7 +108,7 @@ def test_dense_on_checkpoints(dtype, gate, inp, size):
 
 
 def test_long_sequences_over_many_parts():
-    # more tokens than a cluster of CTAs takes in one pass, several passes, a ragged end
+    # strips cut into chunks of tokens, several steps in each, a ragged end
     for l, d, dtype in ((5000, 33, "f32"), (9001, 64, "bf16")):
         x, g = draw(np.random.default_rng(l), (1, l, d), "log", dtype)
         check_dense(x, g, "log", "complement", dtype)
