@@ -353,7 +353,8 @@ typedef enum ssd_gate_form { SSD_GATE_LOG = 0, SSD_GATE_LOGIT = 1 } ssd_gate_for
 #define SSD_CKPT_BLOCK 16
 
 /* Bytes of workspace that the scans need for this problem, forward or backward; 0 on invalid sizes.
- * (At most 64 maps of 512 bytes per 32 channels of a row.) */
+ * (At most 64 maps of 512 bytes per 32 channels of a row.)  The answer is the current device's, which
+ * has to be the one that the scan then runs on. */
 SSD_API size_t ssd_i8_gated_scan_workspace_size(int batch, int seqlen, int channels, int io_dtype);
 
 /*

@@ -410,7 +410,7 @@ cudaError_t dispatch_bwd(const GatedArgs& a, cudaStream_t st) {
         constexpr int W = kBwdWarps<Q>, V = kChannels<T>;
         const long long units = (long long)t.strips * a.batch;
         const Chunks ch = chunks_of(Q ? Work::kFromCodes : Work::kPlain, units, t.blocks, W, kBwdBlocks<Q>,
-                                    t.aligned);
+                                    sm_count(), t.aligned);
         t.chunks = ch.count;
         t.chunk_tiles = ch.tiles;
         t.maps = static_cast<float*>(a.workspace);

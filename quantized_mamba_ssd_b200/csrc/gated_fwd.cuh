@@ -290,7 +290,7 @@ cudaError_t dispatch_fwd(const GatedArgs& a, cudaStream_t st) {
     TileArgs t = tile_args<T>(a);
     const long long units = (long long)t.strips * a.batch;
     const Chunks ch = chunks_of(a.x_q ? Work::kToCodes : Work::kPlain, units, t.blocks, kFwdWarps, kFwdBlocks,
-                                t.aligned);
+                                sm_count(), t.aligned);
     t.chunks = ch.count;
     t.chunk_tiles = ch.tiles;
     t.maps = static_cast<float*>(a.workspace);

@@ -5,6 +5,7 @@
 #include <atomic>
 
 #include "gated_tile.cuh"
+#include "per_device.h"
 
 namespace ssd {
 namespace gated {
@@ -60,15 +61,15 @@ TileArgs tile_args(const GatedArgs& a) {
     return t;
 }
 
+// SMs of the current device (148 where none can be asked: the size of a workspace without a GPU).
 inline int sm_count() {
-    static const int sms = [] {
-        int dev = 0, n = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-            n = 148;
-        return n;
-    }();
-    return sms;
+    static PerDevice sms;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+    return sms.get(dev, 148, [](int d) {
+        int n = 0;
+        return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) == cudaSuccess ? n : 0;
+    });
 }
 
 struct Chunks {
@@ -88,8 +89,9 @@ struct Chunks {
 // of 4 tiles 11.6, 8.7 (4); 128 of 32 tiles 77, 82 (2).  Backward from codes 13.2, 9.3 and 102, 97;
 // 75 of 10 fp32 tiles 37, 32 (4).
 enum class Work { kPlain, kToCodes, kFromCodes };
-inline Chunks chunks_of(Work work, long long strips, int segments, int warps, int per_sm, bool aligned) {
-    const long long room = (long long)sm_count() * per_sm;
+inline Chunks chunks_of(Work work, long long strips, int segments, int warps, int per_sm, int sms,
+                        bool aligned) {
+    const long long room = (long long)sms * per_sm;
     const int tiles = (segments + warps - 1) / warps;
     const double maps = work == Work::kPlain ? 1.85 : work == Work::kToCodes ? 1.6 : 1.4;
     const double second = work == Work::kPlain ? (aligned ? 4 : 2) : work == Work::kToCodes && !aligned ? 0 : 1;

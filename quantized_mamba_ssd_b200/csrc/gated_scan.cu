@@ -87,12 +87,13 @@ size_t gated_workspace_bytes(int batch, int seqlen, int channels, int io_dtype) 
     const int lanes = io_dtype == SSD_IO_F32 ? 32 : 64;  // channels of a strip
     const long long units = (long long)((channels + lanes - 1) / lanes) * batch;
     const int segments = (seqlen + kSub - 1) / kSub;
+    const int sms = sm_count();
     int n = 1;
     for (bool aligned : {false, true})  // the alignment of the rows is not known here
-        n = std::max({n, chunks_of(Work::kPlain, units, segments, kFwdWarps, kFwdBlocks, aligned).count,
-                      chunks_of(Work::kToCodes, units, segments, kFwdWarps, kFwdBlocks, aligned).count,
-                      chunks_of(Work::kPlain, units, segments, kBwdWarps<false>, kBwdBlocks<false>, aligned).count,
-                      chunks_of(Work::kFromCodes, units, segments, kBwdWarps<true>, kBwdBlocks<true>, aligned).count});
+        n = std::max({n, chunks_of(Work::kPlain, units, segments, kFwdWarps, kFwdBlocks, sms, aligned).count,
+                      chunks_of(Work::kToCodes, units, segments, kFwdWarps, kFwdBlocks, sms, aligned).count,
+                      chunks_of(Work::kPlain, units, segments, kBwdWarps<false>, kBwdBlocks<false>, sms, aligned).count,
+                      chunks_of(Work::kFromCodes, units, segments, kBwdWarps<true>, kBwdBlocks<true>, sms, aligned).count});
     return n > 1 ? (size_t)units * n * MapSlots<1>::kFloats * sizeof(float) : 0;
 }
 

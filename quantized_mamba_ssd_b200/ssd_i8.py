@@ -667,7 +667,8 @@ def _gated_workspace(workspace, like: torch.Tensor, b: int, l: int, d: int, code
 
 
 def ssd_i8_gated_scan_workspace_size(batch: int, seqlen: int, channels: int, dtype: str) -> int:
-    """Bytes of workspace of the gated scans, forward and backward ("f32", "f16" or "bf16")."""
+    """Bytes of workspace of the gated scans, forward and backward ("f32", "f16" or "bf16"), on the
+    current device."""
     if dtype not in IO_DTYPES:
         raise ValueError(f"dtype is one of {tuple(IO_DTYPES)}, got {dtype!r}")
     return int(library().ssd_i8_gated_scan_workspace_size(batch, seqlen, channels,

@@ -1,4 +1,7 @@
 """Host-side edges of the gated recurrence (no GPU, nothing launched)."""
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -114,3 +117,45 @@ def test_overlap_of_far_rows(lib):
     assert scan(lib, **far, y=[GB + 12, 1 << 60, 4]) == REFUSED
     assert scan(lib, **far, y=[GB + 16, 1 << 60, 4]) == ACCEPTED
     assert scan(lib, **far, y=[GB, 4, 4]) == REFUSED
+
+
+DEVICES = r"""
+#include <cstdio>
+#include <thread>
+#include <vector>
+#include "per_device.h"
+int main() {
+    static ssd::PerDevice sms;
+    int asked = 0, answers[3] = {0, 132, 148};
+    auto get = [&](int dev) { return sms.get(dev, 99, [&](int d) { ++asked; return answers[d % 3]; }); };
+    // the first device cannot be asked yet: the fallback, which is not kept
+    if (get(0) != 99 || get(0) != 99 || asked != 2) return 1;
+    if (get(1) != 132 || get(2) != 148 || asked != 4) return 2;
+    answers[0] = 160;
+    if (get(0) != 160 || asked != 5) return 3;
+    // each device keeps its own
+    answers[0] = answers[1] = answers[2] = 1;
+    if (get(0) != 160 || get(1) != 132 || get(2) != 148 || asked != 5) return 4;
+    if (get(-1) != 99 || asked != 5) return 5;                            // no current device
+    if (get(64) != 1 || get(64) != 1 || get(1000) != 1 || asked != 8) return 6;  // asked every time
+    static ssd::PerDevice other;
+    std::vector<std::thread> threads;
+    int bad[8] = {};
+    for (int t = 0; t < 8; ++t)
+        threads.emplace_back([&bad, t] {
+            for (int i = 0; i < 6400; ++i) bad[t] += other.get(i % 64, 0, [](int d) { return d + 1; }) != i % 64 + 1;
+        });
+    for (auto& t : threads) t.join();
+    for (int b : bad) if (b) return 7;
+    return 0;
+}
+"""
+
+
+def test_a_device_keeps_its_own_number(tmp_path):
+    # what the scans ask of a device, compiled alone: no machine here has two kinds of GPU
+    src, exe = tmp_path / "devices.cpp", tmp_path / "devices"
+    src.write_text(DEVICES)
+    csrc = os.path.join(os.path.dirname(qbuild.__file__), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-pthread", "-I", csrc, "-o", str(exe), str(src)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
