@@ -12,6 +12,7 @@ import ctypes
 import functools
 import os
 import threading
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -526,6 +527,19 @@ def _raw_stream_of(dev: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream_of)
 
 
+_said: set = set()  # the calls that have said so
+
+
+def _not_recorded(name: str) -> None:
+    """A call on tensors that require gradients, where torch records: says once per call that nothing is
+    recorded.  (No error: the values are right, and a program may not want the gradients.)"""
+    if name not in _said and torch.is_grad_enabled():
+        _said.add(name)
+        warnings.warn(f"{name} records no gradients, although its tensors require them: wrap it and its "
+                      "backward call in a torch.autograd.Function, or call it under torch.no_grad()",
+                      stacklevel=3)
+
+
 class GatedCkpt(NamedTuple):
     """8-bit checkpoints of x and gate: int8 codes of the tensors' shape and uint8 exponents with
     ceil(l / 16) in the place of the token dim (``ssd_i8_gated_ckpt_empty`` allocates one)."""
@@ -713,7 +727,8 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
     ``ckpt`` (``ssd_i8_gated_ckpt_empty``) receives x and gate in 8 bits.  ``workspace`` is a uint8
     CUDA tensor of at least ``ssd_i8_gated_scan_workspace_size`` bytes; one is allocated through
     torch when omitted.  Returns y, of x's shape and dtype; rows outside every packed sequence are
-    left as they were."""
+    left as they were.  Nothing is recorded for autograd (a warning says so where torch would record):
+    a training program wraps this and the backward call in a ``torch.autograd.Function``."""
     dev = _gpu_of(x)
     if stream is not None or torch.cuda.current_device() != dev:
         with _on(dev, stream):
@@ -725,6 +740,8 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
     code, dt, shape = _io_code(x, "x"), x.dtype, x.shape
     form = _form(gate_form, input_form)
     rows = (*_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev))
+    if x.requires_grad or gate.requires_grad or (init_state is not None and init_state.requires_grad):
+        _not_recorded("ssd_i8_gated_scan")
     y, *y_rows = _out_rows(y, "y", x, dev)
     ws, pws, nws = _gated_workspace(workspace, x, b, l, d, code, dev)
     _check("ssd_i8_gated_scan", library().ssd_i8_gated_scan(
@@ -751,6 +768,8 @@ def _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form,
     if span_states is None:
         raise TypeError("span_states must be the tensor that the forward call wrote")
     rows = (*_rows(dy, "dy", dt, shape, dev), *inputs(dt, shape, dev))
+    if dy.requires_grad:
+        _not_recorded(name)
     dx, *dx_rows = _out_rows(dx, "dx", dy, dev)
     dgate, *dgate_rows = _out_rows(dgate, "dgate", dy, dev)
     ws, pws, nws = _gated_workspace(workspace, dy, b, l, d, code, dev)
@@ -820,6 +839,8 @@ def ssd_i8_gated_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, 
     code, dt, form = _io_code(x, "x"), x.dtype, _form(gate_form, input_form)
     ps = _flat(state, "state", torch.float32, shape, dev)
     px, pg = _flat(x, "x", dt, shape, dev), _flat(gate, "gate", dt, shape, dev)
+    if x.requires_grad or gate.requires_grad or state.requires_grad:
+        _not_recorded("ssd_i8_gated_step")
     if y is None:
         y = torch.empty_like(x)
         py = y.data_ptr()
@@ -843,6 +864,8 @@ def ssd_i8_ckpt_pack(x: torch.Tensor, *, q: Optional[torch.Tensor] = None,
         raise ValueError("x must be [b,l,d] or [T,d]")
     code, shape = _io_code(x, "x"), x.shape
     rows, se = _rows(x, "x", x.dtype, shape, dev), _per(CKPT_BLOCK, shape)
+    if x.requires_grad:
+        _not_recorded("ssd_i8_ckpt_pack")
     if q is None:
         q = _like(x, torch.int8)
     if e is None:

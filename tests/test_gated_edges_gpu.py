@@ -249,3 +249,40 @@ def test_long_memory_in_16_bits(dtype, memory, parts):
         want[t], err[t] = h, e
     within(y[0][:, some], want, err + ref.rounded(want, dtype), "y")
     within(final[0, some], h, e, "final_state")
+
+
+def test_tensors_that_require_gradients(monkeypatch):
+    # the values are those of any other call, nothing is recorded, and each call says so once
+    import warnings
+    x, g = draw(np.random.default_rng(3), (2, 70, 33), "log", "f32")
+    dy = torch.randn_like(x)
+    st = torch.randn(2, 33, device=DEV)
+    spans = torch.empty(2, 2, 33, device=DEV)
+    calls = {
+        "ssd_i8_gated_scan": lambda x, g, dy: ssd_i8.ssd_i8_gated_scan(x, g, span_states=spans),
+        "ssd_i8_gated_scan_bwd": lambda x, g, dy: ssd_i8.ssd_i8_gated_scan_bwd(dy, x, g, spans)[0],
+        "ssd_i8_gated_step": lambda x, g, dy: ssd_i8.ssd_i8_gated_step(
+            st.clone(), x[:, 0].contiguous(), g[:, 0].contiguous()),
+        "ssd_i8_ckpt_pack": lambda x, g, dy: ssd_i8.ssd_i8_ckpt_pack(x)[0],
+    }
+    monkeypatch.setattr(ssd_i8, "_said", set())
+    leaves = [t.clone().requires_grad_() for t in (x, g, dy)]
+    for name, call in calls.items():
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            want = call(x, g, dy)
+            with torch.no_grad():
+                assert torch.equal(call(*leaves), want)
+        with pytest.warns(UserWarning, match=name + " records no gradients"):
+            got = call(*leaves)
+        assert torch.equal(got, want) and not got.requires_grad
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            call(*leaves)
+    # one leaf is enough
+    monkeypatch.setattr(ssd_i8, "_said", set())
+    with pytest.warns(UserWarning):
+        ssd_i8.ssd_i8_gated_scan(x, leaves[1])
+    monkeypatch.setattr(ssd_i8, "_said", set())
+    with pytest.warns(UserWarning):
+        ssd_i8.ssd_i8_gated_scan(x, g, init_state=st.clone().requires_grad_())
