@@ -21,6 +21,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libssd_i8.so")
 
 SSD_OK = 0
+SSD_ERR_UNSUPPORTED = 2
 STATUS_NAMES = {0: "SSD_OK", 1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED",
                 3: "SSD_ERR_WORKSPACE", 4: "SSD_ERR_CUDA", 5: "SSD_ERR_TIMEOUT"}
 OUT_DTYPES = {"f32": (0, torch.float32), "f16": (1, torch.float16), "i8": (2, torch.int8)}
@@ -617,13 +618,23 @@ def _out_rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dev: int
     return t, t.data_ptr(), (shape[1] * shape[2] if len(shape) == 3 else 0), shape[-1]
 
 
-def _gated_shape(t: torch.Tensor, name: str, cu_seqlens, dev: int) -> tuple:
+_INT_MAX = 0x7fffffff
+
+
+def _check_sizes(fn: str, *sizes: int) -> None:
+    """The library takes sizes as C ints, which ctypes would cut without a word."""
+    if max(sizes) > _INT_MAX:
+        _check(fn, SSD_ERR_UNSUPPORTED)
+
+
+def _gated_shape(fn: str, t: torch.Tensor, name: str, cu_seqlens, dev: int) -> tuple:
     """(batch, tokens, channels, sequences, pointer of cu_seqlens, their count or 0) of a call on
     [b, l, d] rows, or on packed [T, d] rows with ``cu_seqlens``."""
     if cu_seqlens is None:
         if t.dim() != 3:
             raise ValueError(f"{name} must be [b,l,d], or [T,d] with cu_seqlens")
         b, l, d = t.shape
+        _check_sizes(fn, b, l, d)
         return b, l, d, b, None, 0
     if t.dim() != 2:
         raise ValueError(f"{name} must be [T,d] with cu_seqlens")
@@ -631,6 +642,7 @@ def _gated_shape(t: torch.Tensor, name: str, cu_seqlens, dev: int) -> tuple:
         raise ValueError("cu_seqlens must be an int32 CUDA tensor of nseq + 1 token offsets")
     l, d = t.shape
     nseq = cu_seqlens.numel() - 1
+    _check_sizes(fn, l, d, nseq)
     return 1, l, d, nseq, _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev), nseq
 
 
@@ -685,6 +697,8 @@ def ssd_i8_gated_scan_workspace_size(batch: int, seqlen: int, channels: int, dty
     current device."""
     if dtype not in IO_DTYPES:
         raise ValueError(f"dtype is one of {tuple(IO_DTYPES)}, got {dtype!r}")
+    if not all(0 <= n <= _INT_MAX for n in (batch, seqlen, channels)):
+        return 0  # as the library answers for sizes that it refuses
     return int(library().ssd_i8_gated_scan_workspace_size(batch, seqlen, channels,
                                                           IO_DTYPES[dtype][0]))
 
@@ -736,7 +750,7 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
                                      input_form=input_form, init_state=init_state,
                                      final_state=final_state, y=y, span_states=span_states,
                                      ckpt=ckpt, workspace=workspace)
-    b, l, d, seqs, cu, nseq = _gated_shape(x, "x", cu_seqlens, dev)
+    b, l, d, seqs, cu, nseq = _gated_shape("ssd_i8_gated_scan", x, "x", cu_seqlens, dev)
     code, dt, shape = _io_code(x, "x"), x.dtype, x.shape
     form = _form(gate_form, input_form)
     rows = (*_rows(x, "x", dt, shape, dev), *_rows(gate, "gate", dt, shape, dev))
@@ -762,7 +776,7 @@ def _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form,
         with _on(dev, stream):
             return _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form,
                               init_state, dfinal_state, dinit_state, dx, dgate, workspace, None)
-    b, l, d, seqs, cu, nseq = _gated_shape(dy, "dy", cu_seqlens, dev)
+    b, l, d, seqs, cu, nseq = _gated_shape(name, dy, "dy", cu_seqlens, dev)
     code, dt, shape = _io_code(dy, "dy"), dy.dtype, dy.shape
     form = _form(gate_form, input_form)
     if span_states is None:
@@ -836,6 +850,7 @@ def ssd_i8_gated_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, 
     shape = state.shape
     if len(shape) != 2:
         raise ValueError("state must be [b,d]")
+    _check_sizes("ssd_i8_gated_step", *shape)
     code, dt, form = _io_code(x, "x"), x.dtype, _form(gate_form, input_form)
     ps = _flat(state, "state", torch.float32, shape, dev)
     px, pg = _flat(x, "x", dt, shape, dev), _flat(gate, "gate", dt, shape, dev)
@@ -863,6 +878,7 @@ def ssd_i8_ckpt_pack(x: torch.Tensor, *, q: Optional[torch.Tensor] = None,
     if x.dim() not in (2, 3):
         raise ValueError("x must be [b,l,d] or [T,d]")
     code, shape = _io_code(x, "x"), x.shape
+    _check_sizes("ssd_i8_ckpt_pack", *shape)
     rows, se = _rows(x, "x", x.dtype, shape, dev), _per(CKPT_BLOCK, shape)
     if x.requires_grad:
         _not_recorded("ssd_i8_ckpt_pack")
@@ -889,6 +905,7 @@ def ssd_i8_ckpt_unpack(q: torch.Tensor, e: torch.Tensor, *, dtype: str = "bf16",
     if dtype not in IO_DTYPES:
         raise ValueError(f"dtype is one of {tuple(IO_DTYPES)}, got {dtype!r}")
     (code, dt), shape = IO_DTYPES[dtype], q.shape
+    _check_sizes("ssd_i8_ckpt_unpack", *shape)
     pq = _flat(q, "q", torch.int8, shape, dev)
     pe = _flat(e, "e", torch.uint8, _per(CKPT_BLOCK, shape), dev)
     if x is None:

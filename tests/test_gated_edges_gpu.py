@@ -286,3 +286,24 @@ def test_tensors_that_require_gradients(monkeypatch):
     monkeypatch.setattr(ssd_i8, "_said", set())
     with pytest.warns(UserWarning):
         ssd_i8.ssd_i8_gated_scan(x, g, init_state=st.clone().requires_grad_())
+
+
+@pytest.mark.parametrize("tokens", [2 ** 31, 2 ** 32 + 8])
+def test_sizes_past_32_bits_are_refused(tokens):
+    # the second one's low 32 bits are a small scan, which must not be what runs; no memory behind them
+    wide = lambda *s, **k: torch.zeros((1,) * len(s), device=DEV, **k).expand(*s)
+    row, packed = wide(1, tokens, 1), wide(tokens, 1)
+    cu = torch.tensor([0, 8], dtype=torch.int32, device=DEV)
+    spans = torch.zeros(1, 1, 1, device=DEV)
+    codes, exps = wide(1, tokens, 1, dtype=torch.int8), wide(1, -(-tokens // 16), 1, dtype=torch.uint8)
+    many = torch.zeros(8, 1, device=DEV)
+    for call in (lambda: ssd_i8.ssd_i8_gated_scan(row, row), lambda: ssd_i8.ssd_i8_gated_scan(packed, packed, cu),
+                 lambda: ssd_i8.ssd_i8_gated_scan(wide(tokens, 8, 1), wide(tokens, 8, 1)),
+                 lambda: ssd_i8.ssd_i8_gated_scan(many, many, wide(tokens + 1, dtype=torch.int32)),
+                 lambda: ssd_i8.ssd_i8_gated_scan_bwd(row, row, row, spans),
+                 lambda: ssd_i8.ssd_i8_gated_scan_bwd_ckpt(row, (codes, exps, codes, exps), spans),
+                 lambda: ssd_i8.ssd_i8_gated_step(packed, packed, packed),
+                 lambda: ssd_i8.ssd_i8_ckpt_pack(row), lambda: ssd_i8.ssd_i8_ckpt_unpack(codes, exps)):
+        with pytest.raises(ssd_i8.SSDError) as err:
+            call()
+        assert err.value.status == 2

@@ -119,6 +119,14 @@ def test_overlap_of_far_rows(lib):
     assert scan(lib, **far, y=[GB, 4, 4]) == REFUSED
 
 
+def test_workspace_of_sizes_past_32_bits(lib):
+    f = ssd_i8.ssd_i8_gated_scan_workspace_size
+    assert f(1, 20000, 4, "f32") > 0
+    for sizes in ((1, 2 ** 32 + 20000, 4), (2 ** 32 + 1, 20000, 4), (1, 20000, 2 ** 32 + 4),
+                  (1, 20000 - 2 ** 32, 4), (1, 2 ** 31, 4)):
+        assert f(*sizes, "f32") == 0
+
+
 DEVICES = r"""
 #include <cstdio>
 #include <thread>
