@@ -526,6 +526,8 @@ def _raw_stream_of(dev: int) -> int:
 # handle of the current stream of GPU `dev`, without the Stream object around it (1.2 us of a
 # 9 us decode step) where torch offers that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream_of)
+# the current GPU, likewise without the question whether CUDA is up: a CUDA tensor is at hand
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 _said: set = set()  # the calls that have said so
@@ -621,10 +623,9 @@ def _out_rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dev: int
 _INT_MAX = 0x7fffffff
 
 
-def _check_sizes(fn: str, *sizes: int) -> None:
-    """The library takes sizes as C ints, which ctypes would cut without a word."""
-    if max(sizes) > _INT_MAX:
-        _check(fn, SSD_ERR_UNSUPPORTED)
+def _too_large(fn: str) -> None:
+    """Refuses a size that the library, which takes C ints, would get cut by ctypes without a word."""
+    _check(fn, SSD_ERR_UNSUPPORTED)
 
 
 def _gated_shape(fn: str, t: torch.Tensor, name: str, cu_seqlens, dev: int) -> tuple:
@@ -634,7 +635,8 @@ def _gated_shape(fn: str, t: torch.Tensor, name: str, cu_seqlens, dev: int) -> t
         if t.dim() != 3:
             raise ValueError(f"{name} must be [b,l,d], or [T,d] with cu_seqlens")
         b, l, d = t.shape
-        _check_sizes(fn, b, l, d)
+        if b > _INT_MAX or l > _INT_MAX or d > _INT_MAX:
+            _too_large(fn)
         return b, l, d, b, None, 0
     if t.dim() != 2:
         raise ValueError(f"{name} must be [T,d] with cu_seqlens")
@@ -642,7 +644,8 @@ def _gated_shape(fn: str, t: torch.Tensor, name: str, cu_seqlens, dev: int) -> t
         raise ValueError("cu_seqlens must be an int32 CUDA tensor of nseq + 1 token offsets")
     l, d = t.shape
     nseq = cu_seqlens.numel() - 1
-    _check_sizes(fn, l, d, nseq)
+    if l > _INT_MAX or d > _INT_MAX or nseq > _INT_MAX:
+        _too_large(fn)
     return 1, l, d, nseq, _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev), nseq
 
 
@@ -744,7 +747,7 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
     left as they were.  Nothing is recorded for autograd (a warning says so where torch would record):
     a training program wraps this and the backward call in a ``torch.autograd.Function``."""
     dev = _gpu_of(x)
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or _current_device() != dev:
         with _on(dev, stream):
             return ssd_i8_gated_scan(x, gate, cu_seqlens, gate_form=gate_form,
                                      input_form=input_form, init_state=init_state,
@@ -772,7 +775,7 @@ def ssd_i8_gated_scan(x: torch.Tensor, gate: torch.Tensor,
 def _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form, init_state,
                dfinal_state, dinit_state, dx, dgate, workspace, stream):
     dev = _gpu_of(dy)
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or _current_device() != dev:
         with _on(dev, stream):
             return _gated_bwd(name, dy, inputs, span_states, cu_seqlens, gate_form, input_form,
                               init_state, dfinal_state, dinit_state, dx, dgate, workspace, None)
@@ -843,14 +846,16 @@ def ssd_i8_gated_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, 
     """One token of ``ssd_i8_gated_scan`` for a decode batch: state f32 [b,d] updated in place;
     x, gate [b,d], contiguous.  Returns y [b,d] of x's dtype."""
     dev = _gpu_of(state)
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or _current_device() != dev:
         with _on(dev, stream):
             return ssd_i8_gated_step(state, x, gate, gate_form=gate_form, input_form=input_form,
                                      y=y)
     shape = state.shape
     if len(shape) != 2:
         raise ValueError("state must be [b,d]")
-    _check_sizes("ssd_i8_gated_step", *shape)
+    b, d = shape
+    if b > _INT_MAX or d > _INT_MAX:
+        _too_large("ssd_i8_gated_step")
     code, dt, form = _io_code(x, "x"), x.dtype, _form(gate_form, input_form)
     ps = _flat(state, "state", torch.float32, shape, dev)
     px, pg = _flat(x, "x", dt, shape, dev), _flat(gate, "gate", dt, shape, dev)
@@ -862,7 +867,7 @@ def ssd_i8_gated_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, 
     else:
         py = _flat(y, "y", dt, shape, dev)
     _check("ssd_i8_gated_step", library().ssd_i8_gated_step(
-        ps, px, pg, py, shape[0], shape[1], form, code, _raw_stream(dev)))
+        ps, px, pg, py, b, d, form, code, _raw_stream(dev)))
     return y
 
 
@@ -872,13 +877,14 @@ def ssd_i8_ckpt_pack(x: torch.Tensor, *, q: Optional[torch.Tensor] = None,
     (int8 codes of x's shape, uint8 exponents [b,ceil(l/16),d] or [ceil(T/16),d]); a value is
     code * 2^(exponent - 127) (see ``ssd_i8_ckpt_pack`` in include/ssd_i8.h)."""
     dev = _gpu_of(x)
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or _current_device() != dev:
         with _on(dev, stream):
             return ssd_i8_ckpt_pack(x, q=q, e=e)
     if x.dim() not in (2, 3):
         raise ValueError("x must be [b,l,d] or [T,d]")
     code, shape = _io_code(x, "x"), x.shape
-    _check_sizes("ssd_i8_ckpt_pack", *shape)
+    if max(shape) > _INT_MAX:
+        _too_large("ssd_i8_ckpt_pack")
     rows, se = _rows(x, "x", x.dtype, shape, dev), _per(CKPT_BLOCK, shape)
     if x.requires_grad:
         _not_recorded("ssd_i8_ckpt_pack")
@@ -897,7 +903,7 @@ def ssd_i8_ckpt_unpack(q: torch.Tensor, e: torch.Tensor, *, dtype: str = "bf16",
                        x: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of an 8-bit checkpoint as ``dtype`` ("f32", "f16" or "bf16"), of q's shape."""
     dev = _gpu_of(q)
-    if stream is not None or torch.cuda.current_device() != dev:
+    if stream is not None or _current_device() != dev:
         with _on(dev, stream):
             return ssd_i8_ckpt_unpack(q, e, dtype=dtype, x=x)
     if q.dim() not in (2, 3):
@@ -905,7 +911,8 @@ def ssd_i8_ckpt_unpack(q: torch.Tensor, e: torch.Tensor, *, dtype: str = "bf16",
     if dtype not in IO_DTYPES:
         raise ValueError(f"dtype is one of {tuple(IO_DTYPES)}, got {dtype!r}")
     (code, dt), shape = IO_DTYPES[dtype], q.shape
-    _check_sizes("ssd_i8_ckpt_unpack", *shape)
+    if max(shape) > _INT_MAX:
+        _too_large("ssd_i8_ckpt_unpack")
     pq = _flat(q, "q", torch.int8, shape, dev)
     pe = _flat(e, "e", torch.uint8, _per(CKPT_BLOCK, shape), dev)
     if x is None:
