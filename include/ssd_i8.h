@@ -411,6 +411,12 @@ SSD_API ssd_status ssd_i8_gated_scan_bwd(const void *dy, long long dy_batch_stri
  * Backward from the 8-bit checkpoints of the forward call: the formulas above with the decoded
  * values in the place of x and gate; h_{t-1} is rebuilt inside each span of 64 tokens from that
  * span's saved fp32 state.
+ * How far that is from the exact gradients (root mean square, 2000 tokens of bf16 values): dx 0.3 to
+ * 0.9 %, dgate 1.0 to 1.4 %.  A gate at its limit (a reset, a mask) sets its block's scale to 2^-2, in
+ * which gates between -1/8 and 1/8 become 0: for SSD_GATE_LOG a decay of 1, and with
+ * SSD_INPUT_COMPLEMENT a dx of 0.  In blocks that hold a reset dx is 8 to 12 % off and dgate 16 %
+ * (SSD_GATE_LOGIT 3 and 4 %).  Where resets are frequent, begin a packed sequence instead, or keep x
+ * and gate for ssd_i8_gated_scan_bwd.
  */
 SSD_API ssd_status ssd_i8_gated_scan_bwd_ckpt(const void *dy, long long dy_batch_stride,
                                               long long dy_token_stride, const int8_t *ckpt_x,

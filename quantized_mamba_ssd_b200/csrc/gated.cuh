@@ -208,8 +208,9 @@ struct Coder {
     }
 };
 
-// What a checkpoint keeps of a gate: below -16 the decay (for logits, above 16 its complement)
-// is within 1.2e-7 of its limit, and masks of the lowest value must not set the block's scale.
+// What a checkpoint keeps of a gate: below -16 the decay (for logits, above 16 its complement) is
+// within 1.2e-7 of its limit, so a mask of the lowest value need not take all of the scale.  It takes
+// what -16 takes: its block's scale is 2^-2, in which gates above -1/8 become 0.
 constexpr float kHeldGate = 16.f;
 
 }  // namespace gated
