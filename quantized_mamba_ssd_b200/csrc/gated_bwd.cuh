@@ -7,8 +7,12 @@
 // and nothing depends on the rounding of y.
 //
 // What bounds it (one B200, of the measured copy bandwidth 6.47 TB/s): with enough strips HBM - 8 x
-// 4096 x 5120 bf16 294 us, 89 %; 2 x 16384 x 8192 logits with 1 - a weights 486 us, 86 %; 4 x 2048 x
-// 4096 bf16 63 us, 83 %, fp32 135 us, 77 % - else, and from codes (66 us, 64 %), the instructions.
+// 4096 x 5120 bf16 287 us, 90 %; 2 x 16384 x 8192 logits with 1 - a weights 484 us, 86 %; 4 x 2048 x
+// 4096 bf16 62 us, 84 %, fp32 133 to 140 us, 78 to 74 % - else the instructions.  From codes, where 65 us
+// are 65 % (with 1 - a 79, logits 82, fp32 132 to 172), neither: half of the issue slots are free and DRAM
+// gives 3.6 TB/s.  The main stall is the wait for global memory: a segment's scales and span state are
+// loaded in the step that uses them.  31 of the 48 kernels from codes also spill, 12 to 124 bytes a thread
+// (4 warps with registers enough took 89 us).
 // The hot loop has to stay small and contiguous: with the tokens' checks of sequence borders and of
 // odd rows inside it instead of in loops of their own, the second took 760 us.
 #pragma once

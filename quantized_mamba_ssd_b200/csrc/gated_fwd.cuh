@@ -7,9 +7,11 @@
 // element for the loads and conversions, and 16 dependent steps.)
 //
 // What bounds it (one B200, of the measured copy bandwidth 6.47 TB/s): with enough strips HBM - 8 x
-// 4096 x 5120 bf16 174 us, 90 %; 2 x 16384 x 8192 logits with 1 - a weights 295 us, 85 %; 4 x 2048 x
-// 4096 bf16 37 us, 84 %, fp32 76 us, 82 % - else the instructions: 18 per element (ncu), of which
-// half are the segment's own (copies, maps, meeting), at 2 per SM and cycle.
+// 4096 x 5120 bf16 170 us, 92 %; 2 x 16384 x 8192 logits with 1 - a weights 290 us, 86 %; 4 x 2048 x
+// 4096 bf16 36 us, 87 %, fp32 logits 72 us, 86 % - else the instructions: 18 per element (ncu), of which
+// half are the segment's own (copies, maps, meeting), issued at about 2 per SM and cycle (58 % of the
+// slots where a strip is cut into chunks), and for fp32 log gates, 93 us, 67 %, expf with expm1f.  With
+// codes: 4 x 2048 x 4096 bf16 58 us, fp32 110 (logits) and 131.
 #pragma once
 
 #include <type_traits>

@@ -88,6 +88,10 @@ struct Chunks {
 // 4090 channels 65, 80 (2); 75 of 10 fp32 tiles 19.0, 19.4 (4).  Forward with codes, 48 bf16 strips
 // of 4 tiles 11.6, 8.7 (4); 128 of 32 tiles 77, 82 (2).  Backward from codes 13.2, 9.3 and 102, 97;
 // 75 of 10 fp32 tiles 37, 32 (4).
+// Shapes that the constants were not set on (11 strips of 24 tiles, 50 of 79, 60 of 235, 105 of 7, 210 of
+// 47, 4 of 938, 270 of 20, 119 of 4, fp32 40 of 40 and 10 of 12; forward and backward, with codes and
+// without), against the best of 19 counts each: within 3 % for 35 of the 40, the others 5, 6, 9, 10
+// (backward of 105 strips of 7 tiles, left whole) and 12 % (backward from codes of 60 strips).
 enum class Work { kPlain, kToCodes, kFromCodes };
 inline Chunks chunks_of(Work work, long long strips, int segments, int warps, int per_sm, int sms,
                         bool aligned) {
